@@ -440,6 +440,154 @@ int tern_head_gemv(const int8_t* W, const float* s_row, const int32_t* rowsum, i
                    const int32_t* z, float* y, int64_t ldy, int32_t* acc, hipStream_t stream);
 
 /*
+ * tern_rmsnorm_quantize -- the residual's addition, the root-mean-square norm
+ * and the quantisation of its result, for the linears and the head that read
+ * a layer's normalised hidden state (Neutrino-1 8B model card,
+ * "Architecture": RMSNorm, fp32 norm tensors).  Per token
+ *     h_j = x_j + res_j                                   (fp32)
+ *     y_j = h_j * gain_j / sqrt(mean_j(h_j^2) + eps)      (in fp64, rounded
+ *                                                          once to fp32)
+ * and q, s_act and z of y exactly as tern_quantize_act makes them.
+ *   x      device, M x K finite floats, row stride ldx >= K;
+ *   res    device, M x K finite floats, row stride ldr >= K, or NULL (h = x);
+ *   gain   device, K floats;  eps > 0, finite;
+ *   h      device, M x K floats, row stride ldh >= K (written), or NULL; may
+ *          be x or res itself (same address and stride: in place), and must
+ *          not overlap them otherwise;
+ *   q      device, M x K int8, 16-byte aligned, row stride ldq >= K a multiple
+ *          of 16 when M > 1 (columns < K written);
+ *   s_act  device, M floats (written);  z  device, M int32 (written).
+ * Other rows need 4-byte alignment; rows that are 16-byte aligned (K a
+ * multiple of 4) are read faster.
+ */
+int tern_rmsnorm_quantize(const float* x, int64_t ldx, const float* res, int64_t ldr, const float* gain, float eps,
+                          int64_t M, int64_t K, float* h, int64_t ldh, int8_t* q, int64_t ldq, float* s_act,
+                          int32_t* z, hipStream_t stream);
+
+/*
+ * The int8 key/value cache (the engine's `--kv-dtype int8`: Neutrino-1
+ * 8B model card) in pages of page_tokens positions, with one fp32
+ * scale for each page and KV head, of K and of V apart: a cached value is
+ * code * scale, codes in [-127, 127].
+ *   k        device, pages x heads x page_tokens x head_dim int8, 16-byte
+ *            aligned;
+ *   v        device, pages x heads x head_dim x page_tokens int8 (a page is
+ *            stored transposed), 16-byte aligned;
+ *   k_scale, v_scale  device, pages x heads floats >= 0.
+ * page_tokens is 16, 32, 64 or 128 and head_dim 64 or 128, otherwise
+ * TERN_ERR_UNSUPPORTED.  A fresh cache needs no initial contents.
+ */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages, heads, head_dim, page_tokens;
+} tern_kv_cache;
+
+/*
+ * The sequences of one call.  Sequence s has the new rows start[s] ..
+ * start[s + 1] - 1 (of the call's k, v, q and y) and holds len[s] positions
+ * with them: its new rows are the positions len[s] - n .. len[s] - 1.
+ * Position j is token j % page_tokens of page table[s][j / page_tokens].
+ *   table  device, S x ld_table int32 (ld_table * page_tokens at most
+ *          TERN_KV_MAX_LEN);  start  device, S + 1 int32;  len  device, S int32;
+ *   rows     rows of the call's buffers;
+ *   max_new  the most new rows of a sequence (rows past it are passed over);
+ *   max_len  about the longest len (0: not known): it sets how the work is
+ *            split, and results hold for any len.
+ * The device arrays are not read on the host, and nothing in them reaches
+ * past the buffers: a page outside the cache, or past the table, holds no
+ * positions; a sequence whose rows do not lie in [0, rows) has none; a new
+ * row at a negative position (len[s] < n, such as an idle slot with one row
+ * and len 0) has no place in the cache and sees nothing.
+ */
+#define TERN_KV_MAX_LEN 1073741824
+typedef struct {
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* start;
+  const int32_t* len;
+  int64_t S, rows, max_new, max_len;
+} tern_kv_batch;
+
+/*
+ * tern_kv_append -- quantises the new keys and values into the cache.  For
+ * each page (and KV head, K and V apart) that new tokens reach
+ *     cand    = max |x| / 127 over the page's new tokens
+ *     scale'  = max(scale, cand)   (scale = 0 where the page held no position
+ *                                   of the sequence before)
+ *     codes held   c -> rint(c * (scale / scale')), where scale' > scale
+ *     new codes    clamp(rint(x / scale'), -127, 127)   (0 where scale' = 0)
+ * in fp32, each division and product rounded to nearest, rint half to even.
+ * Other positions of the page keep their codes.
+ *   k, v  device, rows x (heads * head_dim) finite floats, row strides ldk and
+ *         ldv >= heads * head_dim (when rows > 1), 4-byte aligned.
+ * A page that gets tokens belongs to one sequence, and once to that (its codes
+ * and scales are otherwise unspecified); pages only read may be shared.
+ */
+int tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* k, int64_t ldk, const float* v,
+                   int64_t ldv, hipStream_t stream);
+
+/*
+ * tern_attention -- attention of the new rows over the cache, which holds
+ * them already (tern_kv_append of the same batch first): one token per
+ * sequence, drafted tokens, or a prompt.  Query head hq reads KV head
+ * hq / (q_heads / heads).  With position p of the row,
+ *     a_j = scale * sum_d q_d k_jd   for the positions j <= p
+ *     y   = sum_j e^(a_j - max a) v_j / sum_j e^(a_j - max a)
+ * to the accuracy of fp32 (codes and both factors beside them enter the
+ * matrix cores at 22 bits or more; statistics and sums are fp32).  A row that
+ * sees no position is 0.  Rows of no sequence are left as they were.
+ *   q, y  device, rows x (q_heads * head_dim) floats, row strides ldq and
+ *         ldy >= q_heads * head_dim (when rows > 1), 4-byte aligned; q finite;
+ *         scale finite, q_heads a multiple of heads;
+ *   workspace  device, 256-byte aligned, at least
+ *         tern_attention_workspace_bytes(cache, batch, q_heads) bytes: partial
+ *         results of a long context's pieces.  It carries nothing from call
+ *         to call; calls that may overlap need one each.
+ */
+int64_t tern_attention_workspace_bytes(const tern_kv_cache* cache, const tern_kv_batch* batch, int64_t q_heads);
+int tern_attention(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* q, int64_t ldq,
+                   int64_t q_heads, float scale, float* y, int64_t ldy, void* workspace, int64_t workspace_bytes,
+                   hipStream_t stream);
+
+/*
+ * tern_sample -- a token from each row of logits (the head's y), with a given
+ * random number.  With a row's tokens ordered by logit, the largest first
+ * (equal ones: the lowest index first) and weights w = e^((x - max x) / T),
+ * the tokens kept are the first ones of that order that pass every filter,
+ * the very first always:
+ *     top_k   the first k tokens (k < 1: no limit);
+ *     top_p   those whose forerunners hold less than top_p of the weight of
+ *             the first k (1 or more, or NaN: no limit);
+ *     min_p   w >= min_p (0 or less, or NaN: no limit; above 1 as 1).
+ * The token drawn is the first in the order of the vocabulary at which the
+ * running sum of the kept weights passes u times their total.  Weights are
+ * fp64 values summed in integers of 2^-44 (of the largest weight): results
+ * do not depend on the order of any sum.
+ * Logits of -inf and NaN are never drawn; a row without others gives token
+ * -1 (prob 0, kept 0).  T <= 0 or NaN draws the first token of the order
+ * (prob 1, kept 1).  Logits of +inf share all of the weight.
+ *   logits  device, M x N floats, row stride ldl >= N (when M > 1), N at most
+ *           TERN_SAMPLE_MAX_N;
+ *   temperature, u  device, M floats (u in [0, 1));
+ *   top_k  device, M int32, or NULL;  top_p, min_p  device, M floats, or NULL;
+ *   token  device, M int32 (written);
+ *   prob   device, M floats (written: the token's share of the kept weight) or
+ *          NULL;  kept  device, M int32 (written: the number of kept tokens) or
+ *          NULL;
+ *   workspace  device, 256-byte aligned, at least
+ *          tern_sample_workspace_bytes(M, N) bytes; it carries nothing from
+ *          call to call, and calls that may overlap need one each.
+ */
+#define TERN_SAMPLE_MAX_N 524288
+int64_t tern_sample_workspace_bytes(int64_t M, int64_t N);
+int tern_sample(const float* logits, int64_t M, int64_t N, int64_t ldl, const float* temperature, const float* u,
+                const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token, float* prob,
+                int32_t* kept, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * The 1.6-bit layout.  Three states carry about 1.58 bits per weight
  * (article "Neutrino-1: quantization is a training decision, not a
  * deployment one", "Where the bytes go"), so this second layout (also the

@@ -188,6 +188,43 @@ Layout layout_for(int64_t nlin, int64_t workers, int64_t nseg, int64_t nsplit, i
   return l;
 }
 
+// The cache and the sequences of a call, as the kernels take them: sizes
+// checked here, pointers by check_kv_buffers once there is work.
+int check_kv(const tern_kv_cache* c, const tern_kv_batch* b, KvArgs* a) {
+  if (!c || !b) return TERN_ERR_INVALID_ARG;
+  if (c->pages < 0 || c->heads < 1 || b->S < 0 || b->rows < 0 || b->max_new < 0 || b->max_len < 0 || b->ld_table < 0)
+    return TERN_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return TERN_ERR_UNSUPPORTED;
+  int log_p = 0;
+  while (log_p < 8 && (1 << log_p) != c->page_tokens) ++log_p;
+  if (log_p < 4 || log_p > 7) return TERN_ERR_UNSUPPORTED;
+  if (c->pages > kI32Max || c->heads > 65536 || b->S > kI32Max || b->rows > kI32Max || b->max_new > kI32Max ||
+      b->ld_table > (TERN_KV_MAX_LEN >> log_p))
+    return TERN_ERR_RANGE;
+  *a = {c->k, c->v, c->k_scale, c->v_scale, b->table, b->start, b->len, b->ld_table, b->S,
+        std::min(b->max_new, b->rows), b->max_len, (int32_t)c->pages, (int32_t)c->heads, (int32_t)c->head_dim,
+        (int32_t)log_p, (int32_t)b->rows};
+  return TERN_OK;
+}
+
+bool kv_empty(const KvArgs& a) { return a.S == 0 || a.rows == 0 || a.max_new == 0; }
+
+int check_kv_buffers(const KvArgs& a) {
+  if (!a.start || !a.len) return TERN_ERR_INVALID_ARG;
+  if (a.pages < 1 || a.ld_table < 1) return TERN_ERR_INVALID_ARG;
+  if (!a.table || !a.k || !a.v || !a.k_scale || !a.v_scale) return TERN_ERR_INVALID_ARG;
+  if (!aligned(a.k, 16) || !aligned(a.v, 16)) return TERN_ERR_ALIGNMENT;
+  if (!aligned(a.k_scale, 4) || !aligned(a.v_scale, 4) || !aligned(a.table, 4) || !aligned(a.start, 4) ||
+      !aligned(a.len, 4))
+    return TERN_ERR_ALIGNMENT;
+  return TERN_OK;
+}
+
+int check_q_heads(const KvArgs& a, int64_t q_heads) {
+  if (q_heads < 1 || q_heads % a.H != 0) return TERN_ERR_INVALID_ARG;
+  return q_heads > 65536 ? TERN_ERR_RANGE : TERN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -315,6 +352,95 @@ int tern_quantize_act(const float* x, int64_t M, int64_t K, int64_t ldx, int8_t*
   if (!x || !q || !s_act || !z) return TERN_ERR_INVALID_ARG;
   if (!aligned(x, 4) || !aligned(s_act, 4) || !aligned(z, 4)) return TERN_ERR_ALIGNMENT;
   const hipError_t e = launch_quantize_act(x, M, K, ldx, q, ldq, s_act, z, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_rmsnorm_quantize(const float* x, int64_t ldx, const float* res, int64_t ldr, const float* gain, float eps,
+                          int64_t M, int64_t K, float* h, int64_t ldh, int8_t* q, int64_t ldq, float* s_act,
+                          int32_t* z, hipStream_t stream) {
+  if (M < 0 || K < 1 || ldx < K || ldq < K || (res && ldr < K) || (h && ldh < K)) return TERN_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || eps > 3.4e38f) return TERN_ERR_INVALID_ARG;
+  if (K > TERN_MAX_K || rmsnorm_work_items(M) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  if (M == 0) return TERN_OK;
+  if (!x || !gain || !q || !s_act || !z) return TERN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || (M > 1 && ldq % 16 != 0)) return TERN_ERR_ALIGNMENT;
+  if (!aligned(x, 4) || !aligned(res, 4) || !aligned(gain, 4) || !aligned(h, 4) || !aligned(s_act, 4) ||
+      !aligned(z, 4))
+    return TERN_ERR_ALIGNMENT;
+  hipError_t e = launch_rmsnorm_quantize(x, ldx, res, ldr, gain, eps, M, K, h, ldh, q, ldq, s_act, z, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* k, int64_t ldk, const float* v,
+                   int64_t ldv, hipStream_t stream) {
+  KvArgs a;
+  int st = check_kv(cache, batch, &a);
+  if (st != TERN_OK) return st;
+  const int64_t width = (int64_t)a.H * a.D;
+  if (a.rows > 1 && (ldk < width || ldv < width)) return TERN_ERR_INVALID_ARG;
+  if (kv_empty(a)) return TERN_OK;
+  if ((st = check_kv_buffers(a)) != TERN_OK) return st;
+  if (!k || !v) return TERN_ERR_INVALID_ARG;
+  if (!aligned(k, 4) || !aligned(v, 4)) return TERN_ERR_ALIGNMENT;
+  if (kv_append_work_items(a) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  hipError_t e = launch_kv_append(a, k, ldk, v, ldv, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int64_t tern_attention_workspace_bytes(const tern_kv_cache* cache, const tern_kv_batch* batch, int64_t q_heads) {
+  KvArgs a;
+  if (check_kv(cache, batch, &a) != TERN_OK || check_q_heads(a, q_heads) != TERN_OK) return 0;
+  if (kv_empty(a)) return 256;
+  const int cus = device_cus();
+  return cus <= 0 ? 0 : std::max<int64_t>(256, attn_plan(a, q_heads, cus).workspace);
+}
+
+int tern_attention(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* q, int64_t ldq,
+                   int64_t q_heads, float scale, float* y, int64_t ldy, void* workspace, int64_t workspace_bytes,
+                   hipStream_t stream) {
+  KvArgs a;
+  int st = check_kv(cache, batch, &a);
+  if (st != TERN_OK) return st;
+  if ((st = check_q_heads(a, q_heads)) != TERN_OK) return st;
+  if (!(scale > -3.4e38f && scale < 3.4e38f)) return TERN_ERR_INVALID_ARG;
+  const int64_t width = q_heads * a.D;
+  if (a.rows > 1 && (ldq < width || ldy < width)) return TERN_ERR_INVALID_ARG;
+  if (kv_empty(a)) return TERN_OK;
+  if ((st = check_kv_buffers(a)) != TERN_OK) return st;
+  if (!q || !y) return TERN_ERR_INVALID_ARG;
+  if (!aligned(q, 4) || !aligned(y, 4)) return TERN_ERR_ALIGNMENT;
+  // (the fewest workgroups the call can take: one compute unit's split)
+  if (attn_plan(a, q_heads, 1).work_items > kMaxDispatchItems) return TERN_ERR_RANGE;
+  const int cus = device_cus();
+  if (cus <= 0) return hip_fail(hipErrorNoDevice);
+  const AttnPlan p = attn_plan(a, q_heads, cus);
+  if (p.work_items > kMaxDispatchItems || p.join_items > kMaxDispatchItems) return TERN_ERR_RANGE;
+  if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace || !aligned(workspace, 256)))
+    return TERN_ERR_WORKSPACE;
+  hipError_t e = launch_attention(a, p, q, ldq, q_heads, scale, y, ldy, workspace, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int64_t tern_sample_workspace_bytes(int64_t M, int64_t N) {
+  if (M < 0 || N < 1 || N > TERN_SAMPLE_MAX_N || sample_work_items(M, N) > kMaxDispatchItems) return 0;
+  return std::max<int64_t>(256, sample_workspace_bytes(M, N));
+}
+
+int tern_sample(const float* logits, int64_t M, int64_t N, int64_t ldl, const float* temperature, const float* u,
+                const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token, float* prob,
+                int32_t* kept, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (M < 0 || N < 1 || (M > 1 && ldl < N)) return TERN_ERR_INVALID_ARG;
+  if (N > TERN_SAMPLE_MAX_N || sample_work_items(M, N) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  if (M == 0) return TERN_OK;
+  if (!logits || !temperature || !u || !token) return TERN_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)logits, (const void*)temperature, (const void*)u, (const void*)top_k,
+                        (const void*)top_p, (const void*)min_p, (const void*)token, (const void*)prob,
+                        (const void*)kept})
+    if (!aligned(p, 4)) return TERN_ERR_ALIGNMENT;
+  const int64_t need = sample_workspace_bytes(M, N);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return TERN_ERR_WORKSPACE;
+  const SampleArgs a = {logits, M, N, ldl, u, temperature, top_p, min_p, top_k, token, prob, kept};
+  hipError_t e = launch_sample(a, workspace, stream);
   return e == hipSuccess ? TERN_OK : hip_fail(e);
 }
 

@@ -150,6 +150,11 @@ struct LaunchShape {
 // A launch counts its work-items (workgroups x threads per workgroup) in 32
 // bits; the entry points refuse sizes whose launch would need more.
 constexpr int64_t kMaxDispatchItems = 0xFFFFFFFFll;
+// a * b of sizes, INT64_MAX where it does not fit
+inline int64_t mul_sat(int64_t a, int64_t b) {
+  int64_t r;
+  return __builtin_mul_overflow(a, b, &r) ? INT64_MAX : r;
+}
 // Work-items of the launches whose grid grows with the problem size.
 int64_t pack_work_items(int64_t N);  // tern_pack, tern_unpack, tern_validate
 int64_t pack5_work_items(int64_t N);
@@ -271,5 +276,50 @@ hipError_t launch_quantize_act(const float* x, int64_t M, int64_t K, int64_t ldx
 hipError_t launch_read_probe(const void* buf, int64_t bytes, uint32_t* sink, int grid, int unroll,
                              bool nontemporal, hipStream_t s);
 int mfma_stack_blocks_per_cu(int32_t variant);
+
+// residual addition, root-mean-square norm and quantisation (tern_norm.hip)
+int64_t rmsnorm_work_items(int64_t M);
+hipError_t launch_rmsnorm_quantize(const float* x, int64_t ldx, const float* res, int64_t ldr, const float* gain,
+                                   float eps, int64_t M, int64_t K, float* h, int64_t ldh, int8_t* q,
+                                   int64_t ldq, float* s_act, int32_t* z, hipStream_t s);
+
+// The paged int8 cache and a call's sequences, as the kernels take them
+// (tern_kv_cache and tern_kv_batch of the header, checked): pages of
+// 2^log_p tokens, K [page][head][token][D], V [page][head][D][token],
+// scales [page][head].
+struct KvArgs {
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *table, *start, *len;
+  int64_t ld_table, S, max_new, max_len;
+  int32_t pages, H, D, log_p, rows;
+};
+// tern_cache.hip
+int64_t kv_append_work_items(const KvArgs& a);
+hipError_t launch_kv_append(const KvArgs& a, const float* k, int64_t ldk, const float* v, int64_t ldv, hipStream_t s);
+// tern_attn.hip: how a call's rows and positions are split over workgroups
+struct AttnPlan {
+  int nt;             // 16-row tiles a wave holds
+  int64_t row_tiles;  // row tiles of a sequence and KV head
+  int64_t chunk, nchunk;
+  int64_t work_items, join_items, workspace;
+};
+AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus);
+hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q, int64_t ldq, int64_t Hq, float scale,
+                            float* y, int64_t ldy, void* workspace, hipStream_t s);
+
+// sampling (tern_sample.hip)
+struct SampleArgs {
+  const float* x;
+  int64_t M, N, ldx;
+  const float *u, *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  int32_t* token;
+  float* prob;
+  int32_t* kept;
+};
+int64_t sample_workspace_bytes(int64_t M, int64_t N);
+int64_t sample_work_items(int64_t M, int64_t N);
+hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s);
 
 }  // namespace tern

@@ -31,6 +31,8 @@ TERN_BLOCK_MAX_K = 16384
 TERN_HEAD_MAX_M = 8
 TERN_HEAD_MAX_K = 43803
 TERN5_MAX_K = 65520
+TERN_KV_MAX_LEN = 1073741824
+TERN_SAMPLE_MAX_N = 524288
 
 # Every function include/tern.h declares.
 EXPORTS = (
@@ -38,6 +40,8 @@ EXPORTS = (
     "tern_gemm_smallM", "tern_linear_stack_workspace_bytes", "tern_linear_stack_prepare",
     "tern_linear_stack", "tern_linear_stack_status", "tern_linear_stack_prepare_static", "tern_block_rowsum", "tern_gemv_blocked", "tern_quantize_act",
     "tern_quantize_weights", "tern_head_rowsum", "tern_head_gemv", "tern_row_bytes5", "tern_pack5", "tern_gemv5",
+    "tern_rmsnorm_quantize", "tern_kv_append", "tern_attention_workspace_bytes", "tern_attention",
+    "tern_sample_workspace_bytes", "tern_sample",
     "tern_read_probe",
     "tern_status_string", "tern_last_hip_error",
 )
@@ -74,6 +78,21 @@ class tern_stack_plan(ctypes.Structure):
     ]
 
 
+class tern_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("pages", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+        ("page_tokens", ctypes.c_int64),
+    ]
+
+
+class tern_kv_batch(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("start", ctypes.c_void_p), ("len", ctypes.c_void_p),
+        ("S", ctypes.c_int64), ("rows", ctypes.c_int64), ("max_new", ctypes.c_int64), ("max_len", ctypes.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _handle = None
 
@@ -92,7 +111,8 @@ def _lib():
 
 
 def _declare(lib):
-    i64, i32, vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+    i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
+    cache, batch = ctypes.POINTER(tern_kv_cache), ctypes.POINTER(tern_kv_batch)
     sig = {
         "tern_row_bytes": (i64, [i64]),
         "tern_pack": (i32, [vp, i64, i64, i64, vp, vp, vp, vp]),
@@ -114,6 +134,12 @@ def _declare(lib):
         "tern_quantize_weights": (i32, [vp, i64, i64, i64, i64, vp, i64, vp, vp]),
         "tern_head_rowsum": (i32, [vp, i64, i64, i64, vp, vp]),
         "tern_head_gemv": (i32, [vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp]),
+        "tern_rmsnorm_quantize": (i32, [vp, i64, vp, i64, vp, f32, i64, i64, vp, i64, vp, i64, vp, vp, vp]),
+        "tern_kv_append": (i32, [cache, batch, vp, i64, vp, i64, vp]),
+        "tern_attention_workspace_bytes": (i64, [cache, batch, i64]),
+        "tern_attention": (i32, [cache, batch, vp, i64, i64, f32, vp, i64, vp, i64, vp]),
+        "tern_sample_workspace_bytes": (i64, [i64, i64]),
+        "tern_sample": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
         "tern_row_bytes5": (i64, [i64]),
         "tern_pack5": (i32, [vp, i64, i64, i64, vp, vp, vp, vp]),
         "tern_gemv5": (i32, [vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
@@ -215,6 +241,58 @@ def tern_head_gemv(W, s_row, rowsum, N, K, ldw, M, q, ldq, s_act, z, y, ldy, acc
     _check(_lib().tern_head_gemv(_ptr(W), _ptr(s_row), _ptr(rowsum), N, K, ldw, M, _ptr(q), ldq,
                                  _ptr(s_act), _ptr(z), _ptr(y), ldy, _ptr(acc), _stream(stream)),
            "tern_head_gemv")
+
+
+def tern_rmsnorm_quantize(x, gain, eps, M, K, ldx, q, ldq, s_act, z, res=None, ldr=0, h=None, ldh=0, stream=None):
+    """h = x + res (res None: h = x; h None: not written), the RMS norm of h
+    with `gain`, and its int8 codes q, s_act, z."""
+    _check(_lib().tern_rmsnorm_quantize(_ptr(x), ldx, _ptr(res), ldr, _ptr(gain), eps, M, K, _ptr(h), ldh, _ptr(q),
+                                        ldq, _ptr(s_act), _ptr(z), _stream(stream)), "tern_rmsnorm_quantize")
+
+
+def make_kv_cache(k, v, k_scale, v_scale, pages, heads, head_dim, page_tokens) -> tern_kv_cache:
+    """The int8 cache: k pages x heads x page_tokens x head_dim, v pages x heads
+    x head_dim x page_tokens, k_scale and v_scale pages x heads (device
+    tensors; keep them alive)."""
+    return tern_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), int(pages), int(heads),
+                         int(head_dim), int(page_tokens))
+
+
+def make_kv_batch(table, ld_table, start, length, S, rows, max_new, max_len=0) -> tern_kv_batch:
+    """The sequences of a call: device int32 tensors table (S x ld_table page
+    ids), start (S + 1 row offsets) and length (S, the new rows included);
+    plain data, so one batch serves the append and the attention."""
+    return tern_kv_batch(table.data_ptr(), int(ld_table), start.data_ptr(), length.data_ptr(), int(S), int(rows),
+                         int(max_new), int(max_len))
+
+
+def tern_kv_append(cache, batch, k, ldk, v, ldv, stream=None):
+    _check(_lib().tern_kv_append(ctypes.byref(cache), ctypes.byref(batch), _ptr(k), ldk, _ptr(v), ldv,
+                                 _stream(stream)), "tern_kv_append")
+
+
+def tern_attention_workspace_bytes(cache, batch, q_heads) -> int:
+    return int(_lib().tern_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(batch), int(q_heads)))
+
+
+def tern_attention(cache, batch, q, ldq, q_heads, scale, y, ldy, workspace=None, stream=None):
+    """workspace: a device tensor of tern_attention_workspace_bytes bytes."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib().tern_attention(ctypes.byref(cache), ctypes.byref(batch), _ptr(q), ldq, q_heads, scale, _ptr(y), ldy,
+                                 _ptr(workspace), nbytes, _stream(stream)), "tern_attention")
+
+
+def tern_sample_workspace_bytes(M: int, N: int) -> int:
+    return int(_lib().tern_sample_workspace_bytes(int(M), int(N)))
+
+
+def tern_sample(logits, M, N, ldl, temperature, u, token, workspace=None, top_k=None, top_p=None, min_p=None,
+                prob=None, kept=None, stream=None):
+    """workspace: a device tensor of tern_sample_workspace_bytes bytes."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib().tern_sample(_ptr(logits), M, N, ldl, _ptr(temperature), _ptr(u), _ptr(top_k), _ptr(top_p),
+                              _ptr(min_p), _ptr(token), _ptr(prob), _ptr(kept), _ptr(workspace), nbytes,
+                              _stream(stream)), "tern_sample")
 
 
 def tern_row_bytes5(K: int) -> int:

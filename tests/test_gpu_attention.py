@@ -1,0 +1,159 @@
+"""Attention over the paged int8 cache against the oracle in fp64.
+
+The tolerance counts the roundings of the definition's fp32 evaluation, per
+row and head, with A the largest sum of |scale q_d k_jd| over d, V the largest
+|v|, n the positions seen:
+  - a score is off by at most A * (2^-21 + 24 * 2^-24): q enters as two fp16
+    numbers (22 bits of the row's largest element), eight matrix instructions
+    add to an fp32 accumulator twice each, and a few products follow;
+  - a weight e^x is then off by that, plus 2^-22 for the exponential and 2^-21
+    for its two fp16 numbers;
+  - sums of weights and of weighted values: one rounding per 16 positions and
+    lane and per joining step, at most (n / 64 + 32) * 4 roundings of 2^-24.
+Numerator and denominator each carry the error, so y is off by at most twice
+its sum times V."""
+import numpy as np
+import pytest
+
+from oracle import decode
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+from packed_bit_gemv_tern_amd import tern  # noqa: E402
+from gpu_util import DEV, to_dev  # noqa: E402
+from kv_util import Paged  # noqa: E402
+
+
+def attend(pg, new, length, q_heads, extra=0, q_size=2.0, scale=None, q=None, **kw):
+    b = pg.batch(new, length, **kw)
+    D, width = pg.D, q_heads * pg.D
+    scale = D ** -0.5 if scale is None else scale
+    q = pg.rng.normal(0, q_size, (pg.rows, q_heads, D)).astype(np.float32) if q is None else q
+    qd = torch.full((pg.rows, width + extra), float("nan"), device=DEV)
+    qd[:, :width] = to_dev(q.reshape(pg.rows, width))
+    y = torch.full((pg.rows, width + extra), 77.0, device=DEV)
+    n = tern.tern_attention_workspace_bytes(pg.cache, b, q_heads)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)  # (NaN where read before it is written)
+    tern.tern_attention(pg.cache, b, qd, width + extra, q_heads, scale, y, width + extra, ws)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy()
+    assert (got[:, width:] == 77).all()
+    got = got[:, :width].reshape(pg.rows, q_heads, D)
+    ref = np.full((pg.rows, q_heads, D), 77.0)
+    size = decode.attention(pg.host, pg.table, pg.start, pg.length, q, scale, pg.max_new, ref)
+    A, V = size[..., 0:1], size[..., 1:2]
+    n = max(1, int(max(length)))
+    tol = 2 * V * (A * (2 ** -21 + 24 * 2 ** -24) + 2 ** -22 + 2 ** -21 + (n / 64 + 32) * 4 * 2 ** -24)
+    err = np.abs(got - ref)
+    assert np.isfinite(got).all()
+    assert (err <= tol).all(), "off by %.3g, %.3g allowed, at %s" % (
+        err.max(), tol.flat[np.argmax(err - tol)], np.unravel_index(np.argmax(err - tol), err.shape))
+    return got
+
+
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 63, 64, 65, 255, 256, 257, 1000])
+@pytest.mark.parametrize("P,D", [(16, 128), (64, 128), (32, 64), (128, 64)])
+def test_one_token(length, P, D):
+    pg = Paged(2, -(-1000 // P), 2, D, P).upload()
+    attend(pg, [1, 1], [length, max(1, length // 2)], 8)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (8, 4), (3, 5), (2, 8), (1, 17), (2, 40)])
+def test_head_layouts(heads, group):
+    pg = Paged(2, 5, heads, 128, 64, seed=1).upload()
+    attend(pg, [1, 1], [300, 77], heads * group)
+    attend(pg, [3, 5], [300, 5], heads * group)
+
+
+@pytest.mark.parametrize("new", [2, 4, 5, 8, 9, 16, 31, 64, 100])
+@pytest.mark.parametrize("P", [16, 64])
+def test_drafted_tokens_and_prompts(new, P):
+    """Causal among the new rows: context before them, and none."""
+    pg = Paged(3, -(-700 // P), 2, 128, P, seed=2).upload()
+    attend(pg, [new, max(1, new // 2), new], [700, max(1, new // 2), new + 1], 8)
+
+
+@pytest.mark.parametrize("max_len", [0, 1, 5000, 10 ** 6])
+def test_long_context_and_hint(max_len):
+    """The hint sets the pieces, not the result: too small, right, too large."""
+    pg = Paged(2, -(-5000 // 32), 1, 128, 32, seed=3).upload()
+    attend(pg, [1, 1], [5000, 1300], 4, max_len=max_len)
+    attend(pg, [6, 6], [4999, 64], 4, max_len=max_len)
+
+
+def test_ragged_batch_with_idle_slots():
+    """Idle slots (one row, length 0) give 0; rows of no sequence are left as
+    they were, and sequences without rows cost nothing."""
+    pg = Paged(9, 8, 2, 64, 16, seed=4).upload()
+    got = attend(pg, [1, 1, 0, 3, 1, 1, 1, 0, 2], [100, 0, 50, 3, 128, 17, 0, 0, 1], 4, rows=14)
+    assert (got[1] == 0).all() and (got[7] == 0).all()
+    assert (got[8] == 0).all()   # the first of two new rows where one position is held
+    assert (got[10:] == 77).all()
+
+
+def test_bad_pages():
+    """A page outside the cache holds nothing; a row that sees only such pages
+    is 0; lengths past the table end at it."""
+    pg = Paged(4, 4, 2, 128, 64, seed=5).upload()
+    pg.table[0, 1], pg.table[1, :], pg.table[2, 3] = -5, pg.host.pages, 2 ** 31 - 1
+    got = attend(pg, [1, 2, 3, 1], [256, 200, 250, 10 ** 9], 8)
+    assert (got[1:3] == 0).all()
+
+
+def test_pages_never_written():
+    """Slots past the length, and pages the table names past it, hold
+    anything, scales of NaN and infinity among it."""
+    pg = Paged(2, 6, 2, 64, 16, seed=6)
+    for p in pg.table[:, 3:].flat:
+        pg.host.k_scale[p], pg.host.v_scale[p] = np.nan, np.inf
+    pg.upload()
+    attend(pg, [1, 3], [48, 33], 4)
+    pg.table[:, 3:] = -1
+    attend(pg, [1, 3], [48, 33], 4)
+
+
+@pytest.mark.parametrize("lo,hi", [(-6, 3), (-20, -15), (8, 12)])
+def test_value_scales_apart(lo, hi):
+    """Value scales over many powers of ten in one context, and pages of
+    zeros."""
+    def scales(rng, shape):
+        s = 10.0 ** rng.uniform(lo, hi, shape)
+        s[0] = rng.uniform(0.005, 0.02, shape[1:])
+        s[1][rng.random(shape[1:]) < 0.2] = 0
+        return s
+    pg = Paged(2, 20, 2, 128, 16, seed=7, scales=scales).upload()
+    attend(pg, [1, 4], [320, 211], 8)
+
+
+@pytest.mark.parametrize("q_size", [0.0, 1e-12, 1e-3, 10.0, 1e6])
+def test_query_sizes(q_size):
+    """From scores of nothing (the mean of the values) to one position taking
+    it all."""
+    pg = Paged(2, 5, 2, 64, 64, seed=8).upload()
+    attend(pg, [1, 2], [300, 40], 8, q_size=q_size)
+
+
+def test_negative_and_zero_scale():
+    pg = Paged(2, 5, 2, 64, 64, seed=9).upload()
+    attend(pg, [1, 2], [300, 40], 8, scale=-0.2)
+    attend(pg, [1, 2], [300, 40], 8, scale=0.0)
+
+
+def test_strides():
+    pg = Paged(2, 5, 2, 128, 32, seed=10).upload()
+    attend(pg, [2, 1], [130, 40], 8, extra=1)
+    attend(pg, [2, 1], [130, 40], 8, extra=4)
+
+
+def test_shared_pages():
+    """Two sequences reading the same pages, and one page twice in a table."""
+    pg = Paged(2, 5, 2, 128, 32, seed=11).upload()
+    pg.table[1, :3] = pg.table[0, :3]
+    pg.table[1, 4] = pg.table[1, 3]
+    attend(pg, [1, 1], [160, 155], 8)
+
+
+def test_rows_past_max_new():
+    pg = Paged(2, 5, 2, 128, 32, seed=12).upload()
+    got = attend(pg, [6, 2], [130, 40], 8, max_new=4)
+    assert (got[4:6] == 77).all()
