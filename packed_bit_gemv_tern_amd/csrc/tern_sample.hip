@@ -15,42 +15,57 @@
 // Weights are computed in fp64 and summed as integers of 2^-44, so a sum is
 // the same in whatever order it is taken (atomics included), and two rows
 // with the same logits draw the same token.  The largest weight is 1, so
-// 2^18 tokens sum to less than 2^63.
+// 2^19 tokens sum to less than 2^63.
+//
+// Nothing is sorted but a few tokens around the cut.  A row is split in
+// chunks, one workgroup each, and goes through up to four launches:
+//   1. the largest logit and the number of live tokens of each chunk;
+//   2. (rows with top-k or top-p) a histogram of the row, counts and weights
+//      in bins of 1/32 of log-probability below the maximum;
+//   3. from the histogram every workgroup finds the bins that the cuts fall
+//      in, lists the tokens of those bins, and sums the weight that its chunk
+//      holds in the bins above;
+//   4. one workgroup per row orders the listed tokens, fixes the cut exactly,
+//      finds the chunk that the random number falls in, and walks that chunk.
+// A row whose cut bins hold more than kListMax tokens (many equal logits) is
+// cut by the bits of its keys instead, by that one workgroup (slow_cut).
+#include "tern.h"
 #include "tern_device.h"
 
 namespace tern {
 
 namespace {
 
-constexpr int kSampleT = 1024;
-constexpr double kFix = 17592186044416.0;  // 2^44
+typedef unsigned long long u64;
 
-// e^x for x <= 0 (0 below -708) by Cody and Waite's reduction x = k ln 2 + r
-// and the Taylor series of e^r through r^13 (|r| <= 0.347: its next term is
-// 4e-18), in fp64.
-__device__ __forceinline__ double exp_neg(double x) {
-  if (!(x > -708.0)) return 0.0;
-  constexpr double kInvLn2 = 1.4426950408889634074;
-  constexpr double kHead = 0.693147180369123816490;  // ln 2 to 33 bits
-  constexpr double kTail = 1.90821492927058770002e-10;
-  const double k = __builtin_rint(x * kInvLn2);
-  const double r = __builtin_fma(-k, kTail, __builtin_fma(-k, kHead, x));
-  double p = 1.0 / 6227020800.0;
-  p = __builtin_fma(p, r, 1.0 / 479001600.0);
-  p = __builtin_fma(p, r, 1.0 / 39916800.0);
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)k);
-}
+constexpr int kT = 256;          // threads of launches 1 to 3
+constexpr int kFinishT = 1024;   // threads of launch 4
+constexpr int kBins = 1024;      // of 1/32 each; the last one holds all that is further below
+constexpr float kBinsPerUnit = 32.0f;
+constexpr uint32_t kListMax = 2048;
+constexpr int kChunkMin = 4 * kT;
+constexpr int kChunksMax = TERN_SAMPLE_MAX_N / kChunkMin;
+constexpr double kFix = 17592186044416.0;  // 2^44
+static_assert((kBins - 1) / kBinsPerUnit > 31.9f, "the last bin's weights round to 0: 2^44 e^-31.9 < 1/2");
+
+// 2^(-j / 64)
+__constant__ double kExp2[64] = {
+    0x1.0000000000000p+0, 0x1.fa7c1819e90d8p-1, 0x1.f50765b6e4540p-1, 0x1.efa1bee615a27p-1,
+    0x1.ea4afa2a490dap-1, 0x1.e502ee78b3ff6p-1, 0x1.dfc97337b9b5fp-1, 0x1.da9e603db3285p-1,
+    0x1.d5818dcfba487p-1, 0x1.d072d4a07897cp-1, 0x1.cb720dcef9069p-1, 0x1.c67f12e57d14bp-1,
+    0x1.c199bdd85529cp-1, 0x1.bcc1e904bc1d2p-1, 0x1.b7f76f2fb5e47p-1, 0x1.b33a2b84f15fbp-1,
+    0x1.ae89f995ad3adp-1, 0x1.a9e6b5579fdbfp-1, 0x1.a5503b23e255dp-1, 0x1.a0c667b5de565p-1,
+    0x1.9c49182a3f090p-1, 0x1.97d829fde4e50p-1, 0x1.93737b0cdc5e5p-1, 0x1.8f1ae99157736p-1,
+    0x1.8ace5422aa0dbp-1, 0x1.868d99b4492edp-1, 0x1.82589994cce13p-1, 0x1.7e2f336cf4e62p-1,
+    0x1.7a11473eb0187p-1, 0x1.75feb564267c9p-1, 0x1.71f75e8ec5f74p-1, 0x1.6dfb23c651a2fp-1,
+    0x1.6a09e667f3bcdp-1, 0x1.6623882552225p-1, 0x1.6247eb03a5585p-1, 0x1.5e76f15ad2148p-1,
+    0x1.5ab07dd485429p-1, 0x1.56f4736b527dap-1, 0x1.5342b569d4f82p-1, 0x1.4f9b2769d2ca7p-1,
+    0x1.4bfdad5362a27p-1, 0x1.486a2b5c13cd0p-1, 0x1.44e086061892dp-1, 0x1.4160a21f72e2ap-1,
+    0x1.3dea64c123422p-1, 0x1.3a7db34e59ff7p-1, 0x1.371a7373aa9cbp-1, 0x1.33c08b26416ffp-1,
+    0x1.306fe0a31b715p-1, 0x1.2d285a6e4030bp-1, 0x1.29e9df51fdee1p-1, 0x1.26b4565e27cddp-1,
+    0x1.2387a6e756238p-1, 0x1.2063b88628cd6p-1, 0x1.1d4873168b9aap-1, 0x1.1a35beb6fcb75p-1,
+    0x1.172b83c7d517bp-1, 0x1.1429aaea92de0p-1, 0x1.11301d0125b51p-1, 0x1.0e3ec32d3d1a2p-1,
+    0x1.0b5586cf9890fp-1, 0x1.0874518759bc8p-1, 0x1.059b0d3158574p-1, 0x1.02c9a3e778061p-1};
 
 // Monotone key of a logit: larger logit, larger key; 0 for those that can
 // never be drawn (-inf and NaN).  +0 and -0 compare equal and share a key.
@@ -64,31 +79,151 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-typedef unsigned long long u64;
-
-struct RowParams {
-  double inv_t, top_p, min_p;
-  float mx, u;
-  bool greedy;
-  int64_t k;  // tokens of top-k (N: no limit)
+// A row's place in the workspace: its histogram, list and chunks.
+struct RowWs {
+  u64* mass;        // kBins
+  u64* list;        // kListMax: key, complement of the index
+  u64* chunk_top;   // key, complement of the index, of a chunk's largest logit
+  u64* chunk_mass;  // weight that a chunk holds above the cut bins, and its tokens
+  uint32_t* count;  // kBins
+  uint32_t* chunk_live;
+  uint32_t* chunk_kept;
+  uint32_t* list_n;
 };
 
-__device__ __forceinline__ double weight_of(const RowParams& r, float x) {
-  if (x == r.mx) return 1.0;  // (also where both are +inf)
-  return exp_neg(((double)x - (double)r.mx) * r.inv_t);
+struct Launch {
+  SampleArgs a;
+  uint8_t* ws;
+  int64_t row_bytes;
+  int32_t per, chunks;  // tokens per chunk
+  bool vec;             // rows are 16-byte aligned
+};
+
+__host__ __device__ inline int64_t row_ws_bytes(int64_t chunks) {
+  return ((kBins + kListMax) * 8 + chunks * 16 + kBins * 4 + chunks * 8 + 4 + 255) / 256 * 256;
 }
-__device__ __forceinline__ u64 fixed(double w) { return (u64)__builtin_rint(w * kFix); }
 
-struct SampleLds {
-  u64 mass[256];
-  uint32_t count[256];
-  u64 wave64[16];
-  uint32_t wave32[16];
-  u64 out64[2];
-  uint32_t out32[4];
+__device__ __forceinline__ RowWs row_ws(const Launch& L, int64_t row) {
+  uint8_t* p = L.ws + row * L.row_bytes;
+  RowWs w;
+  w.mass = reinterpret_cast<u64*>(p);
+  w.list = w.mass + kBins;
+  w.chunk_top = w.list + kListMax;
+  w.chunk_mass = w.chunk_top + L.chunks;
+  w.count = reinterpret_cast<uint32_t*>(w.chunk_mass + L.chunks);
+  w.chunk_live = w.count + kBins;
+  w.chunk_kept = w.chunk_live + L.chunks;
+  w.list_n = w.chunk_kept + L.chunks;
+  return w;
+}
+
+struct Row {
+  const float* x;
+  double inv_t, top_p, min_p;
+  u64 top;        // key and complement of the index of the first token (0: none)
+  uint32_t live;  // tokens that can be drawn
+  uint32_t k;     // tokens of top-k (live: no limit)
+  float mx, bin_scale, u;
+  bool greedy;
 };
 
-// Exclusive prefix over the workgroup of v (thread order), and the total.
+// The row's parameters, its largest logit and live tokens from the chunks of
+// launch 1 (the same on every thread; `lds` holds 2 T / 64 words).
+template <int T>
+__device__ Row load_row(const Launch& L, const RowWs& w, int64_t row, u64* lds) {
+  const SampleArgs& a = L.a;
+  Row r;
+  r.x = a.x + row * a.ldx;
+  u64 top = 0;
+  uint32_t live = 0;
+  for (int c = threadIdx.x; c < L.chunks; c += T) {
+    const u64 v = load_g(w.chunk_top + c);
+    top = v > top ? v : top;
+    live += load_g(w.chunk_live + c);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const u64 o = __shfl_xor(top, d, 64);
+    top = o > top ? o : top;
+    live += __shfl_xor(live, d, 64);
+  }
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top, lds[T / 64 + (threadIdx.x >> 6)] = live;
+  __syncthreads();
+  live = 0;
+  for (int i = 0; i < T / 64; ++i) {
+    top = lds[i] > top ? lds[i] : top;
+    live += (uint32_t)lds[T / 64 + i];
+  }
+  __syncthreads();
+  const float t = load_g(a.temperature + row);
+  const int32_t k = a.top_k ? load_g(a.top_k + row) : 0;
+  const float tp = a.top_p ? load_g(a.top_p + row) : 1.0f, mp = a.min_p ? load_g(a.min_p + row) : 0.0f;
+  r.top = top;
+  r.live = live;
+  r.mx = key_logit((uint32_t)(top >> 32));
+  r.greedy = !(t > 0.0f);
+  r.inv_t = 1.0 / (double)t;
+  r.bin_scale = (float)(r.inv_t * (double)kBinsPerUnit);
+  r.u = load_g(a.u + row);
+  r.k = k > 0 && (uint32_t)k < live ? (uint32_t)k : live;
+  r.top_p = tp < 1.0f ? (double)fmaxf(tp, 0.0f) : 1.0;  // (a NaN is no filter)
+  r.min_p = mp > 0.0f ? (double)fminf(mp, 1.0f) : 0.0;
+  return r;
+}
+
+// e^((x - max) / T) in fp64: with v = (max - x) / T = k ln 2 / 64 + s, the
+// table's 2^(-(k % 64) / 64), the Taylor series of e^-s through s^4 (|s| <=
+// 0.0055: its next term is 4e-14) and a power of two.
+__device__ __forceinline__ double weight_of(const Row& r, const double* tab, float x) {
+  if (x == r.mx) return 1.0;  // (also where both are +inf)
+  constexpr double kStep = 0x1.62e42fefa39efp-7, kPerUnit = 0x1.71547652b82fep+6;  // ln 2 / 64 and its inverse
+  const double v = ((double)r.mx - (double)x) * r.inv_t;
+  if (!(v < 700.0)) return 0.0;
+  const double k = __builtin_rint(v * kPerUnit);
+  const double s = __builtin_fma(k, kStep, -v);
+  double p = 1.0 / 24.0;
+  p = __builtin_fma(p, s, 1.0 / 6.0);
+  p = __builtin_fma(p, s, 0.5);
+  p = __builtin_fma(p, s, 1.0);
+  p = __builtin_fma(p, s, 1.0);
+  const int ki = (int)k;
+  return __builtin_ldexp(p * tab[ki & 63], -(ki >> 6));
+}
+// w in units of 2^-44, w <= 1: the mantissa of w 2^44 + 2^52
+__device__ __forceinline__ u64 fixed(double w) {
+  return __builtin_bit_cast(u64, __builtin_fma(w, kFix, 4503599627370496.0)) & 0xfffffffffffffull;
+}
+
+__device__ __forceinline__ int bin_of(const Row& r, float x) {
+  if (x == r.mx) return 0;
+  return (int)fminf((r.mx - x) * r.bin_scale, (float)(kBins - 1));  // (a NaN, from T = inf: the last bin)
+}
+
+// fn(index, logit) for the tokens [j0, j1) of a row, four consecutive ones
+// per thread and step.
+template <int T, typename Fn>
+__device__ __forceinline__ void each_token(const float* x, int j0, int j1, bool vec, Fn fn) {
+  for (int j = j0 + 4 * (int)threadIdx.x; j < j1; j += 4 * T) {
+    float v[4];
+    if (vec && j + 4 <= j1) {
+      const f32x4 g = __builtin_bit_cast(f32x4, load16(x + j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = g[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fn(j + i, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i < j1) fn(j + i, load_g(x + j + i));
+    }
+  }
+}
+
+__device__ __forceinline__ u64 pack_token(uint32_t key, int j) { return ((u64)key << 32) | (uint32_t)~(uint32_t)j; }
+
+// Exclusive prefix over the workgroup of v (thread order), and the total;
+// `wave` holds T / 64 words.
+template <int T>
 __device__ __forceinline__ u64 wg_scan(u64 v, u64* wave, u64& total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   u64 s = v;
@@ -102,206 +237,567 @@ __device__ __forceinline__ u64 wg_scan(u64 v, u64* wave, u64& total) {
   __syncthreads();
   u64 before = 0;
   total = 0;
-  for (int i = 0; i < kSampleT / 64; ++i) {
+  for (int i = 0; i < T / 64; ++i) {
     if (i < w) before += wave[i];
     total += wave[i];
   }
   return before + s - v;
 }
 
-// The first tokens of the order up to a border: keys above `key`, and of
-// those with that key the `ties` lowest indices.
-struct Border {
-  uint32_t key;
-  uint32_t ties;
-};
-
-// Finds the border by the 32 bits of the keys, 8 at a time from the top: of
-// the tokens inside `in`, the first `want` (by count) or the first whose
-// forerunners hold less than `mass` (by mass).
-template <bool BY_MASS>
-__device__ Border find_border(const float* x, int64_t N, const RowParams& r, Border in, uint32_t want, u64 mass,
-                              SampleLds& L) {
-  uint32_t prefix = 0, mask = 0, before_n = 0;
-  u64 before_m = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kSampleT) L.mass[i] = 0, L.count[i] = 0;
-    __syncthreads();
-    for (int64_t j = threadIdx.x; j < N; j += kSampleT) {
-      const float v = load_g(x + j);
-      const uint32_t k = logit_key(v);
-      if (k == 0 || (k & mask) != prefix || k < in.key) continue;
-      const int bin = (k >> shift) & 255;
-      atomicAdd(&L.count[bin], 1u);
-      if (BY_MASS) atomicAdd(&L.mass[bin], fixed(weight_of(r, v)));
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int bin = 255;
-      uint32_t n = before_n;
-      u64 m = before_m;
-      for (; bin > 0; --bin) {  // the last bin that is not empty holds the border at the latest
-        if (L.count[bin]) {
-          const bool inside = BY_MASS ? m + L.mass[bin] >= mass : n + L.count[bin] >= want;
-          if (inside) break;
-        }
-        n += L.count[bin];
-        m += L.mass[bin];
-      }
-      L.out32[0] = (uint32_t)bin;
-      L.out32[1] = n;
-      L.out64[0] = m;
-    }
-    __syncthreads();
-    prefix |= L.out32[0] << shift;
-    mask |= 255u << shift;
-    before_n = L.out32[1];
-    before_m = L.out64[0];
-    __syncthreads();
-  }
-  // tokens with the border's key: all have one weight
-  Border out;
-  out.key = prefix;
-  const uint32_t here = L.count[prefix & 255];
-  if (BY_MASS) {
-    const u64 w = fixed(weight_of(r, key_logit(prefix)));
-    // the i-th of them is kept where before_m + i w < mass
-    const u64 need = mass > before_m ? mass - before_m : 0;
-    const u64 n = w ? (need + w - 1) / w : (need ? here : 0);
-    out.ties = (uint32_t)min((u64)here, n);
-  } else {
-    out.ties = min(here, want - before_n);
-  }
-  __syncthreads();
-  if (prefix == in.key) out.ties = min(out.ties, in.ties);
-  return out;
+// Units of weight that the forerunners of a token kept by top-p stay below:
+// forerunners < top_p * total, at least one (the first token always).
+__device__ __forceinline__ u64 mass_limit(double top_p, u64 total) {
+  const double lim = top_p * (double)total;
+  u64 n = (u64)lim;
+  if ((double)n < lim) ++n;
+  return n ? n : 1;
 }
 
-__global__ __launch_bounds__(kSampleT) void sample_kernel(SampleArgs a) {
-  __shared__ SampleLds L;
-  __shared__ u64 best[16];
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-  const int64_t row = blockIdx.x, N = a.N;
-  const float* x = a.x + row * a.ldx;
+// ------------------------------------------------------ launch 1: maxima --
 
-  // largest logit, its lowest index, and the tokens that can be drawn
-  u64 top = 0;  // key, then the complement of the index
-  uint32_t live = 0;
-  for (int64_t j = t; j < N; j += kSampleT) {
-    const uint32_t k = logit_key(load_g(x + j));
-    live += k != 0;
-    const u64 v = k ? ((u64)k << 32) | (uint32_t)~(uint32_t)j : 0;
-    top = v > top ? v : top;
+__global__ __launch_bounds__(kT) void top_kernel(Launch L) {
+  __shared__ u64 tops[kT / 64];
+  __shared__ uint32_t lives[kT / 64];
+  const int c = blockIdx.x % L.chunks;
+  const int64_t row = blockIdx.x / L.chunks;
+  const RowWs w = row_ws(L, row);
+  // the row's histogram and list start empty, its chunks clearing a share each
+  for (int i = c * kT + threadIdx.x; i < kBins; i += L.chunks * kT) {
+    store_g(w.mass + i, (u64)0);
+    store_g(w.count + i, 0u);
   }
+  if (c == 0 && threadIdx.x == 0) store_g(w.list_n, 0u);
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  u64 top = 0;
+  uint32_t live = 0;
+  each_token<kT>(L.a.x + row * L.a.ldx, j0, j1, L.vec, [&](int j, float x) {
+    const uint32_t k = logit_key(x);
+    if (!k) return;
+    ++live;
+    const u64 t = pack_token(k, j);
+    top = t > top ? t : top;
+  });
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
     const u64 o = __shfl_xor(top, d, 64);
     top = o > top ? o : top;
     live += __shfl_xor(live, d, 64);
   }
-  if (lane == 0) best[wv] = top, L.wave32[wv] = live;
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top, lives[threadIdx.x >> 6] = live;
   __syncthreads();
-  live = 0;
-  for (int i = 0; i < kSampleT / 64; ++i) {
-    top = best[i] > top ? best[i] : top;
-    live += L.wave32[i];
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kT / 64; ++i) {
+      top = tops[i] > top ? tops[i] : top;
+      live += lives[i];
+    }
+    store_g(w.chunk_top + c, top);
+    store_g(w.chunk_live + c, live);
   }
-  RowParams r;
-  const float T = load_g(a.temperature + row);
-  r.mx = key_logit((uint32_t)(top >> 32));
-  r.greedy = !(T > 0.0f);
-  r.inv_t = 1.0 / (double)T;
-  r.u = load_g(a.u + row);
-  const int32_t k = a.top_k ? load_g(a.top_k + row) : 0;
-  r.k = k > 0 ? k : N;
-  const float tp = a.top_p ? load_g(a.top_p + row) : 1.0f, mp = a.min_p ? load_g(a.min_p + row) : 0.0f;
-  r.top_p = tp < 1.0f ? (double)fmaxf(tp, 0.0f) : 1.0;  // (a NaN is no filter)
-  r.min_p = mp > 0.0f ? (double)fminf(mp, 1.0f) : 0.0;
-  if (live == 0 || r.greedy) {
+}
+
+// --------------------------------------------------- launch 2: histogram --
+
+__device__ __forceinline__ bool wants_bins(const Row& r) { return r.k < r.live || r.top_p < 1.0; }
+
+__global__ __launch_bounds__(kT) void histogram_kernel(Launch L) {
+  __shared__ u64 mass[kBins];
+  __shared__ uint32_t count[kBins];
+  __shared__ double tab[64];
+  __shared__ u64 red[2 * kT / 64];
+  const int c = blockIdx.x % L.chunks;
+  const int64_t row = blockIdx.x / L.chunks;
+  const RowWs w = row_ws(L, row);
+  const Row r = load_row<kT>(L, w, row, red);
+  if (r.greedy || r.live == 0 || !wants_bins(r)) return;
+  if (threadIdx.x < 64) tab[threadIdx.x] = kExp2[threadIdx.x];
+  for (int i = threadIdx.x; i < kBins; i += kT) mass[i] = 0, count[i] = 0;
+  __syncthreads();
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  const bool weigh = r.top_p < 1.0;
+  uint32_t rest = 0;  // the last bin: no weight, and too many tokens for one counter
+  each_token<kT>(r.x, j0, j1, L.vec, [&](int, float x) {
+    if (!logit_key(x)) return;
+    const int b = bin_of(r, x);
+    if (b == kBins - 1) {
+      ++rest;
+      return;
+    }
+    atomicAdd(&count[b], 1u);
+    if (weigh) atomicAdd(&mass[b], fixed(weight_of(r, tab, x)));
+  });
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) rest += __shfl_xor(rest, d, 64);
+  if ((threadIdx.x & 63) == 0 && rest) atomicAdd(&count[kBins - 1], rest);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kT) {
+    if (!count[i]) continue;
+    atomicAdd(w.count + i, count[i]);
+    if (weigh) atomicAdd(w.mass + i, mass[i]);
+  }
+}
+
+// ------------------------------------------------------------ the cuts --
+
+// Where the cuts fall, from the histogram: bins below `sure` are kept (as far
+// as top-k and top-p go), and the tokens of bins [p1, p2] and of bin `kbin`
+// are listed to be ordered.
+struct Cut {
+  int sure, p1, p2, kbin;  // p1 > p2: no bins of top-p; kbin = kBins: top-k ends with a bin
+  uint32_t kneed;          // tokens of bin kbin among the first k
+  uint32_t rest_kept;      // tokens kept of the last bin, which holds no weight and is not listed
+  u64 mass_p1, mass_k;     // weight before bin p1; before bin kbin, or of the first k
+};
+
+struct CutLds {
+  u64 wave[16];
+  int kb;
+  uint32_t kbefore, kcount;
+  u64 kmass, kbin_mass;
+  int p[2];
+  u64 pm[2];
+};
+
+template <int T>
+__device__ Cut find_cut(const Row& r, const RowWs& w, CutLds& S) {
+  constexpr int V = kBins / T;
+  Cut c;
+  c.sure = kBins;
+  c.p1 = 1, c.p2 = 0;
+  c.kbin = kBins;
+  c.kneed = c.rest_kept = 0;
+  c.mass_p1 = c.mass_k = 0;
+  if (!wants_bins(r)) return c;
+  uint32_t n[V];
+  u64 m[V], nsum = 0, msum = 0, all;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    n[i] = load_g(w.count + V * threadIdx.x + i);
+    m[i] = r.top_p < 1.0 ? load_g(w.mass + V * threadIdx.x + i) : 0;
+    nsum += n[i], msum += m[i];
+  }
+  u64 nb = wg_scan<T>(nsum, S.wave, all);
+  u64 total;
+  const u64 mb0 = wg_scan<T>(msum, S.wave, total);
+  // the bin that the k-th token lies in
+  if (threadIdx.x == 0) S.kb = kBins;
+  __syncthreads();
+  u64 mb = mb0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (nb < r.k && nb + n[i] >= r.k) {  // (one bin at most; r.k >= 1)
+      S.kb = V * (int)threadIdx.x + i;
+      S.kbefore = (uint32_t)nb, S.kcount = n[i];
+      S.kmass = mb, S.kbin_mass = m[i];
+    }
+    nb += n[i], mb += m[i];
+  }
+  __syncthreads();
+  u64 z_lo, z_hi;  // bounds of the weight of the first k
+  const int kb = S.kb;
+  const uint32_t need = r.k - S.kbefore;
+  const bool part = need < S.kcount && kb < kBins - 1;  // (the last bin's tokens weigh nothing)
+  if (part) {
+    c.kbin = kb;
+    c.kneed = need;
+    c.mass_k = z_lo = S.kmass;
+    z_hi = S.kmass + S.kbin_mass;
+    c.sure = kb;
+  } else {
+    c.mass_k = z_lo = z_hi = S.kmass + S.kbin_mass;
+    c.sure = kb < kBins - 1 ? kb + 1 : kBins - 1;
+    // (a min-p above the last bin's weights, e^-31.9 at most, keeps none of its tokens)
+    if (kb == kBins - 1 && !(r.min_p > 1.5e-14)) c.rest_kept = need;
+  }
+  if (r.top_p < 1.0) {
+    const u64 lim[2] = {mass_limit(r.top_p, z_lo), mass_limit(r.top_p, z_hi)};
+    u64 before = mb0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (before < lim[e] && before + m[i] >= lim[e]) {
+          S.p[e] = V * (int)threadIdx.x + i;
+          S.pm[e] = before;
+        }
+      before += m[i];
+    }
+    __syncthreads();
+    c.p1 = S.p[0], c.p2 = S.p[1];
+    c.mass_p1 = S.pm[0];
+    c.sure = c.p1;
+    c.rest_kept = 0;
+  }
+  __syncthreads();
+  return c;
+}
+
+__device__ __forceinline__ bool listed(const Cut& c, int b) { return (b >= c.p1 && b <= c.p2) || b == c.kbin; }
+
+// ------------------------------------- launch 3: listed tokens and sums --
+
+__global__ __launch_bounds__(kT) void gather_kernel(Launch L) {
+  __shared__ double tab[64];
+  __shared__ u64 red[2 * kT / 64];
+  __shared__ CutLds S;
+  const int c = blockIdx.x % L.chunks;
+  const int64_t row = blockIdx.x / L.chunks;
+  const RowWs w = row_ws(L, row);
+  const Row r = load_row<kT>(L, w, row, red);
+  if (r.greedy || r.live == 0) return;
+  if (threadIdx.x < 64) tab[threadIdx.x] = kExp2[threadIdx.x];
+  __syncthreads();
+  const Cut cut = find_cut<kT>(r, w, S);
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  const uint32_t top_key = (uint32_t)(r.top >> 32);
+  u64 sum = 0, kept = 0;
+  each_token<kT>(r.x, j0, j1, L.vec, [&](int j, float x) {
+    const uint32_t key = logit_key(x);
+    if (!key) return;
+    const int b = bin_of(r, x);
+    if (b < cut.sure) {
+      const double wt = weight_of(r, tab, x);
+      if (wt >= r.min_p || key == top_key) {
+        sum += fixed(wt);
+        ++kept;
+      }
+    } else if (listed(cut, b)) {
+      const uint32_t at = atomicAdd(w.list_n, 1u);
+      if (at < kListMax) store_g(w.list + at, pack_token(key, j));
+    }
+  });
+  u64 total, n;
+  wg_scan<kT>(sum, S.wave, total);
+  wg_scan<kT>(kept, S.wave, n);
+  if (threadIdx.x == 0) {
+    store_g(w.chunk_mass + c, total);
+    store_g(w.chunk_kept + c, (uint32_t)n);
+  }
+}
+
+// ------------------------------------------------------ launch 4: the draw --
+
+// Tokens kept: those with key and index up to the border, and in the bins
+// that are kept for sure.
+struct Keep {
+  u64 border;  // packed token: kept where the token's own is not less
+  int sure;
+};
+
+struct FinishLds {
+  double tab[64];
+  u64 red[2 * kFinishT / 64];
+  CutLds cut;
+  u64 mass[256];
+  uint32_t count[256];
+  u64 tok[kListMax];
+  u64 sorted[kListMax];
+  u64 prefix[kListMax + 1];
+  uint32_t rank[kListMax];
+  uint32_t n;
+  uint32_t out32[2];
+  u64 out64;
+};
+
+// The border of a row by the bits of its keys, 8 at a time from the top, a
+// pass over the row for each: of the tokens down to the border `in`, the
+// first `want` (BY_MASS: those whose forerunners weigh less than `mass`).
+struct KeyBorder {
+  uint32_t key, ties;  // tokens with larger keys, and the first `ties` of those with this one
+};
+template <bool BY_MASS>
+__device__ KeyBorder key_border(const Launch& L, const Row& r, KeyBorder in, uint32_t want, u64 mass, FinishLds& F) {
+  uint32_t prefix = 0, mask = 0, before_n = 0;
+  u64 before_m = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kFinishT) F.mass[i] = 0, F.count[i] = 0;
+    __syncthreads();
+    each_token<kFinishT>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
+      const uint32_t k = logit_key(x);
+      if (k == 0 || (k & mask) != prefix || k < in.key) return;
+      const int bin = (k >> shift) & 255;
+      atomicAdd(&F.count[bin], 1u);
+      if (BY_MASS) atomicAdd(&F.mass[bin], fixed(weight_of(r, F.tab, x)));
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int bin = 255;
+      uint32_t n = before_n;
+      u64 m = before_m;
+      for (; bin > 0; --bin) {
+        if (F.count[bin] && (BY_MASS ? m + F.mass[bin] >= mass : n + F.count[bin] >= want)) break;
+        n += F.count[bin];
+        m += F.mass[bin];
+      }
+      F.out32[0] = (uint32_t)bin;
+      F.out32[1] = n;
+      F.out64 = m;
+    }
+    __syncthreads();
+    prefix |= F.out32[0] << shift;
+    mask |= 255u << shift;
+    before_n = F.out32[1];
+    before_m = F.out64;
+    __syncthreads();
+  }
+  KeyBorder out;
+  out.key = prefix;
+  const uint32_t here = F.count[prefix & 255];
+  if (BY_MASS) {
+    // equal keys, equal weights: the i-th is kept where before_m + i w < mass
+    const u64 w = fixed(weight_of(r, F.tab, key_logit(prefix)));
+    const u64 need = mass > before_m ? mass - before_m : 0;
+    out.ties = (uint32_t)min((u64)here, w ? (need + w - 1) / w : (need ? (u64)here : 0));
+  } else {
+    out.ties = min(here, want - before_n);
+  }
+  if (prefix == in.key) out.ties = min(out.ties, in.ties);
+  __syncthreads();
+  return out;
+}
+
+// Cuts a row of too many equal logits, and redoes its chunks' sums.
+__device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLds& F) {
+  KeyBorder cut = {1u, 0xffffffffu};
+  if (r.k < r.live) cut = key_border<false>(L, r, cut, r.k, 0, F);
+  if (r.top_p < 1.0) {
+    u64 sum = 0, total;
+    each_token<kFinishT>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
+      const uint32_t k = logit_key(x);
+      if (k > cut.key || (k == cut.key && cut.ties == 0xffffffffu)) sum += fixed(weight_of(r, F.tab, x));
+    });
+    wg_scan<kFinishT>(sum, F.red, total);
+    if (cut.ties != 0xffffffffu) total += (u64)cut.ties * fixed(weight_of(r, F.tab, key_logit(cut.key)));
+    cut = key_border<true>(L, r, cut, 0, mass_limit(r.top_p, total), F);
+  }
+  // the index of the last tie inside: the one with ties - 1 before it
+  Keep keep = {pack_token(cut.key, 0x7fffffff), 0};
+  uint32_t seen = 0;
+  for (int j0 = 0; j0 < (int)L.a.N && cut.ties != 0xffffffffu; j0 += 4 * kFinishT) {
+    const int j1 = (int)min((int64_t)j0 + 4 * kFinishT, L.a.N);
+    uint32_t mine = 0;
+    each_token<kFinishT>(r.x, j0, j1, L.vec, [&](int, float x) { mine += logit_key(x) == cut.key; });
+    u64 all;
+    uint32_t at = seen + (uint32_t)wg_scan<kFinishT>(mine, F.red, all);
+    each_token<kFinishT>(r.x, j0, j1, L.vec, [&](int j, float x) {
+      if (logit_key(x) == cut.key && ++at == cut.ties) F.out64 = pack_token(cut.key, j);
+    });
+    seen += (uint32_t)all;
+    if (seen >= cut.ties) break;
+  }
+  __syncthreads();
+  if (cut.ties != 0xffffffffu) keep.border = F.out64;
+  for (int c = 0; c < L.chunks; ++c) {
+    u64 sum = 0, kept = 0;
+    each_token<kFinishT>(r.x, c * L.per, (int)min((int64_t)(c + 1) * L.per, L.a.N), L.vec, [&](int j, float x) {
+      const uint32_t k = logit_key(x);
+      if (!k || pack_token(k, j) < keep.border) return;
+      const double wt = weight_of(r, F.tab, x);
+      if (wt >= r.min_p || k == (uint32_t)(r.top >> 32)) sum += fixed(wt), ++kept;
+    });
+    u64 total, n;
+    wg_scan<kFinishT>(sum, F.red, total);
+    wg_scan<kFinishT>(kept, F.red, n);
+    if (threadIdx.x == 0) {
+      store_g(w.chunk_mass + c, total);
+      store_g(w.chunk_kept + c, (uint32_t)n);
+    }
+  }
+  __syncthreads();
+  return keep;
+}
+
+__global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
+  __shared__ u64 cmass[kChunksMax];  // a chunk's kept weight, that of its listed tokens included
+  __shared__ FinishLds F;
+  const SampleArgs& a = L.a;
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x;
+  const RowWs w = row_ws(L, row);
+  const Row r = load_row<kFinishT>(L, w, row, F.red);
+  if (r.greedy || r.live == 0) {
     if (t == 0) {
-      store_g(a.token + row, live ? (int32_t)~(uint32_t)top : -1);
-      if (a.prob) store_g(a.prob + row, live ? 1.0f : 0.0f);
-      if (a.kept) store_g(a.kept + row, live ? 1 : 0);
+      store_g(a.token + row, r.live ? (int32_t)~(uint32_t)r.top : -1);
+      if (a.prob) store_g(a.prob + row, r.live ? 1.0f : 0.0f);
+      if (a.kept) store_g(a.kept + row, r.live ? 1 : 0);
     }
     return;
   }
-
-  Border cut = {1u, 0xffffffffu};  // every live token
-  if (r.k < (int64_t)live) cut = find_border<false>(x, N, r, cut, (uint32_t)r.k, 0, L);
-  if (r.top_p < 1.0) {
-    // weight of the first k: above the border, and the ties inside it
-    u64 sum = 0;
-    for (int64_t j = t; j < N; j += kSampleT) {
-      const float v = load_g(x + j);
-      const uint32_t kk = logit_key(v);
-      if (kk > cut.key || (kk == cut.key && cut.ties == 0xffffffffu)) sum += fixed(weight_of(r, v));
-    }
-    u64 total;
-    wg_scan(sum, L.wave64, total);
-    if (cut.ties != 0xffffffffu) total += (u64)cut.ties * fixed(weight_of(r, key_logit(cut.key)));
-    // forerunners < top_p * total, in whole units: forerunners < ceil(top_p * total)
-    const double lim = r.top_p > 0.0 ? r.top_p * (double)total : 0.0;
-    u64 mass = (u64)lim;
-    if ((double)mass < lim) ++mass;
-    if (mass == 0) mass = 1;  // the first token always
-    __syncthreads();
-    cut = find_border<true>(x, N, r, cut, 0, mass, L);
-  }
-
-  // kept weight, then the token at which its running sum passes u * total.
-  // Thread t takes a run of the row's tokens, so that the scan is in order.
-  const int64_t per = (N + kSampleT - 1) / kSampleT;
-  const int64_t j0 = min(N, t * per), j1 = min(N, j0 + per);
-  uint32_t ties = 0;
-  for (int64_t j = j0; j < j1; ++j) ties += logit_key(load_g(x + j)) == cut.key;
-  u64 all;
-  uint32_t ties_before = (uint32_t)wg_scan(ties, L.wave64, all);
-  auto keeps = [&](float v, uint32_t key, uint32_t& tie, double& w) {
-    if (key < cut.key || key == 0) return false;
-    if (key == cut.key && tie++ >= cut.ties) return false;
-    w = weight_of(r, v);
-    return w >= r.min_p || key == (uint32_t)(top >> 32);
+  if (t < 64) F.tab[t] = kExp2[t];
+  __syncthreads();
+  const Cut cut = find_cut<kFinishT>(r, w, F.cut);
+  const uint32_t top_key = (uint32_t)(r.top >> 32);
+  auto passes = [&](float x, uint32_t key, double& wt) {
+    wt = weight_of(r, F.tab, x);
+    return wt >= r.min_p || key == top_key;
   };
-  u64 sum = 0;
-  uint32_t kept = 0, tie = ties_before;
-  for (int64_t j = j0; j < j1; ++j) {
-    const float v = load_g(x + j);
-    double w;
-    if (keeps(v, logit_key(v), tie, w)) sum += fixed(w), ++kept;
+  Keep keep = {~0ull, cut.sure};
+  u64 list_kept = 0;
+  const uint32_t nl = wants_bins(r) ? load_g(w.list_n) : 0;
+  // (a minimum below the last bin's weights would have to look into it)
+  const bool slow = nl > kListMax || (cut.rest_kept && r.min_p > 0.0);
+  if (slow) {
+    keep = slow_cut(L, w, r, F);
+    for (int c = t; c < L.chunks; c += kFinishT) cmass[c] = load_g(w.chunk_mass + c);
+    __syncthreads();
+  } else {
+    for (int c = t; c < L.chunks; c += kFinishT) cmass[c] = load_g(w.chunk_mass + c);
+    const int n = (int)nl;
+    if (n) {
+      // order: each token's rank is the number of listed tokens before it,
+      // counted by as many threads as there are for a token
+      for (int i = t; i < n; i += kFinishT) F.tok[i] = load_g(w.list + i), F.rank[i] = 0;
+      __syncthreads();
+      int share = 1;
+      while (2 * share * n <= kFinishT) share *= 2;
+      for (int i = t; i < n * share; i += kFinishT) {
+        const int e = i / share;
+        const u64 me = F.tok[e];
+        uint32_t before = 0;
+        for (int o = i % share; o < n; o += share) before += F.tok[o] > me;
+        if (before) atomicAdd(&F.rank[e], before);
+      }
+      __syncthreads();
+      for (int i = t; i < n; i += kFinishT) F.sorted[F.rank[i]] = F.tok[i];
+      __syncthreads();
+      // weights before each of them, two per thread; tokens before bin kbin
+      u64 wt[2], sum = 0, before_k = 0, in_p = 0, all, nk, np;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * t + e;
+        wt[e] = 0;
+        if (i < n) {
+          const float x = key_logit((uint32_t)(F.sorted[i] >> 32));
+          const int b = bin_of(r, x);
+          wt[e] = fixed(weight_of(r, F.tab, x));
+          before_k += b < cut.kbin;
+          in_p += b <= cut.p2;
+        }
+        sum += wt[e];
+      }
+      u64 before = wg_scan<kFinishT>(sum, F.red, all);
+      wg_scan<kFinishT>(before_k, F.red, nk);
+      wg_scan<kFinishT>(in_p, F.red, np);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (2 * t + e <= n) F.prefix[2 * t + e] = before;
+        before += wt[e];
+      }
+      if (t == 0 && n == (int)kListMax) F.prefix[n] = all;
+      __syncthreads();
+      const int kend = cut.kbin < kBins ? (int)nk + (int)cut.kneed : n;  // listed tokens among the first k
+      int end = kend;
+      if (r.top_p < 1.0) {
+        const u64 z = cut.kbin < kBins ? cut.mass_k + F.prefix[kend] - F.prefix[nk] : cut.mass_k;
+        const u64 lim = mass_limit(r.top_p, z);
+        u64 in = 0, kept;
+        for (int i = t; i < min((int)np, kend); i += kFinishT) in += cut.mass_p1 + F.prefix[i] < lim;
+        wg_scan<kFinishT>(in, F.red, kept);
+        end = (int)kept;
+      }
+      if (end > 0) keep.border = F.sorted[end - 1];
+      u64 mine = 0;
+      for (int i = t; i < end; i += kFinishT) {
+        const uint32_t key = (uint32_t)(F.sorted[i] >> 32);
+        double wd;
+        if (!passes(key_logit(key), key, wd)) continue;
+        ++mine;
+        atomicAdd(&cmass[~(uint32_t)F.sorted[i] / (uint32_t)L.per], fixed(wd));
+      }
+      wg_scan<kFinishT>(mine, F.red, list_kept);
+    }
+    __syncthreads();
   }
-  u64 total, nkept;
-  __syncthreads();
-  const u64 before = wg_scan(sum, L.wave64, total);
-  __syncthreads();
-  wg_scan(kept, L.wave64, nkept);
+
+  // the chunk that u * total falls in
+  const int per_t = (L.chunks + kFinishT - 1) / kFinishT;
+  u64 sum = 0, kept = 0, total, nkept;
+  for (int c = t * per_t; c < min(L.chunks, (t + 1) * per_t); ++c) {
+    sum += cmass[c];
+    kept += load_g(w.chunk_kept + c);
+  }
+  u64 before = wg_scan<kFinishT>(sum, F.red, total);
+  wg_scan<kFinishT>(kept, F.red, nkept);
+  nkept += list_kept + (slow ? 0 : cut.rest_kept);
   const double u = r.u > 0.0f ? fmin((double)r.u, 1.0) : 0.0;
   u64 target = (u64)(u * (double)total);
   if (target >= total) target = total - 1;
-  if (before <= target && target < before + sum) {  // exactly one thread
-    u64 run = before;
-    tie = ties_before;
-    for (int64_t j = j0; j < j1; ++j) {
-      const float v = load_g(x + j);
-      double w;
-      if (!keeps(v, logit_key(v), tie, w)) continue;
-      run += fixed(w);
-      if (run > target) {
-        store_g(a.token + row, (int32_t)j);
-        if (a.prob) store_g(a.prob + row, (float)(w * kFix / (double)total));
-        if (a.kept) store_g(a.kept + row, (int32_t)nkept);
-        break;
-      }
-    }
+  if (before <= target && target < before + sum) {  // one thread
+    int c = t * per_t;
+    while (before + cmass[c] <= target) before += cmass[c++];
+    F.out32[0] = (uint32_t)c;
+    F.out64 = before;
   }
+  __syncthreads();
+  const int c = (int)F.out32[0];
+  before = F.out64;
+  __syncthreads();
+
+  // and the token in that chunk
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, a.N);
+  for (int j = j0; j < j1; j += 4 * kFinishT) {
+    const int me = j + 4 * t;
+    float x[4];
+    u64 wt[4], run = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wt[i] = 0;
+      x[i] = 0.0f;
+      if (me + i < j1) {
+        x[i] = load_g(r.x + me + i);
+        const uint32_t key = logit_key(x[i]);
+        double wd;
+        if (key && (bin_of(r, x[i]) < keep.sure || pack_token(key, me + i) >= keep.border) && passes(x[i], key, wd))
+          wt[i] = fixed(wd);
+      }
+      run += wt[i];
+    }
+    const u64 at = before + wg_scan<kFinishT>(run, F.red, all);
+    if (at <= target && target < at + run) {  // one thread of one step
+      u64 s = at;
+      int i = 0;
+      while (s + wt[i] <= target) s += wt[i++];
+      store_g(a.token + row, me + i);
+      if (a.prob) store_g(a.prob + row, (float)(weight_of(r, F.tab, x[i]) * kFix / (double)total));
+      if (a.kept) store_g(a.kept + row, (int32_t)nkept);
+    }
+    before += all;
+    if (before > target) break;
+  }
+}
+
+// Tokens per chunk: single rows need many small chunks to be read at once,
+// many rows larger ones.
+int64_t tokens_per_chunk(int64_t M, int64_t N) {
+  int64_t per = kChunkMin;
+  while (per < 16384 && M * ((N + per - 1) / per) > 2048) per *= 2;
+  return per;
 }
 
 }  // namespace
 
-int64_t sample_workspace_bytes(int64_t, int64_t) { return 0; }
-int64_t sample_work_items(int64_t M, int64_t) { return M * kSampleT; }
+int64_t sample_workspace_bytes(int64_t M, int64_t N) {
+  const int64_t per = tokens_per_chunk(M, N);
+  return mul_sat(M, row_ws_bytes((N + per - 1) / per));
+}
+int64_t sample_work_items(int64_t M, int64_t N) {
+  const int64_t per = tokens_per_chunk(M, N);
+  return mul_sat(mul_sat(M, (N + per - 1) / per), kFinishT);
+}
 
-hipError_t launch_sample(const SampleArgs& a, void*, hipStream_t s) {
-  hipLaunchKernelGGL(sample_kernel, dim3((unsigned)a.M), dim3(kSampleT), 0, s, a);
+hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
+  Launch L;
+  L.a = a;
+  L.ws = static_cast<uint8_t*>(workspace);
+  L.per = (int32_t)tokens_per_chunk(a.M, a.N);
+  L.chunks = (int32_t)((a.N + L.per - 1) / L.per);
+  L.row_bytes = row_ws_bytes(L.chunks);
+  L.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M == 1 || a.ldx % 4 == 0);
+  const dim3 grid((unsigned)(a.M * L.chunks));
+  hipLaunchKernelGGL(top_kernel, grid, dim3(kT), 0, s, L);
+  if (a.top_k || a.top_p) hipLaunchKernelGGL(histogram_kernel, grid, dim3(kT), 0, s, L);
+  hipLaunchKernelGGL(gather_kernel, grid, dim3(kT), 0, s, L);
+  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)a.M), dim3(kFinishT), 0, s, L);
   return hipGetLastError();
 }
 

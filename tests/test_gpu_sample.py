@@ -151,3 +151,29 @@ def test_rows_alike_draw_alike():
     p, ws = f(0.0), torch.empty(tern.tern_sample_workspace_bytes(40, 151936), dtype=torch.uint8, device=DEV)
     tern.tern_sample(xd, 40, 151936, 151936, f(0.9), f(0.77), token, ws, top_p=f(0.95), prob=p)
     assert (token == int(tok[0])).all() and (p == float(prob[0])).all()
+
+
+def test_cut_far_below_the_maximum():
+    """A cut among tokens whose weight is next to nothing: the first k are
+    counted all the same, and a tiny min_p is heeded."""
+    rng = np.random.default_rng(9)
+    x = rng.uniform(-80, 0, (6, 3000)).astype(np.float32)
+    x[:, 77] = 1.0
+    T, u = [0.5, 1.0, 0.2, 0.5, 1.0, 0.2], rng.random(6)
+    for k in (500, 2999, 3000):
+        draw(x, T, u, top_k=[k] * 6)
+        draw(x, T, u, top_k=[k] * 6, min_p=[1e-20, 1e-16, 1e-30, 1e-12, 3e-14, 1e-5])
+        draw(x, T, u, top_k=[k] * 6, top_p=[0.999] * 6)
+
+
+@pytest.mark.parametrize("n", [1, 2, 500, 2047, 2048, 2049, 2500])
+def test_cut_among_many_close_logits(n):
+    """Lists at, under and over the length that is ordered at once."""
+    rng = np.random.default_rng(n)
+    x = np.full((3, 9000), -20.0, np.float32)
+    for r in x:
+        r[rng.permutation(9000)[:n]] = rng.uniform(1.0, 1.02, n)
+    u = rng.random(3)
+    draw(x, [1.0] * 3, u, top_k=[max(1, n // 2)] * 3)
+    draw(x, [1.0] * 3, u, top_p=[0.4] * 3)
+    draw(x, [1.0] * 3, u, top_k=[max(1, n - 1)] * 3, top_p=[0.7] * 3, min_p=[0.5] * 3)
