@@ -21,7 +21,7 @@
 // chunks, one workgroup each, and goes through up to four launches:
 //   1. the largest logit and the number of live tokens of each chunk;
 //   2. (rows with top-k or top-p) a histogram of the row, counts and weights
-//      in bins of 1/32 of log-probability below the maximum;
+//      in bins of 3/64 of log2-probability below the maximum;
 //   3. from the histogram every workgroup finds the bins that the cuts fall
 //      in, lists the tokens of those bins, and sums the weight that its chunk
 //      holds in the bins above;
@@ -40,13 +40,12 @@ typedef unsigned long long u64;
 
 constexpr int kT = 256;          // threads of launches 1 to 3
 constexpr int kFinishT = 1024;   // threads of launch 4
-constexpr int kBins = 1024;      // of 1/32 each; the last one holds all that is further below
-constexpr float kBinsPerUnit = 32.0f;
+constexpr int kBins = 1024;      // of 3 steps of 2^(-1/64) each; the last one holds all that is further below
 constexpr uint32_t kListMax = 2048;
 constexpr int kChunkMin = 4 * kT;
 constexpr int kChunksMax = TERN_SAMPLE_MAX_N / kChunkMin;
 constexpr double kFix = 17592186044416.0;  // 2^44
-static_assert((kBins - 1) / kBinsPerUnit > 31.9f, "the last bin's weights round to 0: 2^44 e^-31.9 < 1/2");
+static_assert((kBins - 1) * 3 / 64.0 - 1 / 128.0 > 47, "the last bin's weights round to 0: 2^44 2^-47 < 1/2");
 
 // 2^(-j / 64)
 __constant__ double kExp2[64] = {
@@ -123,23 +122,78 @@ struct Row {
   u64 top;        // key and complement of the index of the first token (0: none)
   uint32_t live;  // tokens that can be drawn
   uint32_t k;     // tokens of top-k (live: no limit)
-  float mx, bin_scale, u;
+  float mx, u;
   bool greedy;
 };
 
+// v of the lane that the DPP control names (0 where there is none, or where
+// the row mask leaves it out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 dpp64(u64 v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return ((u64)hi << 32) | lo;
+}
+// Inclusive prefix over 16 lanes (row_shr 1, 2, 4, 8), and over the wave
+// (row_bcast 15 and 31 after that).
+__device__ __forceinline__ u64 row_scan(u64 v) {
+  v += dpp64<0x111, 0xF>(v);
+  v += dpp64<0x112, 0xF>(v);
+  v += dpp64<0x114, 0xF>(v);
+  return v + dpp64<0x118, 0xF>(v);
+}
+__device__ __forceinline__ u64 wave_scan(u64 v) {
+  v = row_scan(v);
+  v += dpp64<0x142, 0xA>(v);
+  return v + dpp64<0x143, 0xC>(v);
+}
+__device__ __forceinline__ u64 lane64(u64 v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((u64)hi << 32) | lo;
+}
+
+// Exclusive prefixes over the workgroup of a and b (thread order), and their
+// totals; `wave` holds 32 words.  Every wave scans the waves' totals itself,
+// one per lane: read one after the other by all the threads, they had cost
+// most of the scan.
+template <int T>
+__device__ __forceinline__ void wg_scan2(u64& a, u64& b, u64* wave, u64& ta, u64& tb) {
+  constexpr int W = T / 64;
+  static_assert(W <= 16, "the waves' totals fit a DPP row");
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const u64 sa = wave_scan(a), sb = wave_scan(b);
+  __syncthreads();  // (the words' last readers are past them)
+  if (lane == 63) wave[w] = sa, wave[16 + w] = sb;
+  __syncthreads();
+  const u64 va = row_scan(lane < W ? wave[lane] : 0), vb = row_scan(lane < W ? wave[16 + lane] : 0);
+  ta = lane64(va, W - 1);
+  tb = lane64(vb, W - 1);
+  a = sa - a + (w ? lane64(va, w - 1) : 0);
+  b = sb - b + (w ? lane64(vb, w - 1) : 0);
+}
+template <int T>
+__device__ __forceinline__ u64 wg_scan(u64 v, u64* wave, u64& total) {
+  u64 none = 0, none_total;
+  wg_scan2<T>(v, none, wave, total, none_total);
+  return v;
+}
+
 // The row's parameters, its largest logit and live tokens from the chunks of
-// launch 1 (the same on every thread; `lds` holds 2 T / 64 words).
+// launch 1 (the same on every thread; `lds` holds 32 words).
 template <int T>
 __device__ Row load_row(const Launch& L, const RowWs& w, int64_t row, u64* lds) {
   const SampleArgs& a = L.a;
-  Row r;
-  r.x = a.x + row * a.ldx;
+  // (every load before the first barrier: one trip to memory)
+  const float t = load_g(a.temperature + row), u = load_g(a.u + row);
+  const int32_t k = a.top_k ? load_g(a.top_k + row) : 0;
+  const float tp = a.top_p ? load_g(a.top_p + row) : 1.0f, mp = a.min_p ? load_g(a.min_p + row) : 0.0f;
   u64 top = 0;
   uint32_t live = 0;
   for (int c = threadIdx.x; c < L.chunks; c += T) {
     const u64 v = load_g(w.chunk_top + c);
-    top = v > top ? v : top;
     live += load_g(w.chunk_live + c);
+    top = v > top ? v : top;
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
@@ -147,102 +201,116 @@ __device__ Row load_row(const Launch& L, const RowWs& w, int64_t row, u64* lds) 
     top = o > top ? o : top;
     live += __shfl_xor(live, d, 64);
   }
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top, lds[T / 64 + (threadIdx.x >> 6)] = live;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top, lds[16 + (threadIdx.x >> 6)] = live;
   __syncthreads();
-  live = 0;
-  for (int i = 0; i < T / 64; ++i) {
-    top = lds[i] > top ? lds[i] : top;
-    live += (uint32_t)lds[T / 64 + i];
+  const int lane = threadIdx.x & 63;
+  top = lane < T / 64 ? lds[lane] : 0;
+  live = lane < T / 64 ? (uint32_t)lds[16 + lane] : 0;
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) {
+    const u64 o = __shfl_xor(top, d, 64);
+    top = o > top ? o : top;
+    live += __shfl_xor(live, d, 64);
   }
-  __syncthreads();
-  const float t = load_g(a.temperature + row);
-  const int32_t k = a.top_k ? load_g(a.top_k + row) : 0;
-  const float tp = a.top_p ? load_g(a.top_p + row) : 1.0f, mp = a.min_p ? load_g(a.min_p + row) : 0.0f;
+  top = lane64(top, 0);
+  live = (uint32_t)__builtin_amdgcn_readlane((int)live, 0);
+  Row r;
+  r.x = a.x + row * a.ldx;
   r.top = top;
   r.live = live;
   r.mx = key_logit((uint32_t)(top >> 32));
   r.greedy = !(t > 0.0f);
   r.inv_t = 1.0 / (double)t;
-  r.bin_scale = (float)(r.inv_t * (double)kBinsPerUnit);
-  r.u = load_g(a.u + row);
+  r.u = u;
   r.k = k > 0 && (uint32_t)k < live ? (uint32_t)k : live;
   r.top_p = tp < 1.0f ? (double)fmaxf(tp, 0.0f) : 1.0;  // (a NaN is no filter)
   r.min_p = mp > 0.0f ? (double)fminf(mp, 1.0f) : 0.0;
   return r;
 }
 
-// e^((x - max) / T) in fp64: with v = (max - x) / T = k ln 2 / 64 + s, the
-// table's 2^(-(k % 64) / 64), the Taylor series of e^-s through s^4 (|s| <=
-// 0.0055: its next term is 4e-14) and a power of two.
-__device__ __forceinline__ double weight_of(const Row& r, const double* tab, float x) {
-  if (x == r.mx) return 1.0;  // (also where both are +inf)
+// With v = (max - x) / T in fp64: k = rint(v 64 / ln 2), s = k ln 2 / 64 - v;
+// k is monotone in x and gives the bin (three of its steps each).
+struct Reduced {
+  double s;
+  int k;
+};
+constexpr int kLastStep = 3 * (kBins - 1);
+__device__ __forceinline__ Reduced reduce(const Row& r, float x) {
   constexpr double kStep = 0x1.62e42fefa39efp-7, kPerUnit = 0x1.71547652b82fep+6;  // ln 2 / 64 and its inverse
-  const double v = ((double)r.mx - (double)x) * r.inv_t;
-  if (!(v < 700.0)) return 0.0;
+  // (equal also where both are +inf; a NaN, from T = inf, counts as far below)
+  const double v = x == r.mx ? 0.0 : fmin(((double)r.mx - (double)x) * r.inv_t, 700.0);
   const double k = __builtin_rint(v * kPerUnit);
-  const double s = __builtin_fma(k, kStep, -v);
+  return {__builtin_fma(k, kStep, -v), (int)k};
+}
+__device__ __forceinline__ int bin_of(const Reduced& d) { return (int)((uint32_t)min(d.k, kLastStep) * 21846u >> 16); }
+static_assert((kLastStep * 21846u >> 16) == kBins - 1 && ((kLastStep - 1) * 21846u >> 16) == kBins - 2, "k / 3");
+// e^-v: the table's 2^(-(k % 64) / 64), the Taylor series of e^s through s^4
+// (|s| <= 0.0055: its next term is 4e-14) and a power of two.
+__device__ __forceinline__ double weight_of(const Reduced& d, const double* tab) {
+  const double s = d.s;
   double p = 1.0 / 24.0;
   p = __builtin_fma(p, s, 1.0 / 6.0);
   p = __builtin_fma(p, s, 0.5);
   p = __builtin_fma(p, s, 1.0);
   p = __builtin_fma(p, s, 1.0);
-  const int ki = (int)k;
-  return __builtin_ldexp(p * tab[ki & 63], -(ki >> 6));
+  return __builtin_ldexp(p * tab[d.k & 63], -(d.k >> 6));
+}
+__device__ __forceinline__ double weight_of(const Row& r, const double* tab, float x) {
+  return weight_of(reduce(r, x), tab);
 }
 // w in units of 2^-44, w <= 1: the mantissa of w 2^44 + 2^52
 __device__ __forceinline__ u64 fixed(double w) {
   return __builtin_bit_cast(u64, __builtin_fma(w, kFix, 4503599627370496.0)) & 0xfffffffffffffull;
 }
 
-__device__ __forceinline__ int bin_of(const Row& r, float x) {
-  if (x == r.mx) return 0;
-  return (int)fminf((r.mx - x) * r.bin_scale, (float)(kBins - 1));  // (a NaN, from T = inf: the last bin)
-}
-
-// fn(index, logit) for the tokens [j0, j1) of a row, four consecutive ones
-// per thread and step.
-template <int T, typename Fn>
-__device__ __forceinline__ void each_token(const float* x, int j0, int j1, bool vec, Fn fn) {
-  for (int j = j0 + 4 * (int)threadIdx.x; j < j1; j += 4 * T) {
-    float v[4];
-    if (vec && j + 4 <= j1) {
-      const f32x4 g = __builtin_bit_cast(f32x4, load16(x + j));
+// U groups of four consecutive tokens per thread, all loaded at once: tokens
+// j, ..., j + 4 T U - 1 of a row (-infinity, which no one counts, from j1 on).
+template <int T, int U>
+struct Tile {
+  float v[U][4];
+  __device__ __forceinline__ static int at(int j, int u) { return j + 4 * ((int)threadIdx.x + T * u); }
+  __device__ __forceinline__ void load(const float* x, int j, int j1, bool vec) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = g[i];
+    for (int u = 0; u < U; ++u) {
+      const int k = at(j, u);
+      if (vec && k + 4 <= j1) {
+        const f32x4 g = __builtin_bit_cast(f32x4, load16(x + k));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fn(j + i, v[i]);
-    } else {
+        for (int i = 0; i < 4; ++i) v[u][i] = g[i];
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j + i < j1) fn(j + i, load_g(x + j + i));
+        for (int i = 0; i < 4; ++i) v[u][i] = k + i < j1 ? load_g(x + k + i) : -__builtin_inff();
+      }
     }
   }
+  // fn(index, logit) for each
+  template <typename Fn>
+  __device__ __forceinline__ void each(int j, Fn fn) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fn(at(j, u) + i, v[u][i]);
+  }
+};
+
+// fn(index, logit) for the tokens [j0, j1) of a row; the first tile is
+// already loaded.
+template <int T, int U, typename Fn>
+__device__ __forceinline__ void each_token(Tile<T, U>& tile, const float* x, int j0, int j1, bool vec, Fn fn) {
+  for (int j = j0; j < j1;) {
+    tile.each(j, fn);
+    j += 4 * T * U;
+    if (j < j1) tile.load(x, j, j1, vec);
+  }
+}
+template <int T, typename Fn>
+__device__ __forceinline__ void each_token(const float* x, int j0, int j1, bool vec, Fn fn) {
+  Tile<T, 1> tile;
+  tile.load(x, j0, j1, vec);
+  each_token<T, 1>(tile, x, j0, j1, vec, fn);
 }
 
 __device__ __forceinline__ u64 pack_token(uint32_t key, int j) { return ((u64)key << 32) | (uint32_t)~(uint32_t)j; }
-
-// Exclusive prefix over the workgroup of v (thread order), and the total;
-// `wave` holds T / 64 words.
-template <int T>
-__device__ __forceinline__ u64 wg_scan(u64 v, u64* wave, u64& total) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  u64 s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const u64 o = __shfl_up(s, d, 64);
-    if (lane >= d) s += o;
-  }
-  __syncthreads();
-  if (lane == 63) wave[w] = s;
-  __syncthreads();
-  u64 before = 0;
-  total = 0;
-  for (int i = 0; i < T / 64; ++i) {
-    if (i < w) before += wave[i];
-    total += wave[i];
-  }
-  return before + s - v;
-}
 
 // Units of weight that the forerunners of a token kept by top-p stay below:
 // forerunners < top_p * total, at least one (the first token always).
@@ -255,22 +323,26 @@ __device__ __forceinline__ u64 mass_limit(double top_p, u64 total) {
 
 // ------------------------------------------------------ launch 1: maxima --
 
+template <int U>
 __global__ __launch_bounds__(kT) void top_kernel(Launch L) {
   __shared__ u64 tops[kT / 64];
   __shared__ uint32_t lives[kT / 64];
   const int c = blockIdx.x % L.chunks;
   const int64_t row = blockIdx.x / L.chunks;
   const RowWs w = row_ws(L, row);
+  const float* x = L.a.x + row * L.a.ldx;
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  Tile<kT, U> tile;
+  tile.load(x, j0, j1, L.vec);
   // the row's histogram and list start empty, its chunks clearing a share each
   for (int i = c * kT + threadIdx.x; i < kBins; i += L.chunks * kT) {
     store_g(w.mass + i, (u64)0);
     store_g(w.count + i, 0u);
   }
   if (c == 0 && threadIdx.x == 0) store_g(w.list_n, 0u);
-  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
   u64 top = 0;
   uint32_t live = 0;
-  each_token<kT>(L.a.x + row * L.a.ldx, j0, j1, L.vec, [&](int j, float x) {
+  each_token<kT, U>(tile, x, j0, j1, L.vec, [&](int j, float x) {
     const uint32_t k = logit_key(x);
     if (!k) return;
     ++live;
@@ -299,31 +371,35 @@ __global__ __launch_bounds__(kT) void top_kernel(Launch L) {
 
 __device__ __forceinline__ bool wants_bins(const Row& r) { return r.k < r.live || r.top_p < 1.0; }
 
+template <int U>
 __global__ __launch_bounds__(kT) void histogram_kernel(Launch L) {
   __shared__ u64 mass[kBins];
   __shared__ uint32_t count[kBins];
   __shared__ double tab[64];
-  __shared__ u64 red[2 * kT / 64];
+  __shared__ u64 red[32];
   const int c = blockIdx.x % L.chunks;
   const int64_t row = blockIdx.x / L.chunks;
   const RowWs w = row_ws(L, row);
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  Tile<kT, U> tile;
+  tile.load(L.a.x + row * L.a.ldx, j0, j1, L.vec);
   const Row r = load_row<kT>(L, w, row, red);
   if (r.greedy || r.live == 0 || !wants_bins(r)) return;
   if (threadIdx.x < 64) tab[threadIdx.x] = kExp2[threadIdx.x];
   for (int i = threadIdx.x; i < kBins; i += kT) mass[i] = 0, count[i] = 0;
   __syncthreads();
-  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
   const bool weigh = r.top_p < 1.0;
   uint32_t rest = 0;  // the last bin: no weight, and too many tokens for one counter
-  each_token<kT>(r.x, j0, j1, L.vec, [&](int, float x) {
-    if (!logit_key(x)) return;
-    const int b = bin_of(r, x);
+  each_token<kT, U>(tile, r.x, j0, j1, L.vec, [&](int, float x) {
+    if (!(x > -__builtin_inff())) return;
+    const Reduced d = reduce(r, x);
+    const int b = bin_of(d);
     if (b == kBins - 1) {
       ++rest;
       return;
     }
     atomicAdd(&count[b], 1u);
-    if (weigh) atomicAdd(&mass[b], fixed(weight_of(r, tab, x)));
+    if (weigh) atomicAdd(&mass[b], fixed(weight_of(d, tab)));
   });
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) rest += __shfl_xor(rest, d, 64);
@@ -349,7 +425,7 @@ struct Cut {
 };
 
 struct CutLds {
-  u64 wave[16];
+  u64 wave[32];
   int kb;
   uint32_t kbefore, kcount;
   u64 kmass, kbin_mass;
@@ -357,8 +433,26 @@ struct CutLds {
   u64 pm[2];
 };
 
+// A thread's bins, loaded before anything waits.
 template <int T>
-__device__ Cut find_cut(const Row& r, const RowWs& w, CutLds& S) {
+struct Bins {
+  uint32_t n[kBins / T];
+  u64 m[kBins / T];
+};
+template <int T>
+__device__ __forceinline__ Bins<T> load_bins(const Launch& L, const RowWs& w) {
+  constexpr int V = kBins / T;
+  Bins<T> b;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    b.n[i] = L.a.top_k || L.a.top_p ? load_g(w.count + V * threadIdx.x + i) : 0;
+    b.m[i] = L.a.top_p ? load_g(w.mass + V * threadIdx.x + i) : 0;
+  }
+  return b;
+}
+
+template <int T>
+__device__ Cut find_cut(const Row& r, const Bins<T>& bins, CutLds& S) {
   constexpr int V = kBins / T;
   Cut c;
   c.sure = kBins;
@@ -367,24 +461,17 @@ __device__ Cut find_cut(const Row& r, const RowWs& w, CutLds& S) {
   c.kneed = c.rest_kept = 0;
   c.mass_p1 = c.mass_k = 0;
   if (!wants_bins(r)) return c;
-  uint32_t n[V];
-  u64 m[V], nsum = 0, msum = 0, all;
+  const uint32_t* n = bins.n;
+  const u64* m = bins.m;
+  u64 nb = 0, mb0 = 0, all, total;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    n[i] = load_g(w.count + V * threadIdx.x + i);
-    m[i] = r.top_p < 1.0 ? load_g(w.mass + V * threadIdx.x + i) : 0;
-    nsum += n[i], msum += m[i];
-  }
-  u64 nb = wg_scan<T>(nsum, S.wave, all);
-  u64 total;
-  const u64 mb0 = wg_scan<T>(msum, S.wave, total);
-  // the bin that the k-th token lies in
-  if (threadIdx.x == 0) S.kb = kBins;
-  __syncthreads();
+  for (int i = 0; i < V; ++i) nb += n[i], mb0 += m[i];
+  wg_scan2<T>(nb, mb0, S.wave, all, total);
+  // the bin that the k-th token lies in (there is one: 1 <= k <= live)
   u64 mb = mb0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (nb < r.k && nb + n[i] >= r.k) {  // (one bin at most; r.k >= 1)
+    if (nb < r.k && nb + n[i] >= r.k) {
       S.kb = V * (int)threadIdx.x + i;
       S.kbefore = (uint32_t)nb, S.kcount = n[i];
       S.kmass = mb, S.kbin_mass = m[i];
@@ -405,13 +492,12 @@ __device__ Cut find_cut(const Row& r, const RowWs& w, CutLds& S) {
   } else {
     c.mass_k = z_lo = z_hi = S.kmass + S.kbin_mass;
     c.sure = kb < kBins - 1 ? kb + 1 : kBins - 1;
-    // (a min-p above the last bin's weights, e^-31.9 at most, keeps none of its tokens)
-    if (kb == kBins - 1 && !(r.min_p > 1.5e-14)) c.rest_kept = need;
+    // (a min-p above the last bin's weights, 2^-47 at most, keeps none of its tokens)
+    if (kb == kBins - 1 && !(r.min_p > 1e-14)) c.rest_kept = need;
   }
   if (r.top_p < 1.0) {
     const u64 lim[2] = {mass_limit(r.top_p, z_lo), mass_limit(r.top_p, z_hi)};
     u64 before = mb0;
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -428,7 +514,6 @@ __device__ Cut find_cut(const Row& r, const RowWs& w, CutLds& S) {
     c.sure = c.p1;
     c.rest_kept = 0;
   }
-  __syncthreads();
   return c;
 }
 
@@ -436,39 +521,41 @@ __device__ __forceinline__ bool listed(const Cut& c, int b) { return (b >= c.p1 
 
 // ------------------------------------- launch 3: listed tokens and sums --
 
+template <int U>
 __global__ __launch_bounds__(kT) void gather_kernel(Launch L) {
   __shared__ double tab[64];
-  __shared__ u64 red[2 * kT / 64];
+  __shared__ u64 red[32];
   __shared__ CutLds S;
   const int c = blockIdx.x % L.chunks;
   const int64_t row = blockIdx.x / L.chunks;
   const RowWs w = row_ws(L, row);
+  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
+  Tile<kT, U> tile;
+  tile.load(L.a.x + row * L.a.ldx, j0, j1, L.vec);
+  const Bins<kT> bins = load_bins<kT>(L, w);
   const Row r = load_row<kT>(L, w, row, red);
   if (r.greedy || r.live == 0) return;
   if (threadIdx.x < 64) tab[threadIdx.x] = kExp2[threadIdx.x];
   __syncthreads();
-  const Cut cut = find_cut<kT>(r, w, S);
-  const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, L.a.N);
-  const uint32_t top_key = (uint32_t)(r.top >> 32);
+  const Cut cut = find_cut<kT>(r, bins, S);
   u64 sum = 0, kept = 0;
-  each_token<kT>(r.x, j0, j1, L.vec, [&](int j, float x) {
-    const uint32_t key = logit_key(x);
-    if (!key) return;
-    const int b = bin_of(r, x);
+  each_token<kT, U>(tile, r.x, j0, j1, L.vec, [&](int j, float x) {
+    if (!(x > -__builtin_inff())) return;
+    const Reduced d = reduce(r, x);
+    const int b = bin_of(d);
     if (b < cut.sure) {
-      const double wt = weight_of(r, tab, x);
-      if (wt >= r.min_p || key == top_key) {
+      const double wt = weight_of(d, tab);
+      if (wt >= r.min_p) {  // (the largest logit's weight is 1)
         sum += fixed(wt);
         ++kept;
       }
     } else if (listed(cut, b)) {
       const uint32_t at = atomicAdd(w.list_n, 1u);
-      if (at < kListMax) store_g(w.list + at, pack_token(key, j));
+      if (at < kListMax) store_g(w.list + at, pack_token(logit_key(x), j));
     }
   });
   u64 total, n;
-  wg_scan<kT>(sum, S.wave, total);
-  wg_scan<kT>(kept, S.wave, n);
+  wg_scan2<kT>(sum, kept, S.wave, total, n);
   if (threadIdx.x == 0) {
     store_g(w.chunk_mass + c, total);
     store_g(w.chunk_kept + c, (uint32_t)n);
@@ -486,7 +573,7 @@ struct Keep {
 
 struct FinishLds {
   double tab[64];
-  u64 red[2 * kFinishT / 64];
+  u64 red[32];
   CutLds cut;
   u64 mass[256];
   uint32_t count[256];
@@ -593,7 +680,7 @@ __device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLd
       const uint32_t k = logit_key(x);
       if (!k || pack_token(k, j) < keep.border) return;
       const double wt = weight_of(r, F.tab, x);
-      if (wt >= r.min_p || k == (uint32_t)(r.top >> 32)) sum += fixed(wt), ++kept;
+      if (wt >= r.min_p) sum += fixed(wt), ++kept;
     });
     u64 total, n;
     wg_scan<kFinishT>(sum, F.red, total);
@@ -610,10 +697,21 @@ __device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLd
 __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
   __shared__ u64 cmass[kChunksMax];  // a chunk's kept weight, that of its listed tokens included
   __shared__ FinishLds F;
+  static_assert(kChunksMax <= kFinishT && kListMax == 2 * kFinishT, "a chunk and two listed tokens per thread");
   const SampleArgs& a = L.a;
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x;
   const RowWs w = row_ws(L, row);
+  // everything that the earlier launches left, loaded before anything waits
+  const bool cuts = a.top_k || a.top_p;
+  const Bins<kFinishT> bins = load_bins<kFinishT>(L, w);
+  const uint32_t list_n = cuts ? load_g(w.list_n) : 0;
+  u64 tok[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) tok[e] = cuts ? load_g(w.list + t + e * kFinishT) : 0;
+  u64 chunk_mass = t < L.chunks ? load_g(w.chunk_mass + t) : 0;
+  u64 kept = t < L.chunks ? load_g(w.chunk_kept + t) : 0;
+  if (t < 64) F.tab[t] = kExp2[t];
   const Row r = load_row<kFinishT>(L, w, row, F.red);
   if (r.greedy || r.live == 0) {
     if (t == 0) {
@@ -623,115 +721,100 @@ __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
     }
     return;
   }
-  if (t < 64) F.tab[t] = kExp2[t];
-  __syncthreads();
-  const Cut cut = find_cut<kFinishT>(r, w, F.cut);
-  const uint32_t top_key = (uint32_t)(r.top >> 32);
-  auto passes = [&](float x, uint32_t key, double& wt) {
-    wt = weight_of(r, F.tab, x);
-    return wt >= r.min_p || key == top_key;
-  };
+  const Cut cut = find_cut<kFinishT>(r, bins, F.cut);
   Keep keep = {~0ull, cut.sure};
-  u64 list_kept = 0;
-  const uint32_t nl = wants_bins(r) ? load_g(w.list_n) : 0;
+  const uint32_t nl = wants_bins(r) ? list_n : 0;
   // (a minimum below the last bin's weights would have to look into it)
   const bool slow = nl > kListMax || (cut.rest_kept && r.min_p > 0.0);
   if (slow) {
-    keep = slow_cut(L, w, r, F);
-    for (int c = t; c < L.chunks; c += kFinishT) cmass[c] = load_g(w.chunk_mass + c);
     __syncthreads();
-  } else {
-    for (int c = t; c < L.chunks; c += kFinishT) cmass[c] = load_g(w.chunk_mass + c);
-    const int n = (int)nl;
-    if (n) {
-      // order: each token's rank is the number of listed tokens before it,
-      // counted by as many threads as there are for a token
-      for (int i = t; i < n; i += kFinishT) F.tok[i] = load_g(w.list + i), F.rank[i] = 0;
-      __syncthreads();
-      int share = 1;
-      while (2 * share * n <= kFinishT) share *= 2;
-      for (int i = t; i < n * share; i += kFinishT) {
-        const int e = i / share;
-        const u64 me = F.tok[e];
-        uint32_t before = 0;
-        for (int o = i % share; o < n; o += share) before += F.tok[o] > me;
-        if (before) atomicAdd(&F.rank[e], before);
-      }
-      __syncthreads();
-      for (int i = t; i < n; i += kFinishT) F.sorted[F.rank[i]] = F.tok[i];
-      __syncthreads();
-      // weights before each of them, two per thread; tokens before bin kbin
-      u64 wt[2], sum = 0, before_k = 0, in_p = 0, all, nk, np;
+    keep = slow_cut(L, w, r, F);
+    chunk_mass = t < L.chunks ? load_g(w.chunk_mass + t) : 0;
+    kept = t < L.chunks ? load_g(w.chunk_kept + t) : 0;
+  } else if (t == 0) {
+    kept += cut.rest_kept;
+  }
+  if (t < L.chunks) cmass[t] = chunk_mass;
+  const int n = slow ? 0 : (int)nl;
+  if (n) {
+    // order: each token's rank is the number of listed tokens before it,
+    // counted by as many threads as there are for a token
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * t + e;
-        wt[e] = 0;
-        if (i < n) {
-          const float x = key_logit((uint32_t)(F.sorted[i] >> 32));
-          const int b = bin_of(r, x);
-          wt[e] = fixed(weight_of(r, F.tab, x));
-          before_k += b < cut.kbin;
-          in_p += b <= cut.p2;
-        }
-        sum += wt[e];
-      }
-      u64 before = wg_scan<kFinishT>(sum, F.red, all);
-      wg_scan<kFinishT>(before_k, F.red, nk);
-      wg_scan<kFinishT>(in_p, F.red, np);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * t + e <= n) F.prefix[2 * t + e] = before;
-        before += wt[e];
-      }
-      if (t == 0 && n == (int)kListMax) F.prefix[n] = all;
-      __syncthreads();
-      const int kend = cut.kbin < kBins ? (int)nk + (int)cut.kneed : n;  // listed tokens among the first k
-      int end = kend;
-      if (r.top_p < 1.0) {
-        const u64 z = cut.kbin < kBins ? cut.mass_k + F.prefix[kend] - F.prefix[nk] : cut.mass_k;
-        const u64 lim = mass_limit(r.top_p, z);
-        u64 in = 0, kept;
-        for (int i = t; i < min((int)np, kend); i += kFinishT) in += cut.mass_p1 + F.prefix[i] < lim;
-        wg_scan<kFinishT>(in, F.red, kept);
-        end = (int)kept;
-      }
-      if (end > 0) keep.border = F.sorted[end - 1];
-      u64 mine = 0;
-      for (int i = t; i < end; i += kFinishT) {
-        const uint32_t key = (uint32_t)(F.sorted[i] >> 32);
-        double wd;
-        if (!passes(key_logit(key), key, wd)) continue;
-        ++mine;
-        atomicAdd(&cmass[~(uint32_t)F.sorted[i] / (uint32_t)L.per], fixed(wd));
-      }
-      wg_scan<kFinishT>(mine, F.red, list_kept);
+    for (int e = 0; e < 2; ++e)
+      if (t + e * kFinishT < n) F.tok[t + e * kFinishT] = tok[e], F.rank[t + e * kFinishT] = 0;
+    __syncthreads();
+    int log_share = 0;
+    while ((2 << log_share) * n <= kFinishT) ++log_share;
+    const int share = 1 << log_share;
+    for (int i = t; i < n << log_share; i += kFinishT) {
+      const int e = i >> log_share;
+      const u64 me = F.tok[e];
+      uint32_t before = 0;
+#pragma unroll 4
+      for (int o = i & (share - 1); o < n; o += share) before += F.tok[o] > me;
+      if (before) atomicAdd(&F.rank[e], before);
     }
     __syncthreads();
+    for (int i = t; i < n; i += kFinishT) F.sorted[F.rank[i]] = F.tok[i];
+    __syncthreads();
+    // weights before each of them, two per thread; tokens before bin kbin, and in the bins of top-p
+    u64 wt[2], before = 0, counts = 0, all, all_counts;
+    double wd[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      wt[e] = 0;
+      wd[e] = 0.0;
+      if (2 * t + e < n) {
+        const Reduced d = reduce(r, key_logit((uint32_t)(F.sorted[2 * t + e] >> 32)));
+        const int b = bin_of(d);
+        wd[e] = weight_of(d, F.tab);
+        wt[e] = fixed(wd[e]);
+        counts += (b < cut.kbin ? 1ull : 0ull) | (b <= cut.p2 ? 1ull << 32 : 0ull);
+      }
+      before += wt[e];
+    }
+    wg_scan2<kFinishT>(before, counts, F.red, all, all_counts);
+    const int nk = (int)(uint32_t)all_counts, np = (int)(all_counts >> 32);
+    // (positions 2 t and 2 t + 1, and the total behind the last)
+    if (2 * t <= n) F.prefix[2 * t] = before;
+    if (2 * t + 1 <= n) F.prefix[2 * t + 1] = before + wt[0];
+    if (2 * t + 2 == n) F.prefix[n] = all;
+    __syncthreads();
+    const int kend = cut.kbin < kBins ? nk + (int)cut.kneed : n;  // listed tokens among the first k
+    int end = kend;
+    if (r.top_p < 1.0) {
+      const u64 z = cut.kbin < kBins ? cut.mass_k + F.prefix[kend] - F.prefix[nk] : cut.mass_k;
+      const u64 lim = mass_limit(r.top_p, z);
+      const int most = min(np, kend);
+      if (t == 0) F.out32[0] = 0;
+      __syncthreads();
+      // (forerunners grow along the order: one last token is inside)
+      for (int i = t; i < most; i += kFinishT)
+        if (cut.mass_p1 + F.prefix[i] < lim && (i + 1 == most || cut.mass_p1 + F.prefix[i + 1] >= lim)) F.out32[0] = i + 1;
+      __syncthreads();
+      end = (int)F.out32[0];
+    }
+    if (end > 0) keep.border = F.sorted[end - 1];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * t + e >= end || wd[e] < r.min_p) continue;
+      ++kept;
+      atomicAdd(&cmass[~(uint32_t)F.sorted[2 * t + e] / (uint32_t)L.per], wt[e]);
+    }
   }
+  __syncthreads();
 
   // the chunk that u * total falls in
-  const int per_t = (L.chunks + kFinishT - 1) / kFinishT;
-  u64 sum = 0, kept = 0, total, nkept;
-  for (int c = t * per_t; c < min(L.chunks, (t + 1) * per_t); ++c) {
-    sum += cmass[c];
-    kept += load_g(w.chunk_kept + c);
-  }
-  u64 before = wg_scan<kFinishT>(sum, F.red, total);
-  wg_scan<kFinishT>(kept, F.red, nkept);
-  nkept += list_kept + (slow ? 0 : cut.rest_kept);
+  const u64 sum = t < L.chunks ? cmass[t] : 0;
+  u64 before = sum, total, nkept;
+  wg_scan2<kFinishT>(before, kept, F.red, total, nkept);
   const double u = r.u > 0.0f ? fmin((double)r.u, 1.0) : 0.0;
   u64 target = (u64)(u * (double)total);
   if (target >= total) target = total - 1;
-  if (before <= target && target < before + sum) {  // one thread
-    int c = t * per_t;
-    while (before + cmass[c] <= target) before += cmass[c++];
-    F.out32[0] = (uint32_t)c;
-    F.out64 = before;
-  }
+  if (before <= target && target < before + sum) F.out32[0] = (uint32_t)t, F.out64 = before;  // one thread
   __syncthreads();
   const int c = (int)F.out32[0];
   before = F.out64;
-  __syncthreads();
 
   // and the token in that chunk
   const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, a.N);
@@ -740,23 +823,22 @@ __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
     float x[4];
     u64 wt[4], run = 0, all;
 #pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = me + i < j1 ? load_g(r.x + me + i) : -__builtin_inff();
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       wt[i] = 0;
-      x[i] = 0.0f;
-      if (me + i < j1) {
-        x[i] = load_g(r.x + me + i);
-        const uint32_t key = logit_key(x[i]);
-        double wd;
-        if (key && (bin_of(r, x[i]) < keep.sure || pack_token(key, me + i) >= keep.border) && passes(x[i], key, wd))
-          wt[i] = fixed(wd);
+      const uint32_t key = logit_key(x[i]);
+      if (key) {
+        const Reduced d = reduce(r, x[i]);
+        const double wd = weight_of(d, F.tab);
+        if ((bin_of(d) < keep.sure || pack_token(key, me + i) >= keep.border) && wd >= r.min_p) wt[i] = fixed(wd);
       }
       run += wt[i];
     }
-    const u64 at = before + wg_scan<kFinishT>(run, F.red, all);
+    u64 at = wg_scan<kFinishT>(run, F.red, all) + before;
     if (at <= target && target < at + run) {  // one thread of one step
-      u64 s = at;
       int i = 0;
-      while (s + wt[i] <= target) s += wt[i++];
+      while (at + wt[i] <= target) at += wt[i++];
       store_g(a.token + row, me + i);
       if (a.prob) store_g(a.prob + row, (float)(weight_of(r, F.tab, x[i]) * kFix / (double)total));
       if (a.kept) store_g(a.kept + row, (int32_t)nkept);
@@ -772,6 +854,13 @@ int64_t tokens_per_chunk(int64_t M, int64_t N) {
   int64_t per = kChunkMin;
   while (per < 16384 && M * ((N + per - 1) / per) > 2048) per *= 2;
   return per;
+}
+
+template <int U>
+void launch_chunks(const Launch& L, dim3 grid, hipStream_t s) {
+  hipLaunchKernelGGL(top_kernel<U>, grid, dim3(kT), 0, s, L);
+  if (L.a.top_k || L.a.top_p) hipLaunchKernelGGL(histogram_kernel<U>, grid, dim3(kT), 0, s, L);
+  hipLaunchKernelGGL(gather_kernel<U>, grid, dim3(kT), 0, s, L);
 }
 
 }  // namespace
@@ -794,9 +883,10 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   L.row_bytes = row_ws_bytes(L.chunks);
   L.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M == 1 || a.ldx % 4 == 0);
   const dim3 grid((unsigned)(a.M * L.chunks));
-  hipLaunchKernelGGL(top_kernel, grid, dim3(kT), 0, s, L);
-  if (a.top_k || a.top_p) hipLaunchKernelGGL(histogram_kernel, grid, dim3(kT), 0, s, L);
-  hipLaunchKernelGGL(gather_kernel, grid, dim3(kT), 0, s, L);
+  if (L.per > kChunkMin)
+    launch_chunks<4>(L, grid, s);
+  else
+    launch_chunks<1>(L, grid, s);
   hipLaunchKernelGGL(finish_kernel, dim3((unsigned)a.M), dim3(kFinishT), 0, s, L);
   return hipGetLastError();
 }
