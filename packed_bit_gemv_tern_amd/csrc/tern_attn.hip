@@ -26,6 +26,11 @@
 // dimension.  V pages are stored [dim][token] for that.  So P goes from the
 // first product to the second without leaving the lane's registers, and K
 // and V go from memory to registers by 16-byte loads, without LDS.
+//
+// Loads: a wave issues the next step's K loads once the first product has
+// read the registers, and the next V loads after the second, so 8 to 16 KB
+// per wave are always in flight.  Page ids and scales of up to kWindow
+// positions are fetched to LDS at once, out of the steps' way.
 #include <algorithm>
 
 #include "tern_cache.h"
@@ -40,6 +45,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAttnWaves = 4;
 constexpr int kStep = 64;  // positions per step of a wave
+constexpr int kWindow = 4096;  // positions whose pages are looked up at once
+constexpr int kGroups = kWindow / 16;
+static_assert(kGroups == 64 * kAttnWaves, "one group of 16 positions per thread");
 
 struct AttnArgs {
   KvArgs kv;
@@ -52,6 +60,7 @@ struct AttnArgs {
   int32_t chunk, nchunk;  // positions per chunk, chunks a sequence is split into
   int32_t row_tiles;
   float scale;
+  bool q16;  // query rows are 16-byte aligned
 };
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
@@ -102,8 +111,16 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   constexpr int KS = D / 32;  // k steps of the first product
   constexpr int DT = D / 16;  // 16-dim tiles of the output
   constexpr int LD = D + 4;
-  __shared__ float so[kAttnWaves][16 * NT][LD];
+  // the query operands (high and low halves, by lane), and after the last step the waves' sums of a tile
+  union Share {
+    f16x8 q[NT][KS][2][64];
+    float o[kAttnWaves][16][LD];
+  };
+  __shared__ Share sh;
   __shared__ float sml[kAttnWaves][16 * NT][2];
+  __shared__ float qfac[16 * NT];      // factor of a row's scores: scale * log2(e) * the row's power of two
+  __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
+  __shared__ float kscale[kGroups], vscale[kGroups];
 
   const KvArgs& kv = a.kv;
   int b = blockIdx.x;
@@ -127,39 +144,55 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
 
-  // the query rows, split
-  f16x8 qh[NT][KS], ql[NT][KS];
-  float cs[NT];     // factor of a row's scores: scale * log2(e) * the row's power of two
-  int32_t pos[NT];  // last position that the row sees (-1: none)
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    const int r = row_lo + 16 * u + n;
+  // Loads in three trips to memory: the sequence; page ids and query rows;
+  // scales, K and V.  Wave u prepares query tile u, for all the waves, while
+  // its first K and V are under way.
+  float x[D / 4];
+  if (wave < NT) {
+    const int r = row_lo + 16 * wave + n;
     const bool live = r < rows;
-    pos[u] = live ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
     const float* q = a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
                      (int64_t)(h * a.G + (live ? r % a.G : 0)) * D + g * (D / 4);
-    float x[D / 4];
+    if (a.q16) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const f32x4 v = live ? __builtin_bit_cast(f32x4, load16(q + 4 * j)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * j + i] = v[i];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 4; ++j) x[j] = live ? load_g(q + j) : 0.0f;
+    }
+  }
+  auto prepare_q = [&]() {
     float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < D / 4; ++j) {
-      x[j] = live ? load_g(q + j) : 0.0f;
-      amax = fmaxf(amax, fabsf(x[j]));
-    }
+    for (int j = 0; j < D / 4; ++j) amax = fmaxf(amax, fabsf(x[j]));
     amax = max_groups(amax);
     // 2^(8 - exponent): the largest element lands in [2^8, 2^9)
     const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
     const float up = pow2i(8 - e);
-    cs[u] = a.scale * 1.44269504088896340736f * pow2i(e - 8);
+    if (g == 0) qfac[16 * wave + n] = a.scale * 1.44269504088896340736f * pow2i(e - 8);
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
+      f16x8 qh, ql;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f16x2 hi, lo;
         split2(x[8 * j + 2 * i] * up, x[8 * j + 2 * i + 1] * up, hi, lo);
-        qh[u][j][2 * i] = hi[0], qh[u][j][2 * i + 1] = hi[1];
-        ql[u][j][2 * i] = lo[0], ql[u][j][2 * i + 1] = lo[1];
+        qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
+        ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
       }
+      sh.q[wave][j][0][lane] = qh;
+      sh.q[wave][j][1][lane] = ql;
     }
+  };
+  int32_t pos[NT];  // last position that the row sees (-1: none)
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int r = row_lo + 16 * u + n;
+    pos[u] = r < rows ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
   }
 
   f32x4 o[NT][DT];
@@ -176,182 +209,259 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   // position of the tile that every row sees: below it no mask is needed
   const int64_t all_see = min(sv.len, sv.pos0 + row_lo / a.G + 1);
   const int P = 1 << kv.log_p;
-  for (int64_t j0 = c0 + kStep * wave; j0 < c1; j0 += kStep * kAttnWaves) {
-    // pages of the K rows this lane loads (group n / 4) and of its own positions (group g)
-    const int64_t jk = j0 + 16 * (n >> 2), jv = j0 + 16 * g;
-    const int32_t idk = page_of(kv, s, jk >> kv.log_p), idv = page_of(kv, s, jv >> kv.log_p);
-    // (a group outside its sequence or its cache reads page 0 and counts for nothing)
-    const int8_t* kp = kv.k + ((((int64_t)max(idk, 0) * kv.H + h) << kv.log_p) + (jk & (P - 1))) * D + g * (D / 4);
-    const int8_t* vp = kv.v + ((((int64_t)max(idv, 0) * kv.H + h) * D + n) << kv.log_p) + (jv & (P - 1));
+  for (int64_t w0 = c0; w0 < c1; w0 += kWindow) {
+    const int64_t jg = w0 + 16 * (int)threadIdx.x;
+    const int32_t id = jg < sv.len ? page_of(kv, s, jg >> kv.log_p) : -1;
+    const int64_t si = (int64_t)max(id, 0) * kv.H + h;
+    const float ks_g = load_g(kv.k_scale + si), vs_g = load_g(kv.v_scale + si);
+    if (w0 > c0) __syncthreads();  // (the window before has been read)
+    page[threadIdx.x] = id;
+    __syncthreads();
+    const int steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
     u32x4 kw[4][D / 64], vw[DT];
+    // A step's K rows (this lane's are of group n / 4) and V rows (of its own
+    // positions, group g).  A group without a page reads page 0 and counts
+    // for nothing.
+    auto load_k = [&](int st) {
+      const int gr = 4 * st + (n >> 2);
+      const int64_t base = (((int64_t)max(page[gr], 0) * kv.H + h) << kv.log_p) + (((int)w0 + 16 * gr) & (P - 1));
+      const int8_t* kp = kv.k + (base + (n & 3)) * D + g * (D / 4);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + (4 * t + (n & 3)) * D + 16 * i);
+        for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + 4 * t * D + 16 * i);
+    };
+    auto load_v = [&](int st) {
+      const int gr = 4 * st + g;
+      const int8_t* vp = kv.v + ((((int64_t)max(page[gr], 0) * kv.H + h) * D + n) << kv.log_p) +
+                         (((int)w0 + 16 * gr) & (P - 1));
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vw[d] = load16(vp + ((int64_t)(16 * d) << kv.log_p));
-    const bool here = idv >= 0 && jv < sv.len;
-    const int64_t si = (int64_t)max(idv, 0) * kv.H + h;
-    const float ks = here ? load_g(kv.k_scale + si) : 0.0f;
-    const float vs = here ? load_g(kv.v_scale + si) : 0.0f;
+      for (int d = 0; d < DT; ++d) vw[d] = load16(vp + ((int64_t)(16 * d) << kv.log_p));
+    };
+    if (wave < steps) {
+      load_k(wave);
+      load_v(wave);
+    }
+    kscale[threadIdx.x] = id < 0 ? 0.0f : ks_g;
+    vscale[threadIdx.x] = id < 0 ? 0.0f : vs_g;
+    if (w0 == c0 && wave < NT) prepare_q();
+    __syncthreads();
 
     f32x4 sc[NT][4];
+    auto scores = [&]() {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int u = 0; u < NT; ++u) sc[u][t] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int u = 0; u < NT; ++u) sc[u][t] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const f16x8 kf = codes_f16(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
+        f16x8 qh[NT], ql[NT];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          sc[u][t] = mfma(kf, qh[u][j], sc[u][t]);
-          sc[u][t] = mfma(kf, ql[u][j], sc[u][t]);
+        for (int u = 0; u < NT; ++u) qh[u] = sh.q[u][j][0][lane], ql[u] = sh.q[u][j][1][lane];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const f16x8 kf = codes_f16(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            sc[u][t] = mfma(kf, qh[u], sc[u][t]);
+            sc[u][t] = mfma(kf, ql[u], sc[u][t]);
+          }
         }
       }
-    }
-
-    // a larger V scale: everything summed so far moves to its power of two
-    const int e_new = min((int)(__builtin_bit_cast(uint32_t, max_groups(vs)) >> 23) - 127, 120);
-    if (__builtin_amdgcn_readfirstlane(e_new) > ve) {
-      const int e = __builtin_amdgcn_readfirstlane(e_new);
-      const float f = ve - e < -126 ? 0.0f : pow2i(ve - e);
+    };
+    auto weigh_and_sum = [&](int st) {
+      const int64_t j0 = w0 + kStep * st;
+      const int32_t jv = (int32_t)j0 + 16 * g;
+      const bool here = page[4 * st + g] >= 0;
+      const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
+      // a larger V scale: everything summed so far moves to its power of two
+      const int e = __builtin_amdgcn_readfirstlane(
+          min((int)(__builtin_bit_cast(uint32_t, max_groups(vs)) >> 23) - 127, 120));
+      if (e > ve) {
+        const float f = ve - e < -126 ? 0.0f : pow2i(ve - e);
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[u][d] *= f;
-      ve = e;
-    }
-    const float vn = vs * pow2i(14 - ve > 127 ? 127 : 14 - ve);
-
-    const int32_t jv32 = (int32_t)jv;
-    const bool masked = j0 + kStep > all_see || __any(!here);
-    f16x8 ph[NT][2], pl[NT][2];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      float p[16];
-      float mx = kNegInf;
-      const float f = cs[u] * ks;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = sc[u][i >> 2][i & 3] * f;
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = here && jv32 + i <= pos[u] ? p[i] : kNegInf;
+          for (int d = 0; d < DT; ++d) o[u][d] *= f;
+        ve = e;
       }
+      const float vn = vs * pow2i(14 - ve);
+
+      const bool masked = j0 + kStep > all_see || __any(!here);
+      f16x8 ph[NT][2], pl[NT][2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, p[i]);
-      mx = max_groups(mx);
-      if (__any(mx > m[u])) {
-        const float mn = fmaxf(m[u], mx);
-        const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[u] - mn);
-        m[u] = mn;
-        l[u] *= al;
+      for (int u = 0; u < NT; ++u) {
+        float p[16];
+        float mx = kNegInf;
+        const float f = qfac[16 * u + n] * ks;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[u][d] *= al;
-      }
-      const float mu = m[u] == kNegInf ? 0.0f : m[u];
+        for (int i = 0; i < 16; ++i) p[i] = sc[u][i >> 2][i & 3] * f;
+        if (masked) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
-        l[u] += p[i];
-        p[i] *= vn;
+          for (int i = 0; i < 16; ++i) p[i] = here && jv + i <= pos[u] ? p[i] : kNegInf;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, p[i]);
+        mx = max_groups(mx);
+        if (__any(mx > m[u])) {
+          const float mn = fmaxf(m[u], mx);
+          const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[u] - mn);
+          m[u] = mn;
+          l[u] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[u][d] *= al;
+        }
+        const float mu = m[u] == kNegInf ? 0.0f : m[u];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
+          l[u] += p[i];
+          p[i] *= vn;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f16x2 hi, lo;
+            split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
+            ph[u][k][2 * i] = hi[0], ph[u][k][2 * i + 1] = hi[1];
+            pl[u][k][2 * i] = lo[0], pl[u][k][2 * i + 1] = lo[1];
+          }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f16x2 hi, lo;
-          split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
-          ph[u][k][2 * i] = hi[0], ph[u][k][2 * i + 1] = hi[1];
-          pl[u][k][2 * i] = lo[0], pl[u][k][2 * i + 1] = lo[1];
+        for (int d = 0; d < DT; ++d) {
+          const f16x8 vf = codes_f16(vw[d][2 * k], vw[d][2 * k + 1]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            o[u][d] = mfma(vf, ph[u][k], o[u][d]);
+            o[u][d] = mfma(vf, pl[u][k], o[u][d]);
+          }
         }
+    };
+    // (the last step apart: a load that may or may not have been issued would
+    // have every step wait for all of them)
+    int st = wave;
+    for (; st + kAttnWaves < steps; st += kAttnWaves) {
+      asm volatile("" ::: "memory");  // (the query operands stay in LDS: held in registers they cost a wave per SIMD)
+      scores();
+      load_k(st + kAttnWaves);
+      weigh_and_sum(st);
+      load_v(st + kAttnWaves);
     }
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const f16x8 vf = codes_f16(vw[d][2 * k], vw[d][2 * k + 1]);
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          o[u][d] = mfma(vf, ph[u][k], o[u][d]);
-          o[u][d] = mfma(vf, pl[u][k], o[u][d]);
-        }
-      }
+    if (st < steps) {
+      scores();
+      weigh_and_sum(st);
     }
   }
 
-  // join the four waves
+  // join the four waves, a tile at a time
   const float back = pow2i(max(ve - 14, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     const float lt = sum_groups(l[u]);
     if (g == 0) sml[wave][16 * u + n][0] = m[u], sml[wave][16 * u + n][1] = lt;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-      *reinterpret_cast<f32x4*>(&so[wave][16 * u + n][16 * d + 4 * g]) = o[u][d] * back;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * NT * D; i += 64 * kAttnWaves) {
-    const int r = i / D, d = i % D;
-    if (row_lo + r >= rows) break;
-    float mm = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sml[w][r][0]);
-    float ls = 0.0f, os = 0.0f;
+  for (int u = 0; u < NT; ++u) {
+    __syncthreads();  // (the operands, or the tile before, have been read)
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float f = sml[w][r][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][r][0] - mm);
-      ls = __builtin_fmaf(sml[w][r][1], f, ls);
-      os = __builtin_fmaf(so[w][r][d], f, os);
-    }
-    const int64_t row = sv.row0 + (row_lo + r) / a.G;
-    const int hq = h * a.G + (row_lo + r) % a.G;
-    if (a.nchunk == 1) {
-      store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls > 0.0f ? os / ls : 0.0f);
-    } else {
-      const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
-      store_g(a.part + at * D + d, os);
-      if (d == 0) {
-        store_g(a.part_ml + 2 * at, mm);
-        store_g(a.part_ml + 2 * at + 1, ls);
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = o[u][d] * back;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * D; i += 64 * kAttnWaves) {
+      const int r = 16 * u + i / D, d = i % D;
+      if (row_lo + r >= rows) break;
+      float mm = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sml[w][r][0]);
+      float ls = 0.0f, os = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float f = sml[w][r][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][r][0] - mm);
+        ls = __builtin_fmaf(sml[w][r][1], f, ls);
+        os = __builtin_fmaf(sh.o[w][i / D][d], f, os);
+      }
+      const int64_t row = sv.row0 + (row_lo + r) / a.G;
+      const int hq = h * a.G + (row_lo + r) % a.G;
+      if (a.nchunk == 1) {
+        store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls > 0.0f ? os / ls : 0.0f);
+      } else {
+        const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
+        store_g(a.part + at * D + d, os);
+        if (d == 0) {
+          store_g(a.part_ml + 2 * at, mm);
+          store_g(a.part_ml + 2 * at + 1, ls);
+        }
       }
     }
   }
 }
 
-// Joins the chunks of each (row, query head): one wave each.
+// Joins the chunks of each (row, query head): a workgroup of four waves each,
+// wave w the chunks w, w + 4, ...
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int hq = (int)(w % a.Hq);
-  const int64_t rest = w / a.Hq;
+__global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) {
+  __shared__ float so[kAttnWaves][D], sml[kAttnWaves][2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int hq = (int)(blockIdx.x % a.Hq);
+  const int64_t rest = blockIdx.x / a.Hq;
   const int i = (int)(rest % a.kv.max_new);
-  const int64_t s = rest / a.kv.max_new;
-  if (s >= a.kv.S) return;
-  const SeqView sv = seq_view(a.kv, (int)s);
+  const SeqView sv = seq_view(a.kv, (int)(rest / a.kv.max_new));
   if (i >= sv.n) return;
-  // chunks that wrote: those that start before the last position of the row's tile; the row's own
-  // positions lie in these
+  // chunks that hold positions of the row (their workgroups have written)
   const int64_t end = min(sv.len, sv.pos0 + i + 1);
   const int nc = (int)min((int64_t)a.nchunk, max((end + a.chunk - 1) / a.chunk, (int64_t)1));
   const int64_t row = sv.row0 + i, at = (row * a.Hq + hq) * a.nchunk;
-  float m = kNegInf;
-  for (int c = 0; c < nc; ++c) m = fmaxf(m, load_g(a.part_ml + 2 * (at + c)));
-  float l = 0.0f, o[D / 64];
+  // up to 64 of the wave's chunks at a time: a lane holds one chunk's m and l
+  float m = kNegInf, l = 0.0f, o[D / 64];
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) o[d] = 0.0f;
-  for (int c = 0; c < nc; ++c) {
-    const float mc = load_g(a.part_ml + 2 * (at + c));
-    const float f = mc == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mc - m);
-    l = __builtin_fmaf(load_g(a.part_ml + 2 * (at + c) + 1), f, l);
+  for (int b = wave; b < nc; b += 64 * kAttnWaves) {
+    const int c = b + kAttnWaves * lane;
+    const float mc = c < nc ? load_g(a.part_ml + 2 * (at + c)) : kNegInf;
+    const float lc = c < nc ? load_g(a.part_ml + 2 * (at + c) + 1) : 0.0f;
+    float mn = mc;
 #pragma unroll
-    for (int d = 0; d < D / 64; ++d) o[d] = __builtin_fmaf(load_g(a.part + (at + c) * D + lane + 64 * d), f, o[d]);
+    for (int d = 32; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor(mn, d, 64));
+    mn = fmaxf(mn, m);
+    if (mn == kNegInf) continue;  // (nothing seen yet)
+    const float al = __builtin_amdgcn_exp2f(m - mn), f = __builtin_amdgcn_exp2f(mc - mn);
+    m = mn;
+    float ls = lc * f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) ls += __shfl_xor(ls, d, 64);
+    l = __builtin_fmaf(l, al, ls);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d) o[d] *= al;
+    const int cn = min(64, (nc - b + kAttnWaves - 1) / kAttnWaves);
+#pragma unroll 4
+    for (int e = 0; e < cn; ++e) {
+      const float fe = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), e));
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d)
+        o[d] = __builtin_fmaf(load_g(a.part + (at + b + kAttnWaves * e) * D + lane + 64 * d), fe, o[d]);
+    }
   }
+  if (lane == 0) sml[wave][0] = m, sml[wave][1] = l;
 #pragma unroll
-  for (int d = 0; d < D / 64; ++d)
-    store_g(a.y + row * a.ldy + (int64_t)hq * D + lane + 64 * d, l > 0.0f ? o[d] / l : 0.0f);
+  for (int d = 0; d < D / 64; ++d) so[wave][lane + 64 * d] = o[d];
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += 64 * kAttnWaves) {
+    float mm = kNegInf, ls = 0.0f, os = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sml[w][0]);
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float f = sml[w][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - mm);
+      ls = __builtin_fmaf(sml[w][1], f, ls);
+      os = __builtin_fmaf(so[w][d], f, os);
+    }
+    store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls > 0.0f ? os / ls : 0.0f);
+  }
 }
+
+constexpr int kWgPerCu = 4;
 
 int attn_tiles_per_wave(int64_t rows) { return rows <= 16 ? 1 : 2; }
 
@@ -368,12 +478,12 @@ AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   const int64_t len = kv.max_len > 0 ? std::min(kv.max_len, most) : most;
   const int64_t units = mul_sat(kv.S * kv.H, p.row_tiles);
   const int64_t step = kStep * kAttnWaves;
-  const int64_t want = std::max<int64_t>(1, (int64_t)cus * 4 / std::max<int64_t>(1, units));
+  const int64_t want = std::max<int64_t>(1, (int64_t)cus * kWgPerCu / std::max<int64_t>(1, units));
   const int64_t chunk = std::max<int64_t>(step, ((len + want - 1) / want + step - 1) / step * step);
   p.chunk = std::min<int64_t>(chunk, 1ll << 30);
   p.nchunk = std::max<int64_t>(1, (len + p.chunk - 1) / p.chunk);
   p.work_items = mul_sat(mul_sat(units, p.nchunk), 64 * kAttnWaves);
-  p.join_items = p.nchunk > 1 ? mul_sat(mul_sat(kv.S * kv.max_new, Hq) / 4 + 1, 256) : 0;
+  p.join_items = p.nchunk > 1 ? mul_sat(mul_sat(kv.S * kv.max_new, Hq), 64 * kAttnWaves) : 0;
   p.workspace = p.nchunk > 1 ? mul_sat((int64_t)kv.rows * Hq, p.nchunk * (kv.D + 2) * 4) : 0;
   return p;
 }
@@ -394,6 +504,7 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   a.nchunk = (int32_t)p.nchunk;
   a.row_tiles = (int32_t)p.row_tiles;
   a.scale = scale;
+  a.q16 = reinterpret_cast<uintptr_t>(q) % 16 == 0 && (kv.rows == 1 || ldq % 4 == 0);
   const dim3 grid((unsigned)(p.work_items / (64 * kAttnWaves))), block(64 * kAttnWaves);
   if (kv.D == 64) {
     if (p.nt == 1) hipLaunchKernelGGL((attn_kernel<64, 1>), grid, block, 0, s, a);
@@ -404,9 +515,9 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.nchunk == 1) return e;
-  const dim3 jgrid((unsigned)(p.join_items / 256));
-  if (kv.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, dim3(256), 0, s, a);
+  const dim3 jgrid((unsigned)(p.join_items / (64 * kAttnWaves)));
+  if (kv.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, block, 0, s, a);
   return hipGetLastError();
 }
 
