@@ -83,10 +83,39 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t w0, uint32_t w1) {
   return o.v;
 }
 
+// Eight int8 codes as (code + 128) * 2^-24: u in the low byte of an fp16 is
+// the subnormal u * 2^-24, so nothing is subtracted here.  The first product
+// starts its sums at -128 times the sum of the query row instead; what that
+// costs is a rounding at about twice the magnitude.  (The second product
+// cannot: its sums, of many values of either sign, are small beside those of
+// values + 128.)
+__device__ __forceinline__ f16x8 codes_sub(uint32_t w0, uint32_t w1) {
+  w0 ^= 0x80808080u;
+  w1 ^= 0x80808080u;
+  const u32x4 o = {__builtin_amdgcn_perm(0u, w0, 0x0c010c00u), __builtin_amdgcn_perm(0u, w0, 0x0c030c02u),
+                   __builtin_amdgcn_perm(0u, w1, 0x0c010c00u), __builtin_amdgcn_perm(0u, w1, 0x0c030c02u)};
+  return __builtin_bit_cast(f16x8, o);
+}
+
+// v - hi of one half of a pair: one instruction that reads the fp16 as it is.
+template <bool HIGH>
+__device__ __forceinline__ float minus_half(float v, f16x2 h) {
+  float r;
+  if constexpr (HIGH)
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(v));
+  else
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(v));
+  return r;
+}
 // v = hi + lo to 22 bits (hi rounded toward zero: lo has its sign).
 __device__ __forceinline__ void split2(float a, float b, f16x2& hi, f16x2& lo) {
   hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
-  lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a - (float)hi[0], b - (float)hi[1]));
+  lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(minus_half<false>(a, hi), minus_half<true>(b, hi)));
+}
+
+// The value of the lane eight columns on (the other half of a packed tile).
+__device__ __forceinline__ float other_half(float v) {
+  return __builtin_bit_cast(float, dpp_partner<8>(__builtin_bit_cast(uint32_t, v)));
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
@@ -105,20 +134,25 @@ constexpr float kNegInf = -__builtin_inff();
 
 // One workgroup: one (sequence, KV head), 16 * NT rows (row i: new token i /
 // G, query head i % G of the KV head's), one chunk of the positions, whose
-// steps the four waves take in turn.
-template <int D, int NT>
+// steps the four waves take in turn.  PACK: 8 rows, whose high and low
+// operands are the columns 0-7 and 8-15 of one matrix operand, so a product
+// takes one instruction where two tiles would take two.
+template <int D, int NT, bool PACK>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   constexpr int KS = D / 32;  // k steps of the first product
   constexpr int DT = D / 16;  // 16-dim tiles of the output
   constexpr int LD = D + 4;
+  constexpr int ROWS = PACK ? 8 : 16 * NT;
+  static_assert(!PACK || NT == 1, "a packed tile stands alone");
   // the query operands (high and low halves, by lane), and after the last step the waves' sums of a tile
   union Share {
-    f16x8 q[NT][KS][2][64];
+    f16x8 q[NT][KS][PACK ? 1 : 2][64];
     float o[kAttnWaves][16][LD];
   };
   __shared__ Share sh;
   __shared__ float sml[kAttnWaves][16 * NT][2];
-  __shared__ float qfac[16 * NT];      // factor of a row's scores: scale * log2(e) * the row's power of two
+  // a row's |scale| * log2(e) * powers of two, and where its sums start
+  __shared__ float qfac[16 * NT], qbias[16 * NT];
   __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
   __shared__ float kscale[kGroups], vscale[kGroups];
 
@@ -131,10 +165,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   const int rt = a.row_tiles - 1 - b % a.row_tiles;
   const int s = b / a.row_tiles;
   const SeqView sv = seq_view(kv, s);
-  const int rows = min(sv.n, (int)kv.max_new) * a.G, row_lo = rt * 16 * NT;
+  const int rows = min(sv.n, (int)kv.max_new) * a.G, row_lo = rt * ROWS;
   if (row_lo >= rows) return;
   // positions that some row of the tile sees: up to the last row's own
-  const int64_t last_pos = sv.pos0 + min(row_lo + 16 * NT - 1, rows - 1) / a.G;
+  const int64_t last_pos = sv.pos0 + min(row_lo + ROWS - 1, rows - 1) / a.G;
   const int64_t end = min(sv.len, last_pos + 1);
   const int64_t c0 = (int64_t)c * a.chunk;
   const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
@@ -143,55 +177,77 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
+  const int nr = PACK ? n & 7 : n;  // the lane's row of a tile
+  const bool low = PACK && n >= 8;  // the lane holds low operands
 
   // Loads in three trips to memory: the sequence; page ids and query rows;
   // scales, K and V.  Wave u prepares query tile u, for all the waves, while
   // its first K and V are under way.
   float x[D / 4];
   if (wave < NT) {
-    const int r = row_lo + 16 * wave + n;
+    const int r = row_lo + 16 * wave + nr;
     const bool live = r < rows;
     const float* q = a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
                      (int64_t)(h * a.G + (live ? r % a.G : 0)) * D + g * (D / 4);
+    // (a row past the last reads the sequence's first, for zeros)
     if (a.q16) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        const f32x4 v = live ? __builtin_bit_cast(f32x4, load16(q + 4 * j)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const f32x4 v = __builtin_bit_cast(f32x4, load16(q + 4 * j));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[4 * j + i] = v[i];
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < D / 4; ++j) x[j] = live ? load_g(q + j) : 0.0f;
+      for (int j = 0; j < D / 4; ++j) x[j] = load_g(q + j);
     }
   }
   auto prepare_q = [&]() {
+    const bool live = row_lo + 16 * wave + nr < rows;
     float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < D / 4; ++j) amax = fmaxf(amax, fabsf(x[j]));
+    for (int j = 0; j < D / 4; ++j) {
+      x[j] = live ? x[j] : 0.0f;
+      amax = fmaxf(amax, fabsf(x[j]));
+    }
     amax = max_groups(amax);
-    // 2^(8 - exponent): the largest element lands in [2^8, 2^9)
+    // 2^(8 - exponent): the largest element lands in [2^8, 2^9); the sign of
+    // the scale goes with it, so that a row's factor is not negative
     const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
-    const float up = pow2i(8 - e);
-    if (g == 0) qfac[16 * wave + n] = a.scale * 1.44269504088896340736f * pow2i(e - 8);
+    const float up = a.scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
+    float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
       f16x8 qh, ql;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const float x0 = x[8 * j + 2 * i] * up, x1 = x[8 * j + 2 * i + 1] * up;
         f16x2 hi, lo;
-        split2(x[8 * j + 2 * i] * up, x[8 * j + 2 * i + 1] * up, hi, lo);
+        split2(x0, x1, hi, lo);
         qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
         ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
+        if (PACK)
+          sum += low ? (float)lo[0] + (float)lo[1] : (float)hi[0] + (float)hi[1];
+        else
+          sum += x0 + x1;
       }
-      sh.q[wave][j][0][lane] = qh;
-      sh.q[wave][j][1][lane] = ql;
+      if constexpr (PACK) {
+        sh.q[wave][j][0][lane] = low ? ql : qh;
+      } else {
+        sh.q[wave][j][0][lane] = qh;
+        sh.q[wave][j][1][lane] = ql;
+      }
+    }
+    sum = sum_groups(sum);
+    if (g == 0) {
+      qfac[16 * wave + n] = fabsf(a.scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f;
+      qbias[16 * wave + n] = sum * (-128.0f / 16777216.0f);
     }
   };
   int32_t pos[NT];  // last position that the row sees (-1: none)
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int r = row_lo + 16 * u + n;
+    const int r = row_lo + 16 * u + nr;
     pos[u] = r < rows ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
   }
 
@@ -209,64 +265,78 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   // position of the tile that every row sees: below it no mask is needed
   const int64_t all_see = min(sv.len, sv.pos0 + row_lo / a.G + 1);
   const int P = 1 << kv.log_p;
-  for (int64_t w0 = c0; w0 < c1; w0 += kWindow) {
-    const int64_t jg = w0 + 16 * (int)threadIdx.x;
-    const int32_t id = jg < sv.len ? page_of(kv, s, jg >> kv.log_p) : -1;
+  u32x4 kw[4][D / 64], vw[DT];
+  int64_t w0 = c0;
+  int steps = 0;
+  // A step's K rows (this lane's are of group n / 4) and V rows (of its own
+  // positions, group g).  A group without a page reads page 0 and counts for
+  // nothing.
+  auto load_k = [&](int st) {
+    const int gr = 4 * st + (n >> 2);
+    const int64_t base = (((int64_t)max(page[gr], 0) * kv.H + h) << kv.log_p) + (((int)w0 + 16 * gr) & (P - 1));
+    const int8_t* kp = kv.k + (base + (n & 3)) * D + g * (D / 4);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + 4 * t * D + 16 * i);
+  };
+  auto load_v = [&](int st) {
+    const int gr = 4 * st + g;
+    const int8_t* vp = kv.v + ((((int64_t)max(page[gr], 0) * kv.H + h) * D + n) << kv.log_p) +
+                       (((int)w0 + 16 * gr) & (P - 1));
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vw[d] = load16(vp + ((int64_t)(16 * d) << kv.log_p));
+  };
+  // The pages and scales of the window at w0, and its first loads.
+  auto open_window = [&]() {
+    const int64_t j = w0 + 16 * (int)threadIdx.x;
+    const int32_t id = j < sv.len ? page_of(kv, s, j >> kv.log_p) : -1;
     const int64_t si = (int64_t)max(id, 0) * kv.H + h;
-    const float ks_g = load_g(kv.k_scale + si), vs_g = load_g(kv.v_scale + si);
-    if (w0 > c0) __syncthreads();  // (the window before has been read)
+    const float ks = load_g(kv.k_scale + si), vs = load_g(kv.v_scale + si);
     page[threadIdx.x] = id;
     __syncthreads();
-    const int steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
-    u32x4 kw[4][D / 64], vw[DT];
-    // A step's K rows (this lane's are of group n / 4) and V rows (of its own
-    // positions, group g).  A group without a page reads page 0 and counts
-    // for nothing.
-    auto load_k = [&](int st) {
-      const int gr = 4 * st + (n >> 2);
-      const int64_t base = (((int64_t)max(page[gr], 0) * kv.H + h) << kv.log_p) + (((int)w0 + 16 * gr) & (P - 1));
-      const int8_t* kp = kv.k + (base + (n & 3)) * D + g * (D / 4);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + 4 * t * D + 16 * i);
-    };
-    auto load_v = [&](int st) {
-      const int gr = 4 * st + g;
-      const int8_t* vp = kv.v + ((((int64_t)max(page[gr], 0) * kv.H + h) * D + n) << kv.log_p) +
-                         (((int)w0 + 16 * gr) & (P - 1));
-#pragma unroll
-      for (int d = 0; d < DT; ++d) vw[d] = load16(vp + ((int64_t)(16 * d) << kv.log_p));
-    };
+    steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
     if (wave < steps) {
       load_k(wave);
       load_v(wave);
     }
-    kscale[threadIdx.x] = id < 0 ? 0.0f : ks_g;
-    vscale[threadIdx.x] = id < 0 ? 0.0f : vs_g;
-    if (w0 == c0 && wave < NT) prepare_q();
-    __syncthreads();
-
+    kscale[threadIdx.x] = id < 0 ? 0.0f : ks;
+    vscale[threadIdx.x] = id < 0 ? 0.0f : vs;
+  };
+  open_window();
+  if (wave < NT) prepare_q();
+  __syncthreads();
+  for (;;) {
     f32x4 sc[NT][4];
     auto scores = [&]() {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int u = 0; u < NT; ++u) {
+        const float b = qbias[16 * u + n];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) sc[u][t] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < 4; ++t) sc[u][t] = {b, b, b, b};
+      }
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        f16x8 qh[NT], ql[NT];
+        f16x8 q[NT][2];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) qh[u] = sh.q[u][j][0][lane], ql[u] = sh.q[u][j][1][lane];
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < (PACK ? 1 : 2); ++e) q[u][e] = sh.q[u][j][e][lane];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const f16x8 kf = codes_f16(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
+          const f16x8 kf = codes_sub(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
 #pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            sc[u][t] = mfma(kf, qh[u], sc[u][t]);
-            sc[u][t] = mfma(kf, ql[u], sc[u][t]);
-          }
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < (PACK ? 1 : 2); ++e) sc[u][t] = mfma(kf, q[u][e], sc[u][t]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (PACK) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[0][t][i] += other_half(sc[0][t][i]);
       }
     };
     auto weigh_and_sum = [&](int st) {
@@ -285,24 +355,29 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
           for (int d = 0; d < DT; ++d) o[u][d] *= f;
         ve = e;
       }
+      // weights take the V scale, vn <= 2^15, with the exponential: e^(s - m)
+      // vn = 2^(s' - m' + log2 vn), and sums of weights are divided by it.  A
+      // scale of 0, or far below the largest, is multiplied afterwards.
       const float vn = vs * pow2i(14 - ve);
+      const bool apart = vn < 0x1p-16f;
+      const float lv = apart ? 0.0f : __builtin_amdgcn_logf(vn), rl = apart ? 1.0f : __builtin_amdgcn_rcpf(vn);
+      const bool any_apart = __any(apart);
 
       const bool masked = j0 + kStep > all_see || __any(!here);
-      f16x8 ph[NT][2], pl[NT][2];
+      f16x8 pb[NT][2][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float p[16];
-        float mx = kNegInf;
-        const float f = qfac[16 * u + n] * ks;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = sc[u][i >> 2][i & 3] * f;
+        float f = qfac[16 * u + n] * ks;
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = here && jv + i <= pos[u] ? p[i] : kNegInf;
+          for (int i = 0; i < 16; ++i)
+            sc[u][i >> 2][i & 3] = here && jv + i <= pos[u] ? sc[u][i >> 2][i & 3] * f : kNegInf;
+          f = 1.0f;
         }
+        float mx = sc[u][0][0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, p[i]);
-        mx = max_groups(mx);
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[u][i >> 2][i & 3]);
+        mx = max_groups(mx * f);
         if (__any(mx > m[u])) {
           const float mn = fmaxf(m[u], mx);
           const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[u] - mn);
@@ -311,12 +386,18 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
           for (int d = 0; d < DT; ++d) o[u][d] *= al;
         }
-        const float mu = m[u] == kNegInf ? 0.0f : m[u];
+        const float off = lv - (m[u] == kNegInf ? 0.0f : m[u]);
+        float p[16], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
-          l[u] += p[i];
-          p[i] *= vn;
+          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][i >> 2][i & 3], f, off));
+          sum += p[i];
+        }
+        l[u] = __builtin_fmaf(sum, rl, l[u]);
+        if (any_apart) {
+          const float mul = apart ? vn : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] *= mul;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -324,9 +405,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
           for (int i = 0; i < 4; ++i) {
             f16x2 hi, lo;
             split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
-            ph[u][k][2 * i] = hi[0], ph[u][k][2 * i + 1] = hi[1];
-            pl[u][k][2 * i] = lo[0], pl[u][k][2 * i + 1] = lo[1];
+            if constexpr (PACK) hi = low ? lo : hi;
+            pb[u][k][0][2 * i] = hi[0], pb[u][k][0][2 * i + 1] = hi[1];
+            pb[u][k][1][2 * i] = lo[0], pb[u][k][1][2 * i + 1] = lo[1];
           }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -334,10 +417,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
         for (int d = 0; d < DT; ++d) {
           const f16x8 vf = codes_f16(vw[d][2 * k], vw[d][2 * k + 1]);
 #pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            o[u][d] = mfma(vf, ph[u][k], o[u][d]);
-            o[u][d] = mfma(vf, pl[u][k], o[u][d]);
-          }
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < (PACK ? 1 : 2); ++e) o[u][d] = mfma(vf, pb[u][k][e], o[u][d]);
         }
     };
     // (the last step apart: a load that may or may not have been issued would
@@ -354,6 +436,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
       scores();
       weigh_and_sum(st);
     }
+    w0 += kWindow;
+    if (w0 >= c1) break;
+    __syncthreads();  // (the window before has been read)
+    open_window();
+    __syncthreads();
   }
 
   // join the four waves, a tile at a time
@@ -367,9 +454,16 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   for (int u = 0; u < NT; ++u) {
     __syncthreads();  // (the operands, or the tile before, have been read)
 #pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = o[u][d] * back;
+    for (int d = 0; d < DT; ++d) {
+      f32x4 v = o[u][d] * back;
+      if constexpr (PACK) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += other_half(v[i]);
+      }
+      *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = v;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D; i += 64 * kAttnWaves) {
+    for (int i = threadIdx.x; i < (PACK ? 8 : 16) * D; i += 64 * kAttnWaves) {
       const int r = 16 * u + i / D, d = i % D;
       if (row_lo + r >= rows) break;
       float mm = kNegInf;
@@ -463,15 +557,24 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) 
 
 constexpr int kWgPerCu = 4;
 
-int attn_tiles_per_wave(int64_t rows) { return rows <= 16 ? 1 : 2; }
+// 16-row tiles per workgroup; 0: eight rows in a packed tile.
+int attn_tiles(int64_t rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : 2; }
+
+template <int D>
+void launch_tiles(int nt, dim3 grid, dim3 block, const AttnArgs& a, hipStream_t s) {
+  if (nt == 0) hipLaunchKernelGGL((attn_kernel<D, 1, true>), grid, block, 0, s, a);
+  else if (nt == 1) hipLaunchKernelGGL((attn_kernel<D, 1, false>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attn_kernel<D, 2, false>), grid, block, 0, s, a);
+}
 
 }  // namespace
 
 AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   AttnPlan p;
   const int64_t G = Hq / kv.H, rows = kv.max_new * G;
-  p.nt = attn_tiles_per_wave(rows);
-  p.row_tiles = (rows + 16 * p.nt - 1) / (16 * p.nt);
+  p.nt = attn_tiles(rows);
+  const int64_t tile = p.nt == 0 ? 8 : 16 * p.nt;
+  p.row_tiles = (rows + tile - 1) / tile;
   // Chunks: enough workgroups to fill the chip a few times over, each at
   // least one step per wave.
   const int64_t most = kv.ld_table << kv.log_p;
@@ -506,13 +609,10 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   a.scale = scale;
   a.q16 = reinterpret_cast<uintptr_t>(q) % 16 == 0 && (kv.rows == 1 || ldq % 4 == 0);
   const dim3 grid((unsigned)(p.work_items / (64 * kAttnWaves))), block(64 * kAttnWaves);
-  if (kv.D == 64) {
-    if (p.nt == 1) hipLaunchKernelGGL((attn_kernel<64, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attn_kernel<64, 2>), grid, block, 0, s, a);
-  } else {
-    if (p.nt == 1) hipLaunchKernelGGL((attn_kernel<128, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attn_kernel<128, 2>), grid, block, 0, s, a);
-  }
+  if (kv.D == 64)
+    launch_tiles<64>(p.nt, grid, block, a, s);
+  else
+    launch_tiles<128>(p.nt, grid, block, a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.nchunk == 1) return e;
   const dim3 jgrid((unsigned)(p.join_items / (64 * kAttnWaves)));

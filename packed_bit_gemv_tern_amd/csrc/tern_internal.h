@@ -299,7 +299,7 @@ int64_t kv_append_work_items(const KvArgs& a);
 hipError_t launch_kv_append(const KvArgs& a, const float* k, int64_t ldk, const float* v, int64_t ldv, hipStream_t s);
 // tern_attn.hip: how a call's rows and positions are split over workgroups
 struct AttnPlan {
-  int nt;             // 16-row tiles a wave holds
+  int nt;             // 16-row tiles of a workgroup (0: eight rows, packed)
   int64_t row_tiles;  // row tiles of a sequence and KV head
   int64_t chunk, nchunk;
   int64_t work_items, join_items, workspace;
