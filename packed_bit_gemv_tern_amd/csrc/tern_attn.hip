@@ -29,8 +29,8 @@
 //
 // Loads: a wave issues the next step's K loads once the first product has
 // read the registers, and the next V loads after the second, so 8 to 16 KB
-// per wave are always in flight.  Page ids and scales of up to kWindow
-// positions are fetched to LDS at once, out of the steps' way.
+// per wave are always in flight.  Page ids and scales of 1,024 positions
+// per wave are fetched to LDS at once, out of the steps' way.
 #include <algorithm>
 
 #include "tern_cache.h"
@@ -43,11 +43,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kAttnWaves = 4;
 constexpr int kStep = 64;  // positions per step of a wave
-constexpr int kWindow = 4096;  // positions whose pages are looked up at once
-constexpr int kGroups = kWindow / 16;
-static_assert(kGroups == 64 * kAttnWaves, "one group of 16 positions per thread");
+constexpr int kJoinWaves = 4;
 
 struct AttnArgs {
   KvArgs kv;
@@ -60,7 +57,7 @@ struct AttnArgs {
   int32_t chunk, nchunk;  // positions per chunk, chunks a sequence is split into
   int32_t row_tiles;
   float scale;
-  bool q16;  // query rows are 16-byte aligned
+  bool q16, y16;  // query rows, output rows are 16-byte aligned
 };
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
@@ -132,25 +129,148 @@ __device__ __forceinline__ float sum_groups(float v) {
 
 constexpr float kNegInf = -__builtin_inff();
 
+// The elements of a query row that lane group g holds: 16 g .. 16 g + 15 of
+// every 64, the operands of k steps 2 i and 2 i + 1 (8 each).
+template <int D>
+__device__ __forceinline__ void load_query(const AttnArgs& a, const float* q, int g, float (&x)[D / 4]) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const float* p = q + 64 * i + 16 * g;
+    if (a.q16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 v = __builtin_bit_cast(f32x4, load16(p + 4 * j));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[16 * i + 4 * j + e] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[16 * i + j] = load_g(p + j);
+    }
+  }
+}
+
+// A query row's operands, high and low: the row times a power of two that
+// brings its largest element to [2^8, 2^9) (and the sign of the scale, so
+// that the factor of its scores is not negative).  Returns that factor,
+// |scale| * log2(e) * the powers of two left out; `sum_h` and `sum_l` get the
+// sums of the halves over the row.
+template <int D>
+__device__ __forceinline__ float split_query(float scale, float (&x)[D / 4], f16x8 (&qh)[D / 32], f16x8 (&ql)[D / 32],
+                                             float& sum_h, float& sum_l) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 4; ++j) amax = fmaxf(amax, fabsf(x[j]));
+  amax = max_groups(amax);
+  const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
+  const float up = scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
+  sum_h = sum_l = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f16x2 hi, lo;
+      split2(x[8 * j + 2 * i] * up, x[8 * j + 2 * i + 1] * up, hi, lo);
+      qh[j][2 * i] = hi[0], qh[j][2 * i + 1] = hi[1];
+      ql[j][2 * i] = lo[0], ql[j][2 * i + 1] = lo[1];
+      sum_h += (float)hi[0] + (float)hi[1];
+      sum_l += (float)lo[0] + (float)lo[1];
+    }
+  sum_h = sum_groups(sum_h);
+  sum_l = sum_groups(sum_l);
+  return fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f;
+}
+constexpr float kBias = -128.0f / 16777216.0f;  // times a row's sum: where its scores start (codes_sub)
+
+// The V scale of the lane's 16 positions in a step.  Weights take it with the
+// exponential: e^(s - m) vn = 2^(s' - m' + log2 vn), vn = vs * 2^(14 - ve) <=
+// 2^15, and sums of weights are divided by it.  A scale of 0, or far below
+// the largest, is multiplied afterwards (`apart`).
+struct VScale {
+  float vn, lv, rl;
+  bool apart, any_apart;
+};
+// `ve` is the exponent of the largest V scale met: where this step's is
+// larger, the sums so far move to its power of two.
+template <int DT, int NT>
+__device__ __forceinline__ VScale v_scale(float vs, int& ve, f32x4 (&o)[NT][DT]) {
+  const int e = __builtin_amdgcn_readfirstlane(
+      min((int)(__builtin_bit_cast(uint32_t, max_groups(vs)) >> 23) - 127, 120));
+  if (e > ve) {
+    const float f = ve - e < -126 ? 0.0f : pow2i(ve - e);
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[u][d] *= f;
+    ve = e;
+  }
+  VScale v;
+  v.vn = vs * pow2i(14 - ve);
+  v.apart = v.vn < 0x1p-16f;
+  v.lv = v.apart ? 0.0f : __builtin_amdgcn_logf(v.vn);
+  v.rl = v.apart ? 1.0f : __builtin_amdgcn_rcpf(v.vn);
+  v.any_apart = __any(v.apart);
+  return v;
+}
+// One row's 16 scores of a step (times f: in units of log2) to weights p; m,
+// l and o follow a larger maximum.  Where `masked`, only positions up to
+// `last` of the lane's 16 count.
+template <int DT>
+__device__ __forceinline__ void softmax_step(f32x4 (&sc)[4], float f, bool masked, int last, const VScale& v, float& m,
+                                             float& l, f32x4 (&o)[DT], float (&p)[16]) {
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
+    f = 1.0f;
+  }
+  float mx = sc[0][0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
+  mx = max_groups(mx * f);
+  if (__any(mx > m)) {
+    const float mn = fmaxf(m, mx);
+    const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l *= al;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] *= al;
+  }
+  const float off = v.lv - (m == kNegInf ? 0.0f : m);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 2][i & 3], f, off));
+    sum += p[i];
+  }
+  l = __builtin_fmaf(sum, v.rl, l);
+  if (v.any_apart) {
+    const float mul = v.apart ? v.vn : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] *= mul;
+  }
+}
+
 // One workgroup: one (sequence, KV head), 16 * NT rows (row i: new token i /
 // G, query head i % G of the KV head's), one chunk of the positions, whose
-// steps the four waves take in turn.  PACK: 8 rows, whose high and low
+// steps the W waves take in turn.  PACK: 8 rows, whose high and low
 // operands are the columns 0-7 and 8-15 of one matrix operand, so a product
 // takes one instruction where two tiles would take two.
-template <int D, int NT, bool PACK>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
+template <int D, int NT, bool PACK, int W>
+__global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   constexpr int KS = D / 32;  // k steps of the first product
   constexpr int DT = D / 16;  // 16-dim tiles of the output
   constexpr int LD = D + 4;
+  constexpr int kGroups = 64 * W;         // groups of 16 positions, one per thread,
+  constexpr int kWindow = 16 * kGroups;   // whose pages are looked up at once
   constexpr int ROWS = PACK ? 8 : 16 * NT;
   static_assert(!PACK || NT == 1, "a packed tile stands alone");
   // the query operands (high and low halves, by lane), and after the last step the waves' sums of a tile
   union Share {
     f16x8 q[NT][KS][PACK ? 1 : 2][64];
-    float o[kAttnWaves][16][LD];
+    float o[W][16][LD];
   };
   __shared__ Share sh;
-  __shared__ float sml[kAttnWaves][16 * NT][2];
+  __shared__ float sml[W][16 * NT][2];
   // a row's |scale| * log2(e) * powers of two, and where its sums start
   __shared__ float qfac[16 * NT], qbias[16 * NT];
   __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
@@ -187,61 +307,29 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   if (wave < NT) {
     const int r = row_lo + 16 * wave + nr;
     const bool live = r < rows;
-    const float* q = a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
-                     (int64_t)(h * a.G + (live ? r % a.G : 0)) * D + g * (D / 4);
     // (a row past the last reads the sequence's first, for zeros)
-    if (a.q16) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        const f32x4 v = __builtin_bit_cast(f32x4, load16(q + 4 * j));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * j + i] = v[i];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 4; ++j) x[j] = load_g(q + j);
-    }
+    load_query<D>(a, a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
+                         (int64_t)(h * a.G + (live ? r % a.G : 0)) * D, g, x);
   }
   auto prepare_q = [&]() {
     const bool live = row_lo + 16 * wave + nr < rows;
-    float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < D / 4; ++j) {
-      x[j] = live ? x[j] : 0.0f;
-      amax = fmaxf(amax, fabsf(x[j]));
-    }
-    amax = max_groups(amax);
-    // 2^(8 - exponent): the largest element lands in [2^8, 2^9); the sign of
-    // the scale goes with it, so that a row's factor is not negative
-    const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
-    const float up = a.scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
-    float sum = 0.0f;
+    for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
+    f16x8 qh[KS], ql[KS];
+    float sum_h, sum_l;
+    const float f = split_query<D>(a.scale, x, qh, ql, sum_h, sum_l);
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-      f16x8 qh, ql;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = x[8 * j + 2 * i] * up, x1 = x[8 * j + 2 * i + 1] * up;
-        f16x2 hi, lo;
-        split2(x0, x1, hi, lo);
-        qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
-        ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
-        if (PACK)
-          sum += low ? (float)lo[0] + (float)lo[1] : (float)hi[0] + (float)hi[1];
-        else
-          sum += x0 + x1;
-      }
       if constexpr (PACK) {
-        sh.q[wave][j][0][lane] = low ? ql : qh;
+        sh.q[wave][j][0][lane] = low ? ql[j] : qh[j];
       } else {
-        sh.q[wave][j][0][lane] = qh;
-        sh.q[wave][j][1][lane] = ql;
+        sh.q[wave][j][0][lane] = qh[j];
+        sh.q[wave][j][1][lane] = ql[j];
       }
     }
-    sum = sum_groups(sum);
     if (g == 0) {
-      qfac[16 * wave + n] = fabsf(a.scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f;
-      qbias[16 * wave + n] = sum * (-128.0f / 16777216.0f);
+      qfac[16 * wave + n] = f;
+      qbias[16 * wave + n] = kBias * (PACK ? (low ? sum_l : sum_h) : sum_h + sum_l);
     }
   };
   int32_t pos[NT];  // last position that the row sees (-1: none)
@@ -274,11 +362,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   auto load_k = [&](int st) {
     const int gr = 4 * st + (n >> 2);
     const int64_t base = (((int64_t)max(page[gr], 0) * kv.H + h) << kv.log_p) + (((int)w0 + 16 * gr) & (P - 1));
-    const int8_t* kp = kv.k + (base + (n & 3)) * D + g * (D / 4);
+    const int8_t* kp = kv.k + (base + (n & 3)) * D + 16 * g;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + 4 * t * D + 16 * i);
+      for (int i = 0; i < D / 64; ++i) kw[t][i] = load16(kp + 4 * t * D + 64 * i);
   };
   auto load_v = [&](int st) {
     const int gr = 4 * st + g;
@@ -344,61 +432,13 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
       const int32_t jv = (int32_t)j0 + 16 * g;
       const bool here = page[4 * st + g] >= 0;
       const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
-      // a larger V scale: everything summed so far moves to its power of two
-      const int e = __builtin_amdgcn_readfirstlane(
-          min((int)(__builtin_bit_cast(uint32_t, max_groups(vs)) >> 23) - 127, 120));
-      if (e > ve) {
-        const float f = ve - e < -126 ? 0.0f : pow2i(ve - e);
-#pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[u][d] *= f;
-        ve = e;
-      }
-      // weights take the V scale, vn <= 2^15, with the exponential: e^(s - m)
-      // vn = 2^(s' - m' + log2 vn), and sums of weights are divided by it.  A
-      // scale of 0, or far below the largest, is multiplied afterwards.
-      const float vn = vs * pow2i(14 - ve);
-      const bool apart = vn < 0x1p-16f;
-      const float lv = apart ? 0.0f : __builtin_amdgcn_logf(vn), rl = apart ? 1.0f : __builtin_amdgcn_rcpf(vn);
-      const bool any_apart = __any(apart);
-
+      const VScale v = v_scale<DT>(vs, ve, o);
       const bool masked = j0 + kStep > all_see || __any(!here);
       f16x8 pb[NT][2][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float f = qfac[16 * u + n] * ks;
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sc[u][i >> 2][i & 3] = here && jv + i <= pos[u] ? sc[u][i >> 2][i & 3] * f : kNegInf;
-          f = 1.0f;
-        }
-        float mx = sc[u][0][0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[u][i >> 2][i & 3]);
-        mx = max_groups(mx * f);
-        if (__any(mx > m[u])) {
-          const float mn = fmaxf(m[u], mx);
-          const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[u] - mn);
-          m[u] = mn;
-          l[u] *= al;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[u][d] *= al;
-        }
-        const float off = lv - (m[u] == kNegInf ? 0.0f : m[u]);
-        float p[16], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][i >> 2][i & 3], f, off));
-          sum += p[i];
-        }
-        l[u] = __builtin_fmaf(sum, rl, l[u]);
-        if (any_apart) {
-          const float mul = apart ? vn : 1.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] *= mul;
-        }
+        float p[16];
+        softmax_step<DT>(sc[u], qfac[16 * u + n] * ks, masked, here ? pos[u] - jv : -1, v, m[u], l[u], o[u], p);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -425,12 +465,12 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
     // (the last step apart: a load that may or may not have been issued would
     // have every step wait for all of them)
     int st = wave;
-    for (; st + kAttnWaves < steps; st += kAttnWaves) {
+    for (; st + W < steps; st += W) {
       asm volatile("" ::: "memory");  // (the query operands stay in LDS: held in registers they cost a wave per SIMD)
       scores();
-      load_k(st + kAttnWaves);
+      load_k(st + W);
       weigh_and_sum(st);
-      load_v(st + kAttnWaves);
+      load_v(st + W);
     }
     if (st < steps) {
       scores();
@@ -443,7 +483,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
     __syncthreads();
   }
 
-  // join the four waves, a tile at a time
+  // join the waves, a tile at a time
   const float back = pow2i(max(ve - 14, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
@@ -463,15 +503,15 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
       *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = v;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (PACK ? 8 : 16) * D; i += 64 * kAttnWaves) {
+    for (int i = threadIdx.x; i < (PACK ? 8 : 16) * D; i += 64 * W) {
       const int r = 16 * u + i / D, d = i % D;
       if (row_lo + r >= rows) break;
       float mm = kNegInf;
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sml[w][r][0]);
+      for (int w = 0; w < W; ++w) mm = fmaxf(mm, sml[w][r][0]);
       float ls = 0.0f, os = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = sml[w][r][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][r][0] - mm);
         ls = __builtin_fmaf(sml[w][r][1], f, ls);
         os = __builtin_fmaf(sh.o[w][i / D][d], f, os);
@@ -492,11 +532,225 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(AttnArgs a) {
   }
 }
 
+// Prompts: a workgroup of four waves takes 128 rows, a wave 32 of them over
+// all positions.  Each step's 64 positions are converted to fp16 once, by all
+// the waves, into one of two LDS buffers, laid out as the products read them
+// (16 bytes per lane, a whole kilobyte per instruction), so a wave's 32 rows
+// cost a quarter of the conversions and every operand read is free of bank
+// conflicts: slot (n ^ 4 g) of lane group g keeps the writes, whose lanes run
+// over g and the low bits of n, off each other's banks too.  The codes of the
+// step after the next are on their way to registers meanwhile.  Two
+// workgroups per CU: one's matrix instructions run beside the other's
+// exponentials.  Matrix bound: four products (two halves each of Q and P)
+// where 16-bit attention takes two.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
+  constexpr int KS = D / 32, DT = D / 16, NT = 2, W = 4, ROWS = 16 * NT * W;
+  constexpr int kGroups = 64 * W, kWindow = 16 * kGroups;
+  constexpr int NP = D / 64;  // 16-code pieces of K, and of V, per thread
+  __shared__ f16x8 kf[2][4][KS][64];
+  __shared__ f16x8 vf[2][DT][2][64];
+  __shared__ int32_t page[kGroups];
+  __shared__ float kscale[kGroups], vscale[kGroups];
+
+  const KvArgs& kv = a.kv;
+  int b = blockIdx.x;
+  const int h = b % kv.H;
+  b /= kv.H;
+  const int c = b % a.nchunk;
+  b /= a.nchunk;
+  const int rt = a.row_tiles - 1 - b % a.row_tiles;  // (the longest first)
+  const int s = b / a.row_tiles;
+  const SeqView sv = seq_view(kv, s);
+  const int rows = min(sv.n, (int)kv.max_new) * a.G, row_lo = rt * ROWS;
+  if (row_lo >= rows) return;
+  const int64_t last_pos = sv.pos0 + min(row_lo + ROWS - 1, rows - 1) / a.G;
+  const int64_t end = min(sv.len, last_pos + 1);
+  const int64_t c0 = (int64_t)c * a.chunk;
+  const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
+  if (c0 >= c1 && c > 0) return;
+
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  const int slot = 16 * g + (n ^ (4 * g));
+
+  f16x8 qh[NT][KS], ql[NT][KS];
+  float qfac[NT], qbias[NT];
+  int32_t pos[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int r = row_lo + 16 * (NT * wave + u) + n;
+    const bool live = r < rows;
+    pos[u] = live ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
+    float x[D / 4], sum_h, sum_l;
+    load_query<D>(a, a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
+                         (int64_t)(h * a.G + (live ? r % a.G : 0)) * D, g, x);
+#pragma unroll
+    for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
+    qfac[u] = split_query<D>(a.scale, x, qh[u], ql[u], sum_h, sum_l);
+    qbias[u] = kBias * (sum_h + sum_l);
+  }
+
+  f32x4 o[NT][DT];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    m[u] = kNegInf;
+    l[u] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[u][d] = {0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  int ve = -100;
+  const int64_t all_see = min(sv.len, sv.pos0 + (row_lo + 16 * NT * wave) / a.G + 1);
+  const int P = 1 << kv.log_p;
+
+  // A thread's pieces of a step: K piece e is 16 dims (g' + 4 i) of position
+  // 16 grp + r; V piece e is the 16 positions of group g' of one dim.  g'
+  // and the low bits of the position or dim are the lane's lowest bits.
+  const int pg = t & 3;
+  u32x4 kraw[NP], vraw[NP];
+  int64_t w0 = c0;
+  auto k_piece = [&](int e, int& tok, int& i) {
+    const int id = (t >> 2) + 64 * e;  // position, then the 64 dims
+    tok = id & 63, i = id >> 6;
+  };
+  auto load_codes = [&](int st) {
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      int tok, i;
+      k_piece(e, tok, i);
+      const int gr = 4 * st + (tok >> 4);
+      const int64_t base = (((int64_t)max(page[gr], 0) * kv.H + h) << kv.log_p) + (((int)w0 + kStep * st + tok) & (P - 1));
+      kraw[e] = load16(kv.k + base * D + 64 * i + 16 * pg);
+      const int d = (t >> 2) + 64 * e, gv = 4 * st + pg;
+      vraw[e] = load16(kv.v + ((((int64_t)max(page[gv], 0) * kv.H + h) * D + d) << kv.log_p) +
+                       (((int)w0 + 16 * gv) & (P - 1)));
+    }
+  };
+  auto write_codes = [&](int buf) {
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      int tok, i;
+      k_piece(e, tok, i);
+      const int r = tok & 15, kn = 4 * (tok >> 4) + (r & 3);
+      const int at = 16 * pg + (kn ^ (4 * pg));
+      kf[buf][r >> 2][2 * i][at] = codes_sub(kraw[e][0], kraw[e][1]);
+      kf[buf][r >> 2][2 * i + 1][at] = codes_sub(kraw[e][2], kraw[e][3]);
+      const int d = (t >> 2) + 64 * e;
+      const int vt = 16 * pg + ((d & 15) ^ (4 * pg));
+      vf[buf][d >> 4][0][vt] = codes_f16(vraw[e][0], vraw[e][1]);
+      vf[buf][d >> 4][1][vt] = codes_f16(vraw[e][2], vraw[e][3]);
+    }
+  };
+
+  for (; w0 < c1; w0 += kWindow) {
+    {
+      const int64_t j = w0 + 16 * t;
+      const int32_t id = j < sv.len ? page_of(kv, s, j >> kv.log_p) : -1;
+      const int64_t si = (int64_t)max(id, 0) * kv.H + h;
+      const float ks = load_g(kv.k_scale + si), vs = load_g(kv.v_scale + si);
+      __syncthreads();  // (the window before has been read)
+      page[t] = id;
+      kscale[t] = id < 0 ? 0.0f : ks;
+      vscale[t] = id < 0 ? 0.0f : vs;
+      __syncthreads();
+    }
+    const int steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
+    load_codes(0);
+    write_codes(0);
+    load_codes(min(1, steps - 1));
+    for (int st = 0; st < steps; ++st) {
+      const int buf = st & 1;
+      // this step's operands are written; every wave is past the step before,
+      // whose buffer the next step's go to
+      __syncthreads();
+      f32x4 sc[NT][4];
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[u][e] = {qbias[u], qbias[u], qbias[u], qbias[u]};
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x8 k = kf[buf][e][j][slot];
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            sc[u][e] = mfma(k, qh[u][j], sc[u][e]);
+            sc[u][e] = mfma(k, ql[u][j], sc[u][e]);
+          }
+        }
+      if (st + 1 < steps) {
+        write_codes(buf ^ 1);
+        if (st + 2 < steps) load_codes(st + 2);
+      }
+      const int64_t j0 = w0 + kStep * st;
+      const int32_t jv = (int32_t)j0 + 16 * g;
+      const bool here = page[4 * st + g] >= 0;
+      const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
+      const VScale v = v_scale<DT>(vs, ve, o);
+      const bool masked = j0 + kStep > all_see || __any(!here);
+      f16x8 pb[NT][2][2];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        float p[16];
+        softmax_step<DT>(sc[u], qfac[u] * ks, masked, here ? pos[u] - jv : -1, v, m[u], l[u], o[u], p);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f16x2 hi, lo;
+            split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
+            pb[u][k][0][2 * i] = hi[0], pb[u][k][0][2 * i + 1] = hi[1];
+            pb[u][k][1][2 * i] = lo[0], pb[u][k][1][2 * i + 1] = lo[1];
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const f16x8 w = vf[buf][d][k][slot];
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            o[u][d] = mfma(w, pb[u][k][0], o[u][d]);
+            o[u][d] = mfma(w, pb[u][k][1], o[u][d]);
+          }
+        }
+    }
+  }
+
+  const float back = pow2i(max(ve - 14, -126));
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const float lt = sum_groups(l[u]);
+    const int r = row_lo + 16 * (NT * wave + u) + n;
+    if (r >= rows) continue;
+    const int64_t row = sv.row0 + r / a.G, hq = h * a.G + r % a.G;
+    const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
+    const bool whole = a.nchunk == 1;
+    const float f = whole ? (lt > 0.0f ? back / lt : 0.0f) : back;
+    float* out = whole ? a.y + row * a.ldy + hq * D : a.part + at * D;
+    if (!whole && g == 0) {
+      store_g(a.part_ml + 2 * at, m[u]);
+      store_g(a.part_ml + 2 * at + 1, lt);
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      if (a.y16 || !whole) {
+        store_g(reinterpret_cast<f32x4*>(out + 16 * d + 4 * g), o[u][d] * f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_g(out + 16 * d + 4 * g + i, o[u][d][i] * f);
+      }
+    }
+  }
+}
+
 // Joins the chunks of each (row, query head): a workgroup of four waves each,
 // wave w the chunks w, w + 4, ...
 template <int D>
-__global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) {
-  __shared__ float so[kAttnWaves][D], sml[kAttnWaves][2];
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) {
+  __shared__ float so[kJoinWaves][D], sml[kJoinWaves][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hq = (int)(blockIdx.x % a.Hq);
   const int64_t rest = blockIdx.x / a.Hq;
@@ -511,8 +765,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) 
   float m = kNegInf, l = 0.0f, o[D / 64];
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) o[d] = 0.0f;
-  for (int b = wave; b < nc; b += 64 * kAttnWaves) {
-    const int c = b + kAttnWaves * lane;
+  for (int b = wave; b < nc; b += 64 * kJoinWaves) {
+    const int c = b + kJoinWaves * lane;
     const float mc = c < nc ? load_g(a.part_ml + 2 * (at + c)) : kNegInf;
     const float lc = c < nc ? load_g(a.part_ml + 2 * (at + c) + 1) : 0.0f;
     float mn = mc;
@@ -528,25 +782,25 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) 
     l = __builtin_fmaf(l, al, ls);
 #pragma unroll
     for (int d = 0; d < D / 64; ++d) o[d] *= al;
-    const int cn = min(64, (nc - b + kAttnWaves - 1) / kAttnWaves);
+    const int cn = min(64, (nc - b + kJoinWaves - 1) / kJoinWaves);
 #pragma unroll 4
     for (int e = 0; e < cn; ++e) {
       const float fe = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), e));
 #pragma unroll
       for (int d = 0; d < D / 64; ++d)
-        o[d] = __builtin_fmaf(load_g(a.part + (at + b + kAttnWaves * e) * D + lane + 64 * d), fe, o[d]);
+        o[d] = __builtin_fmaf(load_g(a.part + (at + b + kJoinWaves * e) * D + lane + 64 * d), fe, o[d]);
     }
   }
   if (lane == 0) sml[wave][0] = m, sml[wave][1] = l;
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) so[wave][lane + 64 * d] = o[d];
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 64 * kAttnWaves) {
+  for (int d = threadIdx.x; d < D; d += 64 * kJoinWaves) {
     float mm = kNegInf, ls = 0.0f, os = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sml[w][0]);
+    for (int w = 0; w < kJoinWaves; ++w) mm = fmaxf(mm, sml[w][0]);
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < kJoinWaves; ++w) {
       const float f = sml[w][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][0] - mm);
       ls = __builtin_fmaf(sml[w][1], f, ls);
       os = __builtin_fmaf(so[w][d], f, os);
@@ -555,16 +809,20 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_join_kernel(AttnArgs a) 
   }
 }
 
-constexpr int kWgPerCu = 4;
-
-// 16-row tiles per workgroup; 0: eight rows in a packed tile.
-int attn_tiles(int64_t rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : 2; }
+// 16-row tiles per workgroup (or per wave, for prompts).
+AttnKind attn_kind(int64_t rows) {
+  return rows <= 8 ? ATTN_PACKED : rows <= 16 ? ATTN_16 : rows <= 64 ? ATTN_32 : ATTN_PROMPT;
+}
+int attn_rows(AttnKind k) { return k == ATTN_PACKED ? 8 : k == ATTN_16 ? 16 : k == ATTN_32 ? 32 : 128; }
 
 template <int D>
-void launch_tiles(int nt, dim3 grid, dim3 block, const AttnArgs& a, hipStream_t s) {
-  if (nt == 0) hipLaunchKernelGGL((attn_kernel<D, 1, true>), grid, block, 0, s, a);
-  else if (nt == 1) hipLaunchKernelGGL((attn_kernel<D, 1, false>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_kernel<D, 2, false>), grid, block, 0, s, a);
+void launch_kind(AttnKind k, dim3 grid, dim3 block, const AttnArgs& a, hipStream_t s) {
+  switch (k) {
+    case ATTN_PACKED: hipLaunchKernelGGL((attn_kernel<D, 1, true, 4>), grid, block, 0, s, a); break;
+    case ATTN_16: hipLaunchKernelGGL((attn_kernel<D, 1, false, 4>), grid, block, 0, s, a); break;
+    case ATTN_32: hipLaunchKernelGGL((attn_kernel<D, 2, false, 4>), grid, block, 0, s, a); break;
+    case ATTN_PROMPT: hipLaunchKernelGGL((attn_prompt_kernel<D>), grid, block, 0, s, a); break;
+  }
 }
 
 }  // namespace
@@ -572,21 +830,25 @@ void launch_tiles(int nt, dim3 grid, dim3 block, const AttnArgs& a, hipStream_t 
 AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   AttnPlan p;
   const int64_t G = Hq / kv.H, rows = kv.max_new * G;
-  p.nt = attn_tiles(rows);
-  const int64_t tile = p.nt == 0 ? 8 : 16 * p.nt;
+  p.kind = attn_kind(rows);
+  const int64_t tile = attn_rows(p.kind);
   p.row_tiles = (rows + tile - 1) / tile;
-  // Chunks: enough workgroups to fill the chip a few times over, each at
-  // least one step per wave.
   const int64_t most = kv.ld_table << kv.log_p;
   const int64_t len = kv.max_len > 0 ? std::min(kv.max_len, most) : most;
   const int64_t units = mul_sat(kv.S * kv.H, p.row_tiles);
-  const int64_t step = kStep * kAttnWaves;
-  const int64_t want = std::max<int64_t>(1, (int64_t)cus * kWgPerCu / std::max<int64_t>(1, units));
-  const int64_t chunk = std::max<int64_t>(step, ((len + want - 1) / want + step - 1) / step * step);
+  p.waves = 4;
+  const int64_t step = kStep * p.waves;
+  // Positions per workgroup.  One sequence: what gives every CU one workgroup;
+  // several, ragged as a rule: two, and pieces short enough to even them out.
+  const int64_t want = std::max<int64_t>(1, cus * (kv.S > 1 ? 2 : 1) / units);
+  int64_t chunk = (len + want - 1) / want;
+  if (units < 4 * cus && kv.S > 1) chunk = std::min(chunk, std::max<int64_t>(1280, len / 8));
+  if (units >= cus / 2 && len <= 1024) chunk = len;
+  chunk = std::max<int64_t>(step, (chunk + step - 1) / step * step);
   p.chunk = std::min<int64_t>(chunk, 1ll << 30);
   p.nchunk = std::max<int64_t>(1, (len + p.chunk - 1) / p.chunk);
-  p.work_items = mul_sat(mul_sat(units, p.nchunk), 64 * kAttnWaves);
-  p.join_items = p.nchunk > 1 ? mul_sat(mul_sat(kv.S * kv.max_new, Hq), 64 * kAttnWaves) : 0;
+  p.work_items = mul_sat(mul_sat(units, p.nchunk), 64 * p.waves);
+  p.join_items = p.nchunk > 1 ? mul_sat(mul_sat(kv.S * kv.max_new, Hq), 64 * kJoinWaves) : 0;
   p.workspace = p.nchunk > 1 ? mul_sat((int64_t)kv.rows * Hq, p.nchunk * (kv.D + 2) * 4) : 0;
   return p;
 }
@@ -607,17 +869,21 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   a.nchunk = (int32_t)p.nchunk;
   a.row_tiles = (int32_t)p.row_tiles;
   a.scale = scale;
-  a.q16 = reinterpret_cast<uintptr_t>(q) % 16 == 0 && (kv.rows == 1 || ldq % 4 == 0);
-  const dim3 grid((unsigned)(p.work_items / (64 * kAttnWaves))), block(64 * kAttnWaves);
+  auto rows16 = [&](const float* p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (kv.rows == 1 || ld % 4 == 0);
+  };
+  a.q16 = rows16(q, ldq);
+  a.y16 = rows16(y, ldy);
+  const dim3 grid((unsigned)(p.work_items / (64 * p.waves))), block(64 * p.waves), jblock(64 * kJoinWaves);
   if (kv.D == 64)
-    launch_tiles<64>(p.nt, grid, block, a, s);
+    launch_kind<64>(p.kind, grid, block, a, s);
   else
-    launch_tiles<128>(p.nt, grid, block, a, s);
+    launch_kind<128>(p.kind, grid, block, a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.nchunk == 1) return e;
-  const dim3 jgrid((unsigned)(p.join_items / (64 * kAttnWaves)));
-  if (kv.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, block, 0, s, a);
+  const dim3 jgrid((unsigned)(p.join_items / jblock.x));
+  if (kv.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, jblock, 0, s, a);
+  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, jblock, 0, s, a);
   return hipGetLastError();
 }
 

@@ -298,8 +298,10 @@ struct KvArgs {
 int64_t kv_append_work_items(const KvArgs& a);
 hipError_t launch_kv_append(const KvArgs& a, const float* k, int64_t ldk, const float* v, int64_t ldv, hipStream_t s);
 // tern_attn.hip: how a call's rows and positions are split over workgroups
+enum AttnKind { ATTN_PACKED, ATTN_16, ATTN_32, ATTN_PROMPT };  // 8, 16, 32, 128 rows per workgroup
 struct AttnPlan {
-  int nt;             // 16-row tiles of a workgroup (0: eight rows, packed)
+  AttnKind kind;
+  int waves;          // waves of a workgroup
   int64_t row_tiles;  // row tiles of a sequence and KV head
   int64_t chunk, nchunk;
   int64_t work_items, join_items, workspace;

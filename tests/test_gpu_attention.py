@@ -157,3 +157,26 @@ def test_rows_past_max_new():
     pg = Paged(2, 5, 2, 128, 32, seed=12).upload()
     got = attend(pg, [6, 2], [130, 40], 8, max_new=4)
     assert (got[4:6] == 77).all()
+
+
+# prompts: row tiles of 128 that end inside a token's heads, inside a wave and inside a step, windows of pages, splits
+@pytest.mark.parametrize("new,length,heads,group,P,D", [
+    ([130, 1, 77], [130, 40, 300], 2, 4, 16, 128), ([33, 64], [700, 64], 1, 3, 64, 64),
+    ([200], [4500], 1, 2, 32, 128), ([65, 128], [5000, 4097], 1, 1, 128, 128), ([17, 40], [17, 1000], 2, 8, 64, 64),
+    ([300], [300], 1, 5, 16, 64)])
+def test_prompts(new, length, heads, group, P, D):
+    pg = Paged(len(new), -(-max(length) // P), heads, D, P, seed=13).upload()
+    attend(pg, new, length, heads * group, max_len=max(length))
+    attend(pg, new, length, heads * group, max_len=64, extra=3)
+
+
+def test_prompt_with_bad_pages_and_scales():
+    def scales(rng, shape):
+        s = 10.0 ** rng.uniform(-6, 3, shape)
+        s[0] = rng.uniform(0.005, 0.02, shape[1:])
+        s[1][rng.random(shape[1:]) < 0.2] = 0
+        return s
+    pg = Paged(3, 20, 2, 128, 16, seed=14, scales=scales).upload()
+    pg.table[0, [0, 3, 7]], pg.table[1, :] = -1, pg.host.pages
+    got = attend(pg, [40, 70, 90], [300, 200, 90], 8, rows=230)
+    assert (got[40:110] == 0).all() and (got[200:] == 77).all()
