@@ -119,8 +119,10 @@ __device__ __forceinline__ float pow2i(int e) { return __builtin_bit_cast(float,
 
 // Maximum / sum over the four lanes that hold one query row.
 __device__ __forceinline__ float max_groups(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+  p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
 }
 __device__ __forceinline__ float sum_groups(float v) {
   v += __shfl_xor(v, 16, 64);
@@ -183,12 +185,11 @@ __device__ __forceinline__ float split_query(float scale, float (&x)[D / 4], f16
 constexpr float kBias = -128.0f / 16777216.0f;  // times a row's sum: where its scores start (codes_sub)
 
 // The V scale of the lane's 16 positions in a step.  Weights take it with the
-// exponential: e^(s - m) vn = 2^(s' - m' + log2 vn), vn = vs * 2^(14 - ve) <=
-// 2^15, and sums of weights are divided by it.  A scale of 0, or far below
-// the largest, is multiplied afterwards (`apart`).
+// exponential: e^(s - m) vn = 2^(s' - m' + lv), vn = vs * 2^(14 - ve) = 2^lv
+// <= 2^15, and sums of weights are multiplied by rl = 2^-lv.  (Far below the
+// largest scale, 0 included, lv ends at -40: those weights are 0 as fp16.)
 struct VScale {
-  float vn, lv, rl;
-  bool apart, any_apart;
+  float lv, rl;
 };
 // `ve` is the exponent of the largest V scale met: where this step's is
 // larger, the sums so far move to its power of two.
@@ -204,20 +205,15 @@ __device__ __forceinline__ VScale v_scale(float vs, int& ve, f32x4 (&o)[NT][DT])
       for (int d = 0; d < DT; ++d) o[u][d] *= f;
     ve = e;
   }
-  VScale v;
-  v.vn = vs * pow2i(14 - ve);
-  v.apart = v.vn < 0x1p-16f;
-  v.lv = v.apart ? 0.0f : __builtin_amdgcn_logf(v.vn);
-  v.rl = v.apart ? 1.0f : __builtin_amdgcn_rcpf(v.vn);
-  v.any_apart = __any(v.apart);
-  return v;
+  const float lv = fmaxf(__builtin_amdgcn_logf(vs * pow2i(14 - ve)), -40.0f);
+  return {lv, __builtin_amdgcn_exp2f(-lv)};
 }
-// One row's 16 scores of a step (times f: in units of log2) to weights p; m,
-// l and o follow a larger maximum.  Where `masked`, only positions up to
+// One row's 16 scores of a step (times f: in units of log2): the running
+// maximum m, which l and o follow.  Where `masked`, only positions up to
 // `last` of the lane's 16 count.
 template <int DT>
-__device__ __forceinline__ void softmax_step(f32x4 (&sc)[4], float f, bool masked, int last, const VScale& v, float& m,
-                                             float& l, f32x4 (&o)[DT], float (&p)[16]) {
+__device__ __forceinline__ void row_maximum(f32x4 (&sc)[4], float& f, bool masked, int last, float& m, float& l,
+                                            f32x4 (&o)[DT]) {
   if (masked) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
@@ -235,20 +231,30 @@ __device__ __forceinline__ void softmax_step(f32x4 (&sc)[4], float f, bool maske
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] *= al;
   }
+}
+// and their weights, as operands of the second product (high and low).
+__device__ __forceinline__ void row_weights(const f32x4 (&sc)[4], float f, const VScale& v, float m, float& l,
+                                            f16x8 (&hi)[2], f16x8 (&lo)[2]) {
   const float off = v.lv - (m == kNegInf ? 0.0f : m);
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 2][i & 3], f, off));
-    sum += p[i];
-  }
-  l = __builtin_fmaf(sum, v.rl, l);
-  if (v.any_apart) {
-    const float mul = v.apart ? v.vn : 1.0f;
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) p[i] *= mul;
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int e = 8 * k + 2 * i;
+      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e >> 2][e & 3], f, off));
+      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e >> 2][(e & 3) + 1], f, off));
+      sum += p0 + p1;
+      f16x2 h, r;
+      split2(p0, p1, h, r);
+      hi[k][2 * i] = h[0], hi[k][2 * i + 1] = h[1];
+      lo[k][2 * i] = r[0], lo[k][2 * i + 1] = r[1];
+    }
+  l = __builtin_fmaf(sum, v.rl, l);
 }
+
+// see attn_prompt_kernel
+__device__ __forceinline__ int swizzle(int g) { return (0x84C0 >> (4 * g)) & 15; }
 
 // One workgroup: one (sequence, KV head), 16 * NT rows (row i: new token i /
 // G, query head i % G of the KV head's), one chunk of the positions, whose
@@ -437,18 +443,22 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
       f16x8 pb[NT][2][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float p[16];
-        softmax_step<DT>(sc[u], qfac[16 * u + n] * ks, masked, here ? pos[u] - jv : -1, v, m[u], l[u], o[u], p);
+        float f = qfac[16 * u + n] * ks;
+        row_maximum<DT>(sc[u], f, masked, here ? pos[u] - jv : -1, m[u], l[u], o[u]);
+        f16x8 hi[2], lo[2];
+        row_weights(sc[u], f, v, m[u], l[u], hi, lo);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (PACK) {
+            const u32x4 a4 = __builtin_bit_cast(u32x4, hi[k]), b4 = __builtin_bit_cast(u32x4, lo[k]);
+            u32x4 c4;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f16x2 hi, lo;
-            split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
-            if constexpr (PACK) hi = low ? lo : hi;
-            pb[u][k][0][2 * i] = hi[0], pb[u][k][0][2 * i + 1] = hi[1];
-            pb[u][k][1][2 * i] = lo[0], pb[u][k][1][2 * i + 1] = lo[1];
+            for (int i = 0; i < 4; ++i) c4[i] = low ? b4[i] : a4[i];
+            hi[k] = __builtin_bit_cast(f16x8, c4);
           }
+          pb[u][k][0] = hi[k];
+          pb[u][k][1] = lo[k];
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -536,9 +546,11 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 // all positions.  Each step's 64 positions are converted to fp16 once, by all
 // the waves, into one of two LDS buffers, laid out as the products read them
 // (16 bytes per lane, a whole kilobyte per instruction), so a wave's 32 rows
-// cost a quarter of the conversions and every operand read is free of bank
-// conflicts: slot (n ^ 4 g) of lane group g keeps the writes, whose lanes run
-// over g and the low bits of n, off each other's banks too.  The codes of the
+// cost a quarter of the conversions.  Operand n of lane group g is in slot
+// 16 g + (n ^ swizzle(g)): writes run over g and the low bits of n, reads
+// over n, and 16-byte accesses are served sixteen lanes at a time as 0-3,
+// 12-15, 20-27 and so on; these four constants keep both off each other's
+// banks (4 g had half of the read cycles lost to conflicts).  The codes of the
 // step after the next are on their way to registers meanwhile.  Two
 // workgroups per CU: one's matrix instructions run beside the other's
 // exponentials.  Matrix bound: four products (two halves each of Q and P)
@@ -572,7 +584,11 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
 
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int n = lane & 15, g = lane >> 4;
-  const int slot = 16 * g + (n ^ (4 * g));
+  const int slot = 16 * g + (n ^ swizzle(g));
+
+  // (of two workgroups on a CU the second's waves go first: out of step, one's
+  // products fill the other's exponentials; 261 -> 249 us)
+  if ((blockIdx.x >> 8) & 1) __builtin_amdgcn_s_setprio(1);
 
   f16x8 qh[NT][KS], ql[NT][KS];
   float qfac[NT], qbias[NT];
@@ -633,11 +649,11 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       int tok, i;
       k_piece(e, tok, i);
       const int r = tok & 15, kn = 4 * (tok >> 4) + (r & 3);
-      const int at = 16 * pg + (kn ^ (4 * pg));
+      const int at = 16 * pg + (kn ^ swizzle(pg));
       kf[buf][r >> 2][2 * i][at] = codes_sub(kraw[e][0], kraw[e][1]);
       kf[buf][r >> 2][2 * i + 1][at] = codes_sub(kraw[e][2], kraw[e][3]);
       const int d = (t >> 2) + 64 * e;
-      const int vt = 16 * pg + ((d & 15) ^ (4 * pg));
+      const int vt = 16 * pg + ((d & 15) ^ swizzle(pg));
       vf[buf][d >> 4][0][vt] = codes_f16(vraw[e][0], vraw[e][1]);
       vf[buf][d >> 4][1][vt] = codes_f16(vraw[e][2], vraw[e][3]);
     }
@@ -664,58 +680,74 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       // this step's operands are written; every wave is past the step before,
       // whose buffer the next step's go to
       __syncthreads();
-      f32x4 sc[NT][4];
-#pragma unroll
-      for (int u = 0; u < NT; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[u][e] = {qbias[u], qbias[u], qbias[u], qbias[u]};
-#pragma unroll
-      for (int j = 0; j < KS; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f16x8 k = kf[buf][e][j][slot];
-#pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            sc[u][e] = mfma(k, qh[u][j], sc[u][e]);
-            sc[u][e] = mfma(k, ql[u][j], sc[u][e]);
-          }
-        }
-      if (st + 1 < steps) {
-        write_codes(buf ^ 1);
-        if (st + 2 < steps) load_codes(st + 2);
-      }
       const int64_t j0 = w0 + kStep * st;
       const int32_t jv = (int32_t)j0 + 16 * g;
       const bool here = page[4 * st + g] >= 0;
       const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
       const VScale v = v_scale<DT>(vs, ve, o);
       const bool masked = j0 + kStep > all_see || __any(!here);
-      f16x8 pb[NT][2][2];
+      f32x4 sc[NT][4];
+      f16x8 hi[NT][2], lo[NT][2];
+      float f[NT];
+      // Both products: the next four operands are read while the matrix
+      // instructions of these four run (sixteen; the high halves first, so
+      // that none waits for the one before it).
+      f16x8 fr[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) fr[0][e] = kf[buf][e][0][slot];
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[u][e] = {qbias[u], qbias[u], qbias[u], qbias[u]};
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        if (j + 1 < KS) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) fr[(j + 1) & 1][e] = kf[buf][e][j + 1][slot];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int u = 0; u < NT; ++u) sc[u][e] = mfma(fr[j & 1][e], qh[u][j], sc[u][e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int u = 0; u < NT; ++u) sc[u][e] = mfma(fr[j & 1][e], ql[u][j], sc[u][e]);
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 16, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // (after the last step: codes that no one reads)
+      write_codes(buf ^ 1);
+      load_codes(min(st + 2, steps - 1));
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float p[16];
-        softmax_step<DT>(sc[u], qfac[u] * ks, masked, here ? pos[u] - jv : -1, v, m[u], l[u], o[u], p);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f16x2 hi, lo;
-            split2(p[8 * k + 2 * i], p[8 * k + 2 * i + 1], hi, lo);
-            pb[u][k][0][2 * i] = hi[0], pb[u][k][0][2 * i + 1] = hi[1];
-            pb[u][k][1][2 * i] = lo[0], pb[u][k][1][2 * i + 1] = lo[1];
-          }
+        f[u] = qfac[u] * ks;
+        row_maximum<DT>(sc[u], f[u], masked, here ? pos[u] - jv : -1, m[u], l[u], o[u]);
+        row_weights(sc[u], f[u], v, m[u], l[u], hi[u], lo[u]);
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int e = 0; e < 4; ++e) fr[0][e] = vf[buf][e][0][slot];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const f16x8 w = vf[buf][d][k][slot];
+      for (int x = 0; x < DT / 2; ++x) {  // four dims' tiles of one half of the positions
+        const int k = x / (DT / 4), d0 = 4 * (x % (DT / 4));
+        if (x + 1 < DT / 2) {
 #pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            o[u][d] = mfma(w, pb[u][k][0], o[u][d]);
-            o[u][d] = mfma(w, pb[u][k][1], o[u][d]);
-          }
+          for (int e = 0; e < 4; ++e)
+            fr[(x + 1) & 1][e] = vf[buf][4 * ((x + 1) % (DT / 4)) + e][(x + 1) / (DT / 4)][slot];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int u = 0; u < NT; ++u) o[u][d0 + e] = mfma(fr[x & 1][e], hi[u][k], o[u][d0 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int u = 0; u < NT; ++u) o[u][d0 + e] = mfma(fr[x & 1][e], lo[u][k], o[u][d0 + e]);
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 1);
+        __builtin_amdgcn_sched_group_barrier(0x008, 16, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 
