@@ -56,6 +56,16 @@ __device__ __forceinline__ void wg_range(float& lo, float& hi, float (*red)[16])
   for (int i = 0; i < T / 64; ++i) lo = fminf(lo, red[0][i]), hi = fmaxf(hi, red[1][i]);
 }
 
+// act_code of a row's scale, with the quotient from the reciprocal and the
+// division only where that lies near a border between two codes: it is off by
+// at most 255 * 2^-22.
+__device__ __forceinline__ int32_t row_code(float y, float s, float inv, int32_t zm) {
+  const float v = y * inv;
+  float c = __builtin_rintf(v);
+  if (!(fabsf(v - c) < 0.4999f)) c = __builtin_rintf(__fdiv_rn(y, s));  // (also where the reciprocal overflows)
+  return min(127, max(-128, (int32_t)c + zm));
+}
+
 __device__ __forceinline__ float normed(float h, double r, float gain) {
   return (float)((double)h * r * (double)gain);
 }
@@ -96,6 +106,18 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
       }
     }
   }
+  // (the gains are on their way while the sum is joined)
+  f32x4 gain[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    gain[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (VEC) {
+      if (col(v, 0) < K) gain[v] = __builtin_bit_cast(f32x4, load16(a.gain + col(v, 0)));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) gain[v][c] = col(v, c) < K ? load_g(a.gain + col(v, c)) : 0.0f;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -120,16 +142,9 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
   float lo = 0.0f, hi = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (VEC) {
-      if (col(v, 0) < K) g = __builtin_bit_cast(f32x4, load16(a.gain + col(v, 0)));
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) g[c] = col(v, c) < K ? load_g(a.gain + col(v, c)) : 0.0f;
-    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      val[v][c] = normed(val[v][c], r, g[c]);
+      val[v][c] = normed(val[v][c], r, gain[v][c]);
       lo = fminf(lo, val[v][c]);
       hi = fmaxf(hi, val[v][c]);
     }
@@ -138,18 +153,19 @@ __global__ __launch_bounds__(T) void norm_kernel(NormArgs a) {
   float s;
   int32_t zm;
   act_params(lo, hi, s, zm);
+  const float inv = __fdiv_rn(1.0f, s);
   int8_t* q = a.q + m * a.ldq;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (VEC) {
       uint32_t word = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) word |= ((uint32_t)act_code(val[v][c], s, zm) & 0xffu) << (8 * c);
+      for (int c = 0; c < 4; ++c) word |= ((uint32_t)row_code(val[v][c], s, inv, zm) & 0xffu) << (8 * c);
       if (col(v, 0) < K) store_g(reinterpret_cast<uint32_t*>(q + col(v, 0)), word);
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (col(v, c) < K) store_g(q + col(v, c), (int8_t)act_code(val[v][c], s, zm));
+        if (col(v, c) < K) store_g(q + col(v, c), (int8_t)row_code(val[v][c], s, inv, zm));
     }
   }
   if (t == 0) {
@@ -220,12 +236,19 @@ hipError_t launch_rmsnorm_quantize(const float* x, int64_t ldx, const float* res
     return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (M == 1 || ld % 4 == 0));
   };
   const bool vec = K % 4 == 0 && rows16(x, ldx) && rows16(res, ldr) && rows16(h, ldh) && rows16(gain, 0);
+  // A few rows: as many threads as the row has groups, for the latency of one
+  // row (4,096 columns: 4.2 us).  From a row per CU on: fewer, longer threads,
+  // several rows per CU (512 x 4,096: 10.2 -> 8.5 us, 4,096 x 2,048: 38 -> 28,
+  // 4,096 x 4,096: 58 -> 50).
+  const bool many = M >= 256;
   if (K <= 1024)
     launch_rows<256, 1>(vec, M, a, s);
+  else if (K <= 2048 && many)
+    launch_rows<256, 2>(vec, M, a, s);
   else if (K <= 4096)
-    launch_rows<1024, 1>(vec, M, a, s);
+    many ? launch_rows<256, 4>(vec, M, a, s) : launch_rows<1024, 1>(vec, M, a, s);
   else if (K <= 8192)
-    launch_rows<1024, 2>(vec, M, a, s);
+    many ? launch_rows<512, 4>(vec, M, a, s) : launch_rows<1024, 2>(vec, M, a, s);
   else if (K <= 16384)
     launch_rows<1024, 4>(vec, M, a, s);
   else
