@@ -46,6 +46,24 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kStep = 64;  // positions per step of a wave
 constexpr int kJoinWaves = 4;
 
+// n / d for 0 <= n < 2^31 by a multiplication (an integer division is some
+// thirty instructions, and a workgroup begins with several).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+  __device__ __forceinline__ uint32_t divmod(uint32_t n, uint32_t& rem) const {
+    const uint32_t q = div(n);
+    rem = n - q * d;
+    return q;
+  }
+};
+inline FastDiv fast_div(int64_t d) {  // d in [1, 2^31)
+  FastDiv f = {(uint32_t)d, 0, 0};
+  while ((1ull << f.shift) < (uint64_t)d) ++f.shift;
+  f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - (uint64_t)d)) / (uint64_t)d + 1);
+  return f;
+}
+
 struct AttnArgs {
   KvArgs kv;
   const float* q;
@@ -53,9 +71,10 @@ struct AttnArgs {
   float* part;  // per (row, head, chunk): D sums, then m and l per (row, head, chunk)
   float* part_ml;
   int64_t ldq, ldy;
-  int32_t Hq, G;
+  int32_t Hq;
   int32_t chunk, nchunk;  // positions per chunk, chunks a sequence is split into
   int32_t row_tiles;
+  FastDiv by_h, by_chunks, by_tiles, by_g;  // KV heads, chunks, row tiles, query heads per KV head
   float scale;
   bool q16, y16;  // query rows, output rows are 16-byte aligned
 };
@@ -152,35 +171,35 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const float* q, in
   }
 }
 
-// A query row's operands, high and low: the row times a power of two that
-// brings its largest element to [2^8, 2^9) (and the sign of the scale, so
-// that the factor of its scores is not negative).  Returns that factor,
-// |scale| * log2(e) * the powers of two left out; `sum_h` and `sum_l` get the
-// sums of the halves over the row.
+// The power of two that brings a query row's largest element to [2^8, 2^9),
+// with the sign of the scale (so that the factor of its scores is not
+// negative), and that factor: |scale| * log2(e) * the powers of two left out.
+struct QueryScale {
+  float up, factor;
+};
 template <int D>
-__device__ __forceinline__ float split_query(float scale, float (&x)[D / 4], f16x8 (&qh)[D / 32], f16x8 (&ql)[D / 32],
-                                             float& sum_h, float& sum_l) {
+__device__ __forceinline__ QueryScale query_scale(float scale, const float (&x)[D / 4]) {
   float amax = 0.0f;
 #pragma unroll
   for (int j = 0; j < D / 4; ++j) amax = fmaxf(amax, fabsf(x[j]));
   amax = max_groups(amax);
   const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
   const float up = scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
+  return {up, fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f};
+}
+// One k step's operands, high and low, and their sums.
+__device__ __forceinline__ void split_query(const float (&x)[8], float up, f16x8& qh, f16x8& ql, float& sum_h,
+                                            float& sum_l) {
   sum_h = sum_l = 0.0f;
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f16x2 hi, lo;
-      split2(x[8 * j + 2 * i] * up, x[8 * j + 2 * i + 1] * up, hi, lo);
-      qh[j][2 * i] = hi[0], qh[j][2 * i + 1] = hi[1];
-      ql[j][2 * i] = lo[0], ql[j][2 * i + 1] = lo[1];
-      sum_h += (float)hi[0] + (float)hi[1];
-      sum_l += (float)lo[0] + (float)lo[1];
-    }
-  sum_h = sum_groups(sum_h);
-  sum_l = sum_groups(sum_l);
-  return fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f;
+  for (int i = 0; i < 4; ++i) {
+    f16x2 hi, lo;
+    split2(x[2 * i] * up, x[2 * i + 1] * up, hi, lo);
+    qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
+    ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
+    sum_h += (float)hi[0] + (float)hi[1];
+    sum_l += (float)lo[0] + (float)lo[1];
+  }
 }
 constexpr float kBias = -128.0f / 16777216.0f;  // times a row's sum: where its scores start (codes_sub)
 
@@ -277,24 +296,21 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   };
   __shared__ Share sh;
   __shared__ float sml[W][16 * NT][2];
-  // a row's |scale| * log2(e) * powers of two, and where its sums start
-  __shared__ float qfac[16 * NT], qbias[16 * NT];
+  // a row's |scale| * log2(e) * powers of two, and the sums of its operands
+  __shared__ float qfac[16 * NT], qsum[KS][16 * NT];
   __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
   __shared__ float kscale[kGroups], vscale[kGroups];
 
   const KvArgs& kv = a.kv;
-  int b = blockIdx.x;
-  const int h = b % kv.H;
-  b /= kv.H;
-  const int c = b % a.nchunk;
-  b /= a.nchunk;
-  const int rt = a.row_tiles - 1 - b % a.row_tiles;
-  const int s = b / a.row_tiles;
+  uint32_t h, cu, tile;
+  const int s = (int)a.by_tiles.divmod(a.by_chunks.divmod(a.by_h.divmod(blockIdx.x, h), cu), tile);
+  const int c = (int)cu, G = (int)a.by_g.d;
+  const int rt = a.row_tiles - 1 - (int)tile;
   const SeqView sv = seq_view(kv, s);
-  const int rows = min(sv.n, (int)kv.max_new) * a.G, row_lo = rt * ROWS;
+  const int rows = min(sv.n, (int)kv.max_new) * G, row_lo = rt * ROWS;
   if (row_lo >= rows) return;
   // positions that some row of the tile sees: up to the last row's own
-  const int64_t last_pos = sv.pos0 + min(row_lo + ROWS - 1, rows - 1) / a.G;
+  const int64_t last_pos = sv.pos0 + (int)a.by_g.div(min(row_lo + ROWS - 1, rows - 1));
   const int64_t end = min(sv.len, last_pos + 1);
   const int64_t c0 = (int64_t)c * a.chunk;
   const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
@@ -307,42 +323,52 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   const bool low = PACK && n >= 8;  // the lane holds low operands
 
   // Loads in three trips to memory: the sequence; page ids and query rows;
-  // scales, K and V.  Wave u prepares query tile u, for all the waves, while
-  // its first K and V are under way.
+  // scales, K and V.  The query operands are prepared by all the waves, some k
+  // steps of one tile each, while the first K and V are under way.
+  constexpr int PREP = NT * KS > W ? NT * KS / W : 1;  // operands per wave
+  const int pu = wave * PREP / KS, pj = wave * PREP % KS;
+  const bool prepares = wave * PREP < NT * KS;
   float x[D / 4];
-  if (wave < NT) {
-    const int r = row_lo + 16 * wave + nr;
-    const bool live = r < rows;
+  if (prepares) {
+    const int r = row_lo + 16 * pu + nr;
     // (a row past the last reads the sequence's first, for zeros)
-    load_query<D>(a, a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
-                         (int64_t)(h * a.G + (live ? r % a.G : 0)) * D, g, x);
+    uint32_t rem;
+    const int i = (int)a.by_g.divmod(r < rows ? r : 0, rem);
+    load_query<D>(a, a.q + (int64_t)(sv.row0 + i) * a.ldq + (int64_t)(h * G + rem) * D, g, x);
   }
   auto prepare_q = [&]() {
-    const bool live = row_lo + 16 * wave + nr < rows;
+    const bool live = row_lo + 16 * pu + nr < rows;
 #pragma unroll
     for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
-    f16x8 qh[KS], ql[KS];
-    float sum_h, sum_l;
-    const float f = split_query<D>(a.scale, x, qh, ql, sum_h, sum_l);
+    const QueryScale f = query_scale<D>(a.scale, x);
+    if (g == 0 && pj == 0) qfac[16 * pu + n] = f.factor;
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      if constexpr (PACK) {
-        sh.q[wave][j][0][lane] = low ? ql[j] : qh[j];
-      } else {
-        sh.q[wave][j][0][lane] = qh[j];
-        sh.q[wave][j][1][lane] = ql[j];
+    for (int i = 0; i < PREP; ++i) {
+      f16x8 qh, ql;
+      float sum_h, sum_l;
+      float part[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        part[e] = x[8 * i + e];
+#pragma unroll
+        for (int j = 1; j < KS / PREP; ++j) part[e] = pj == j * PREP ? x[8 * (j * PREP + i) + e] : part[e];
       }
-    }
-    if (g == 0) {
-      qfac[16 * wave + n] = f;
-      qbias[16 * wave + n] = kBias * (PACK ? (low ? sum_l : sum_h) : sum_h + sum_l);
+      split_query(part, f.up, qh, ql, sum_h, sum_l);
+      if constexpr (PACK) {
+        sh.q[pu][pj + i][0][lane] = low ? ql : qh;
+      } else {
+        sh.q[pu][pj + i][0][lane] = qh;
+        sh.q[pu][pj + i][1][lane] = ql;
+      }
+      const float s = sum_groups(PACK ? (low ? sum_l : sum_h) : sum_h + sum_l);
+      if (g == 0) qsum[pj + i][16 * pu + n] = s;
     }
   };
   int32_t pos[NT];  // last position that the row sees (-1: none)
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     const int r = row_lo + 16 * u + nr;
-    pos[u] = r < rows ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
+    pos[u] = r < rows ? (int32_t)max(min(sv.pos0 + (int)a.by_g.div(r), sv.len - 1), (int64_t)-1) : -1;
   }
 
   f32x4 o[NT][DT];
@@ -357,7 +383,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   int ve = -100;  // o holds sums of code * weight * 2^(14 - ve)
 
   // position of the tile that every row sees: below it no mask is needed
-  const int64_t all_see = min(sv.len, sv.pos0 + row_lo / a.G + 1);
+  const int64_t all_see = min(sv.len, sv.pos0 + (int)a.by_g.div(row_lo) + 1);
   const int P = 1 << kv.log_p;
   u32x4 kw[4][D / 64], vw[DT];
   int64_t w0 = c0;
@@ -381,8 +407,9 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) vw[d] = load16(vp + ((int64_t)(16 * d) << kv.log_p));
   };
-  // The pages and scales of the window at w0, and its first loads.
-  auto open_window = [&]() {
+  // The pages and scales of the window at w0, and its first loads; `meanwhile`
+  // is done while those are on their way.
+  auto open_window = [&](auto meanwhile) {
     const int64_t j = w0 + 16 * (int)threadIdx.x;
     const int32_t id = j < sv.len ? page_of(kv, s, j >> kv.log_p) : -1;
     const int64_t si = (int64_t)max(id, 0) * kv.H + h;
@@ -394,18 +421,30 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
       load_k(wave);
       load_v(wave);
     }
+    meanwhile();
+    // (this waits for K and V too: loads return in order, and not every wave has some)
     kscale[threadIdx.x] = id < 0 ? 0.0f : ks;
     vscale[threadIdx.x] = id < 0 ? 0.0f : vs;
   };
-  open_window();
-  if (wave < NT) prepare_q();
+  open_window([&]() {
+    if (prepares) prepare_q();
+  });
   __syncthreads();
+  float fac[NT], bias[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    fac[u] = qfac[16 * u + n];
+    bias[u] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) bias[u] += qsum[j][16 * u + n];
+    bias[u] *= kBias;
+  }
   for (;;) {
     f32x4 sc[NT][4];
     auto scores = [&]() {
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        const float b = qbias[16 * u + n];
+        const float b = bias[u];
 #pragma unroll
         for (int t = 0; t < 4; ++t) sc[u][t] = {b, b, b, b};
       }
@@ -416,13 +455,19 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int e = 0; e < (PACK ? 1 : 2); ++e) q[u][e] = sh.q[u][j][e][lane];
+        // (the high halves first: no instruction waits for the one before it)
+        f16x8 kf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const f16x8 kf = codes_sub(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
+          kf[t] = codes_sub(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
 #pragma unroll
-          for (int u = 0; u < NT; ++u)
+          for (int u = 0; u < NT; ++u) sc[u][t] = mfma(kf[t], q[u][0], sc[u][t]);
+        }
+        if constexpr (!PACK) {
 #pragma unroll
-            for (int e = 0; e < (PACK ? 1 : 2); ++e) sc[u][t] = mfma(kf, q[u][e], sc[u][t]);
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) sc[u][t] = mfma(kf[t], q[u][1], sc[u][t]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -443,7 +488,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
       f16x8 pb[NT][2][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float f = qfac[16 * u + n] * ks;
+        float f = fac[u] * ks;
         row_maximum<DT>(sc[u], f, masked, here ? pos[u] - jv : -1, m[u], l[u], o[u]);
         f16x8 hi[2], lo[2];
         row_weights(sc[u], f, v, m[u], l[u], hi, lo);
@@ -464,12 +509,20 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const f16x8 vf = codes_f16(vw[d][2 * k], vw[d][2 * k + 1]);
+        for (int d0 = 0; d0 < DT; d0 += 4) {
+          f16x8 vf[4];
 #pragma unroll
-          for (int u = 0; u < NT; ++u)
+          for (int d = 0; d < 4; ++d) {
+            vf[d] = codes_f16(vw[d0 + d][2 * k], vw[d0 + d][2 * k + 1]);
 #pragma unroll
-            for (int e = 0; e < (PACK ? 1 : 2); ++e) o[u][d] = mfma(vf, pb[u][k][e], o[u][d]);
+            for (int u = 0; u < NT; ++u) o[u][d0 + d] = mfma(vf[d], pb[u][k][0], o[u][d0 + d]);
+          }
+          if constexpr (!PACK) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+              for (int u = 0; u < NT; ++u) o[u][d0 + d] = mfma(vf[d], pb[u][k][1], o[u][d0 + d]);
+          }
         }
     };
     // (the last step apart: a load that may or may not have been issued would
@@ -489,7 +542,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
     w0 += kWindow;
     if (w0 >= c1) break;
     __syncthreads();  // (the window before has been read)
-    open_window();
+    open_window([]() {});
     __syncthreads();
   }
 
@@ -513,26 +566,35 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
       *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = v;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (PACK ? 8 : 16) * D; i += 64 * W) {
-      const int r = 16 * u + i / D, d = i % D;
+    // four dims per thread and turn
+    for (int i = threadIdx.x; i < (PACK ? 8 : 16) * (D / 4); i += 64 * W) {
+      const int rr = i / (D / 4), d = 4 * (i % (D / 4)), r = 16 * u + rr;
       if (row_lo + r >= rows) break;
       float mm = kNegInf;
 #pragma unroll
       for (int w = 0; w < W; ++w) mm = fmaxf(mm, sml[w][r][0]);
-      float ls = 0.0f, os = 0.0f;
+      float ls = 0.0f;
+      f32x4 os = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float f = sml[w][r][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sml[w][r][0] - mm);
         ls = __builtin_fmaf(sml[w][r][1], f, ls);
-        os = __builtin_fmaf(sh.o[w][i / D][d], f, os);
+        os += *reinterpret_cast<const f32x4*>(&sh.o[w][rr][d]) * f;
       }
-      const int64_t row = sv.row0 + (row_lo + r) / a.G;
-      const int hq = h * a.G + (row_lo + r) % a.G;
+      uint32_t rem;
+      const int64_t row = sv.row0 + a.by_g.divmod(row_lo + r, rem), hq = h * G + rem;
       if (a.nchunk == 1) {
-        store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls > 0.0f ? os / ls : 0.0f);
+        float* y = a.y + row * a.ldy + hq * D + d;
+        os *= ls > 0.0f ? 1.0f / ls : 0.0f;
+        if (a.y16) {
+          store_g(reinterpret_cast<f32x4*>(y), os);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store_g(y + e, os[e]);
+        }
       } else {
         const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
-        store_g(a.part + at * D + d, os);
+        store_g(reinterpret_cast<f32x4*>(a.part + at * D + d), os);
         if (d == 0) {
           store_g(a.part_ml + 2 * at, mm);
           store_g(a.part_ml + 2 * at + 1, ls);
@@ -566,17 +628,14 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
   __shared__ float kscale[kGroups], vscale[kGroups];
 
   const KvArgs& kv = a.kv;
-  int b = blockIdx.x;
-  const int h = b % kv.H;
-  b /= kv.H;
-  const int c = b % a.nchunk;
-  b /= a.nchunk;
-  const int rt = a.row_tiles - 1 - b % a.row_tiles;  // (the longest first)
-  const int s = b / a.row_tiles;
+  uint32_t h, cu, tile;
+  const int s = (int)a.by_tiles.divmod(a.by_chunks.divmod(a.by_h.divmod(blockIdx.x, h), cu), tile);
+  const int c = (int)cu, G = (int)a.by_g.d;
+  const int rt = a.row_tiles - 1 - (int)tile;  // (the longest first)
   const SeqView sv = seq_view(kv, s);
-  const int rows = min(sv.n, (int)kv.max_new) * a.G, row_lo = rt * ROWS;
+  const int rows = min(sv.n, (int)kv.max_new) * G, row_lo = rt * ROWS;
   if (row_lo >= rows) return;
-  const int64_t last_pos = sv.pos0 + min(row_lo + ROWS - 1, rows - 1) / a.G;
+  const int64_t last_pos = sv.pos0 + (int)a.by_g.div(min(row_lo + ROWS - 1, rows - 1));
   const int64_t end = min(sv.len, last_pos + 1);
   const int64_t c0 = (int64_t)c * a.chunk;
   const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
@@ -597,14 +656,25 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
   for (int u = 0; u < NT; ++u) {
     const int r = row_lo + 16 * (NT * wave + u) + n;
     const bool live = r < rows;
-    pos[u] = live ? (int32_t)max(min(sv.pos0 + r / a.G, sv.len - 1), (int64_t)-1) : -1;
-    float x[D / 4], sum_h, sum_l;
-    load_query<D>(a, a.q + (int64_t)(sv.row0 + (live ? r / a.G : 0)) * a.ldq +
-                         (int64_t)(h * a.G + (live ? r % a.G : 0)) * D, g, x);
+    uint32_t rem;
+    const int i = (int)a.by_g.divmod(live ? r : 0, rem);
+    pos[u] = live ? (int32_t)max(min(sv.pos0 + i, sv.len - 1), (int64_t)-1) : -1;
+    float x[D / 4];
+    load_query<D>(a, a.q + (int64_t)(sv.row0 + i) * a.ldq + (int64_t)(h * G + rem) * D, g, x);
 #pragma unroll
     for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
-    qfac[u] = split_query<D>(a.scale, x, qh[u], ql[u], sum_h, sum_l);
-    qbias[u] = kBias * (sum_h + sum_l);
+    const QueryScale f = query_scale<D>(a.scale, x);
+    qfac[u] = f.factor;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      float part[8], sum_h, sum_l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[e] = x[8 * j + e];
+      split_query(part, f.up, qh[u][j], ql[u][j], sum_h, sum_l);
+      sum += sum_h + sum_l;
+    }
+    qbias[u] = kBias * sum_groups(sum);
   }
 
   f32x4 o[NT][DT];
@@ -617,7 +687,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     for (int d = 0; d < DT; ++d) o[u][d] = {0.0f, 0.0f, 0.0f, 0.0f};
   }
   int ve = -100;
-  const int64_t all_see = min(sv.len, sv.pos0 + (row_lo + 16 * NT * wave) / a.G + 1);
+  const int64_t all_see = min(sv.len, sv.pos0 + (int)a.by_g.div(row_lo + 16 * NT * wave) + 1);
   const int P = 1 << kv.log_p;
 
   // A thread's pieces of a step: K piece e is 16 dims (g' + 4 i) of position
@@ -757,7 +827,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     const float lt = sum_groups(l[u]);
     const int r = row_lo + 16 * (NT * wave + u) + n;
     if (r >= rows) continue;
-    const int64_t row = sv.row0 + r / a.G, hq = h * a.G + r % a.G;
+    uint32_t rem;
+    const int64_t row = sv.row0 + a.by_g.divmod(r, rem), hq = h * G + rem;
     const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
     const bool whole = a.nchunk == 1;
     const float f = whole ? (lt > 0.0f ? back / lt : 0.0f) : back;
@@ -896,7 +967,10 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   a.ldq = ldq;
   a.ldy = ldy;
   a.Hq = (int32_t)Hq;
-  a.G = (int32_t)(Hq / kv.H);
+  a.by_h = fast_div(kv.H);
+  a.by_chunks = fast_div(p.nchunk);
+  a.by_tiles = fast_div(p.row_tiles);
+  a.by_g = fast_div(Hq / kv.H);
   a.chunk = (int32_t)p.chunk;
   a.nchunk = (int32_t)p.nchunk;
   a.row_tiles = (int32_t)p.row_tiles;
