@@ -39,10 +39,16 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kT = 256;          // threads of launches 1 to 3
-constexpr int kFinishT = 1024;   // threads of launch 4
+// Threads of launch 4.  Few rows, short chunks: one wave per SIMD, since the
+// launch is a chain of short steps between barriers and four waves per SIMD
+// take turns at each of them (one row: 10.0 us with 1,024 threads, 7.3 with
+// 256).  Many rows, long chunks: the walk through a chunk and the ordering of
+// a long list want more.
+constexpr int kFinishFew = 256, kFinishMany = 1024;
 constexpr int kBins = 1024;      // of 3 steps of 2^(-1/64) each; the last one holds all that is further below
 constexpr uint32_t kListMax = 2048;
 constexpr int kChunkMin = 4 * kT;
+constexpr int kChunkMax = 16384;
 constexpr int kChunksMax = TERN_SAMPLE_MAX_N / kChunkMin;
 constexpr double kFix = 17592186044416.0;  // 2^44
 static_assert((kBins - 1) * 3 / 64.0 - 1 / 128.0 > 47, "the last bin's weights round to 0: 2^44 2^-47 < 1/2");
@@ -590,17 +596,20 @@ struct Keep {
   int sure;
 };
 
+template <int T>
 struct FinishLds {
+  // (the lists' place holds a chunk's tiles afterwards)
   double tab[64];
   u64 red[32];
   CutLds cut;
   u64 mass[256];
   uint32_t count[256];
-  u64 tok[kListMax];
-  u64 sorted[kListMax];
-  u64 prefix[kListMax + 1];
+  u64 tok[kListMax];         // the listed tokens, ordered
+  double weight[kListMax];   // theirs
+  u64 list[kListMax];        // and as they came
   uint32_t rank[kListMax];
-  uint32_t n;
+  u64 prefix[kListMax + 1];  // weight before each, and of all
+  u64 tiles[(kChunkMax + 4 * T - 1) / (4 * T)][T / 64];  // weight of a chunk's tiles, by wave
   uint32_t out32[2];
   u64 out64;
 };
@@ -611,14 +620,14 @@ struct FinishLds {
 struct KeyBorder {
   uint32_t key, ties;  // tokens with larger keys, and the first `ties` of those with this one
 };
-template <bool BY_MASS>
-__device__ KeyBorder key_border(const Launch& L, const Row& r, KeyBorder in, uint32_t want, u64 mass, FinishLds& F) {
+template <int T, bool BY_MASS>
+__device__ KeyBorder key_border(const Launch& L, const Row& r, KeyBorder in, uint32_t want, u64 mass, FinishLds<T>& F) {
   uint32_t prefix = 0, mask = 0, before_n = 0;
   u64 before_m = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kFinishT) F.mass[i] = 0, F.count[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += T) F.mass[i] = 0, F.count[i] = 0;
     __syncthreads();
-    each_token<kFinishT>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
+    each_token<T>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
       const uint32_t k = logit_key(x);
       if (k == 0 || (k & mask) != prefix || k < in.key) return;
       const int bin = (k >> shift) & 255;
@@ -663,29 +672,30 @@ __device__ KeyBorder key_border(const Launch& L, const Row& r, KeyBorder in, uin
 }
 
 // Cuts a row of too many equal logits, and redoes its chunks' sums.
-__device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLds& F) {
+template <int T>
+__device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLds<T>& F) {
   KeyBorder cut = {1u, 0xffffffffu};
-  if (r.k < r.live) cut = key_border<false>(L, r, cut, r.k, 0, F);
+  if (r.k < r.live) cut = key_border<T, false>(L, r, cut, r.k, 0, F);
   if (r.top_p < 1.0) {
     u64 sum = 0, total;
-    each_token<kFinishT>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
+    each_token<T>(r.x, 0, (int)L.a.N, L.vec, [&](int, float x) {
       const uint32_t k = logit_key(x);
       if (k > cut.key || (k == cut.key && cut.ties == 0xffffffffu)) sum += fixed(weight_of(r, F.tab, x));
     });
-    wg_scan<kFinishT>(sum, F.red, total);
+    wg_scan<T>(sum, F.red, total);
     if (cut.ties != 0xffffffffu) total += (u64)cut.ties * fixed(weight_of(r, F.tab, key_logit(cut.key)));
-    cut = key_border<true>(L, r, cut, 0, mass_limit(r.top_p, total), F);
+    cut = key_border<T, true>(L, r, cut, 0, mass_limit(r.top_p, total), F);
   }
   // the index of the last tie inside: the one with ties - 1 before it
   Keep keep = {pack_token(cut.key, 0x7fffffff), 0};
   uint32_t seen = 0;
-  for (int j0 = 0; j0 < (int)L.a.N && cut.ties != 0xffffffffu; j0 += 4 * kFinishT) {
-    const int j1 = (int)min((int64_t)j0 + 4 * kFinishT, L.a.N);
+  for (int j0 = 0; j0 < (int)L.a.N && cut.ties != 0xffffffffu; j0 += 4 * T) {
+    const int j1 = (int)min((int64_t)j0 + 4 * T, L.a.N);
     uint32_t mine = 0;
-    each_token<kFinishT>(r.x, j0, j1, L.vec, [&](int, float x) { mine += logit_key(x) == cut.key; });
+    each_token<T>(r.x, j0, j1, L.vec, [&](int, float x) { mine += logit_key(x) == cut.key; });
     u64 all;
-    uint32_t at = seen + (uint32_t)wg_scan<kFinishT>(mine, F.red, all);
-    each_token<kFinishT>(r.x, j0, j1, L.vec, [&](int j, float x) {
+    uint32_t at = seen + (uint32_t)wg_scan<T>(mine, F.red, all);
+    each_token<T>(r.x, j0, j1, L.vec, [&](int j, float x) {
       if (logit_key(x) == cut.key && ++at == cut.ties) F.out64 = pack_token(cut.key, j);
     });
     seen += (uint32_t)all;
@@ -695,15 +705,15 @@ __device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLd
   if (cut.ties != 0xffffffffu) keep.border = F.out64;
   for (int c = 0; c < L.chunks; ++c) {
     u64 sum = 0, kept = 0;
-    each_token<kFinishT>(r.x, c * L.per, (int)min((int64_t)(c + 1) * L.per, L.a.N), L.vec, [&](int j, float x) {
+    each_token<T>(r.x, c * L.per, (int)min((int64_t)(c + 1) * L.per, L.a.N), L.vec, [&](int j, float x) {
       const uint32_t k = logit_key(x);
       if (!k || pack_token(k, j) < keep.border) return;
       const double wt = weight_of(r, F.tab, x);
       if (wt >= r.min_p) sum += fixed(wt), ++kept;
     });
     u64 total, n;
-    wg_scan<kFinishT>(sum, F.red, total);
-    wg_scan<kFinishT>(kept, F.red, n);
+    wg_scan<T>(sum, F.red, total);
+    wg_scan<T>(kept, F.red, n);
     if (threadIdx.x == 0) {
       store_g(w.chunk_mass + c, total);
       store_g(w.chunk_kept + c, (uint32_t)n);
@@ -713,25 +723,55 @@ __device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLd
   return keep;
 }
 
-__global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
+// Orders n packed tokens, the largest first: each one's place is the number of
+// larger ones, counted by as many threads as there are for a token (a bitonic
+// network of 1,027 tokens took 33 us, its 66 barriers each waiting for LDS).
+// `tok` is read, `sorted` written; `rank` is scratch.
+template <int T>
+__device__ void order_tokens(const u64* tok, uint32_t* rank, u64* sorted, int n) {
+  for (int i = threadIdx.x; i < n; i += T) rank[i] = 0;
+  __syncthreads();
+  int log_share = 0;
+  while ((2 << log_share) * n <= T) ++log_share;
+  const int share = 1 << log_share;
+  for (int i = threadIdx.x; i < n << log_share; i += T) {
+    const int e = i >> log_share;
+    const u64 me = tok[e];
+    uint32_t before = 0;
+#pragma unroll 8
+    for (int o = i & (share - 1); o < n; o += share) before += tok[o] > me;
+    if (before) atomicAdd(&rank[e], before);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += T) sorted[rank[i]] = tok[i];
+  __syncthreads();
+}
+
+template <int T>
+__global__ __launch_bounds__(T) void finish_kernel(Launch L) {
+  constexpr int kPer = kListMax / T;   // listed tokens per thread
+  constexpr int kCh = (kChunksMax + T - 1) / T;  // chunks per thread
   __shared__ u64 cmass[kChunksMax];  // a chunk's kept weight, that of its listed tokens included
-  __shared__ FinishLds F;
-  static_assert(kChunksMax <= kFinishT && kListMax == 2 * kFinishT, "a chunk and two listed tokens per thread");
+  __shared__ FinishLds<T> F;
   const SampleArgs& a = L.a;
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x;
   const RowWs w = row_ws(L, row);
   // everything that the earlier launches left, loaded before anything waits
   const bool cuts = a.top_k || a.top_p;
-  const Bins<kFinishT> bins = load_bins<kFinishT>(L, w);
+  const Bins<T> bins = load_bins<T>(L, w);
   const uint32_t list_n = cuts ? load_g(w.list_n) : 0;
-  u64 tok[2];
+  u64 tok[kPer], chunk_mass[kCh], kept = 0;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) tok[e] = cuts ? load_g(w.list + t + e * kFinishT) : 0;
-  u64 chunk_mass = t < L.chunks ? load_g(w.chunk_mass + t) : 0;
-  u64 kept = t < L.chunks ? load_g(w.chunk_kept + t) : 0;
+  for (int e = 0; e < kPer; ++e) tok[e] = cuts ? load_g(w.list + t + e * T) : 0;
+#pragma unroll
+  for (int e = 0; e < kCh; ++e) {
+    const int c = t + e * T;
+    chunk_mass[e] = c < L.chunks ? load_g(w.chunk_mass + c) : 0;
+    kept += c < L.chunks ? load_g(w.chunk_kept + c) : 0;
+  }
   if (t < 64) F.tab[t] = kExp2[t];
-  const Row r = load_row<kFinishT>(L, w, row, F.red);
+  const Row r = load_row<T>(L, w, row, F.red);
   if (r.greedy || r.live == 0) {
     if (t == 0) {
       store_g(a.token + row, r.live ? (int32_t)~(uint32_t)r.top : -1);
@@ -740,64 +780,53 @@ __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
     }
     return;
   }
-  const Cut cut = find_cut<kFinishT>(r, bins, F.cut);
+  const Cut cut = find_cut<T>(r, bins, F.cut);
   Keep keep = {~0ull, cut.sure};
+  float least = cut_logit(r, cut);
   const uint32_t nl = wants_bins(r) ? list_n : 0;
   // (a minimum below the last bin's weights would have to look into it)
   const bool slow = nl > kListMax || (cut.rest_kept && r.min_p > 0.0);
   if (slow) {
     __syncthreads();
-    keep = slow_cut(L, w, r, F);
-    chunk_mass = t < L.chunks ? load_g(w.chunk_mass + t) : 0;
-    kept = t < L.chunks ? load_g(w.chunk_kept + t) : 0;
+    keep = slow_cut<T>(L, w, r, F);
+    least = -__builtin_inff();
+    kept = 0;
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) {
+      const int c = t + e * T;
+      chunk_mass[e] = c < L.chunks ? load_g(w.chunk_mass + c) : 0;
+      kept += c < L.chunks ? load_g(w.chunk_kept + c) : 0;
+    }
   } else if (t == 0) {
     kept += cut.rest_kept;
   }
-  if (t < L.chunks) cmass[t] = chunk_mass;
+#pragma unroll
+  for (int e = 0; e < kCh; ++e)
+    if (t + e * T < L.chunks) cmass[t + e * T] = chunk_mass[e];
   const int n = slow ? 0 : (int)nl;
   if (n) {
-    // order: each token's rank is the number of listed tokens before it,
-    // counted by as many threads as there are for a token
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (t + e * kFinishT < n) F.tok[t + e * kFinishT] = tok[e], F.rank[t + e * kFinishT] = 0;
-    __syncthreads();
-    int log_share = 0;
-    while ((2 << log_share) * n <= kFinishT) ++log_share;
-    const int share = 1 << log_share;
-    for (int i = t; i < n << log_share; i += kFinishT) {
-      const int e = i >> log_share;
-      const u64 me = F.tok[e];
-      uint32_t before = 0;
-#pragma unroll 4
-      for (int o = i & (share - 1); o < n; o += share) before += F.tok[o] > me;
-      if (before) atomicAdd(&F.rank[e], before);
+    for (int e = 0; e < kPer; ++e)
+      if (t + e * T < n) F.list[t + e * T] = tok[e];
+    order_tokens<T>(F.list, F.rank, F.tok, n);
+    // weights before each of them; tokens before bin kbin, and in the bins of top-p
+    const int per = (n + T - 1) / T, i0 = min(n, t * per), i1 = min(n, i0 + per);
+    u64 before = 0, counts = 0, all, all_counts;
+    for (int i = i0; i < i1; ++i) {
+      const Reduced d = reduce(r, key_logit((uint32_t)(F.tok[i] >> 32)));
+      const int b = bin_of(d);
+      const double wd = weight_of(d, F.tab);
+      F.weight[i] = wd;
+      before += fixed(wd);
+      counts += (b < cut.kbin ? 1ull : 0ull) | (b <= cut.p2 ? 1ull << 32 : 0ull);
     }
-    __syncthreads();
-    for (int i = t; i < n; i += kFinishT) F.sorted[F.rank[i]] = F.tok[i];
-    __syncthreads();
-    // weights before each of them, two per thread; tokens before bin kbin, and in the bins of top-p
-    u64 wt[2], before = 0, counts = 0, all, all_counts;
-    double wd[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      wt[e] = 0;
-      wd[e] = 0.0;
-      if (2 * t + e < n) {
-        const Reduced d = reduce(r, key_logit((uint32_t)(F.sorted[2 * t + e] >> 32)));
-        const int b = bin_of(d);
-        wd[e] = weight_of(d, F.tab);
-        wt[e] = fixed(wd[e]);
-        counts += (b < cut.kbin ? 1ull : 0ull) | (b <= cut.p2 ? 1ull << 32 : 0ull);
-      }
-      before += wt[e];
-    }
-    wg_scan2<kFinishT>(before, counts, F.red, all, all_counts);
+    wg_scan2<T>(before, counts, F.red, all, all_counts);
     const int nk = (int)(uint32_t)all_counts, np = (int)(all_counts >> 32);
-    // (positions 2 t and 2 t + 1, and the total behind the last)
-    if (2 * t <= n) F.prefix[2 * t] = before;
-    if (2 * t + 1 <= n) F.prefix[2 * t + 1] = before + wt[0];
-    if (2 * t + 2 == n) F.prefix[n] = all;
+    for (int i = i0; i < i1; ++i) {
+      F.prefix[i] = before;
+      before += fixed(F.weight[i]);
+    }
+    if (t == 0) F.prefix[n] = all, F.out32[0] = 0;
     __syncthreads();
     const int kend = cut.kbin < kBins ? nk + (int)cut.kneed : n;  // listed tokens among the first k
     int end = kend;
@@ -805,65 +834,105 @@ __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
       const u64 z = cut.kbin < kBins ? cut.mass_k + F.prefix[kend] - F.prefix[nk] : cut.mass_k;
       const u64 lim = mass_limit(r.top_p, z);
       const int most = min(np, kend);
-      if (t == 0) F.out32[0] = 0;
-      __syncthreads();
       // (forerunners grow along the order: one last token is inside)
-      for (int i = t; i < most; i += kFinishT)
+      for (int i = t; i < most; i += T)
         if (cut.mass_p1 + F.prefix[i] < lim && (i + 1 == most || cut.mass_p1 + F.prefix[i + 1] >= lim)) F.out32[0] = i + 1;
       __syncthreads();
       end = (int)F.out32[0];
     }
-    if (end > 0) keep.border = F.sorted[end - 1];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (2 * t + e >= end || wd[e] < r.min_p) continue;
+    if (end > 0) keep.border = F.tok[end - 1];
+    for (int i = t; i < end; i += T) {
+      if (F.weight[i] < r.min_p) continue;
       ++kept;
-      atomicAdd(&cmass[~(uint32_t)F.sorted[2 * t + e] / (uint32_t)L.per], wt[e]);
+      atomicAdd(&cmass[~(uint32_t)F.tok[i] / (uint32_t)L.per], fixed(F.weight[i]));
     }
   }
   __syncthreads();
 
-  // the chunk that u * total falls in
-  const u64 sum = t < L.chunks ? cmass[t] : 0;
-  u64 before = sum, total, nkept;
-  wg_scan2<kFinishT>(before, kept, F.red, total, nkept);
+  // the chunk that u * total falls in (kCh consecutive ones per thread)
+  u64 mine[kCh], before = 0, total, nkept;
+#pragma unroll
+  for (int e = 0; e < kCh; ++e) {
+    mine[e] = kCh * t + e < L.chunks ? cmass[kCh * t + e] : 0;
+    before += mine[e];
+  }
+  wg_scan2<T>(before, kept, F.red, total, nkept);
   const double u = r.u > 0.0f ? fmin((double)r.u, 1.0) : 0.0;
   u64 target = (u64)(u * (double)total);
   if (target >= total) target = total - 1;
-  if (before <= target && target < before + sum) F.out32[0] = (uint32_t)t, F.out64 = before;  // one thread
+#pragma unroll
+  for (int e = 0; e < kCh; ++e) {
+    if (before <= target && target < before + mine[e]) F.out32[0] = (uint32_t)(kCh * t + e), F.out64 = before;  // once
+    before += mine[e];
+  }
   __syncthreads();
   const int c = (int)F.out32[0];
   before = F.out64;
 
-  // and the token in that chunk
+  // the tile of that chunk, four tokens per thread, and the token in it
   const int j0 = c * L.per, j1 = (int)min((int64_t)(c + 1) * L.per, a.N);
-  for (int j = j0; j < j1; j += 4 * kFinishT) {
-    const int me = j + 4 * t;
-    float x[4];
-    u64 wt[4], run = 0, all;
+  auto weight = [&](float x, int j) {  // of token j where it is kept
+    u64 f = 0;
+    const uint32_t key = x >= least ? logit_key(x) : 0;
+    if (key) {
+      const Reduced d = reduce(r, x);
+      const double wd = weight_of(d, F.tab);
+      if ((bin_of(d) < keep.sure || pack_token(key, j) >= keep.border) && wd >= r.min_p) f = fixed(wd);
+    }
+    return f;
+  };
+  constexpr int kTile = 4 * T, kAtOnce = kFinishMany / T * 2;
+  static_assert(2 * kListMax * sizeof(u64) >= kAtOnce * kTile * sizeof(float), "the tiles fit where tok and weight were");
+  Tile<T, 1> tile;
+  int at = j0;
+  if (j1 - j0 > kTile) {
+    // every tile's weight, several tiles loaded at once (and kept in LDS, where
+    // the lists were: one copy of the code for all of them)
+    float* mem = reinterpret_cast<float*>(F.tok);
+    for (int jb = j0; jb < j1; jb += kAtOnce * kTile) {
+      Tile<T, kAtOnce> all;
+      all.load(r.x, jb, j1, L.vec);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = me + i < j1 ? load_g(r.x + me + i) : -__builtin_inff();
+      for (int e = 0; e < kAtOnce; ++e)
+        *reinterpret_cast<f32x4*>(mem + kTile * e + 4 * t) = f32x4{all.v[e][0], all.v[e][1], all.v[e][2], all.v[e][3]};
+#pragma unroll 1
+      for (int e = 0; e < kAtOnce && jb + e * kTile < j1; ++e) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(mem + kTile * e + 4 * t);
+        const int j = Tile<T, 1>::at(jb + e * kTile, 0);
+        u64 sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      wt[i] = 0;
-      const uint32_t key = logit_key(x[i]);
-      if (key) {
-        const Reduced d = reduce(r, x[i]);
-        const double wd = weight_of(d, F.tab);
-        if ((bin_of(d) < keep.sure || pack_token(key, me + i) >= keep.border) && wd >= r.min_p) wt[i] = fixed(wd);
+        for (int i = 0; i < 4; ++i) sum += weight(x[i], j + i);
+        sum = wave_scan(sum);
+        if ((t & 63) == 63) F.tiles[(jb - j0) / kTile + e][t >> 6] = sum;
       }
-      run += wt[i];
     }
-    u64 at = wg_scan<kFinishT>(run, F.red, all) + before;
-    if (at <= target && target < at + run) {  // one thread of one step
-      int i = 0;
-      while (at + wt[i] <= target) at += wt[i++];
-      store_g(a.token + row, me + i);
-      if (a.prob) store_g(a.prob + row, (float)(weight_of(r, F.tab, x[i]) * kFix / (double)total));
-      if (a.kept) store_g(a.kept + row, (int32_t)nkept);
+    __syncthreads();
+    for (;; at += kTile) {  // (every thread alike)
+      u64 sum = 0;
+#pragma unroll
+      for (int v = 0; v < T / 64; ++v) sum += F.tiles[(at - j0) / kTile][v];
+      if (before + sum > target) break;
+      before += sum;
     }
-    before += all;
-    if (before > target) break;
+  }
+  tile.load(r.x, at, j1, L.vec);
+  u64 wt[4], sum = 0, all;
+  const int me = Tile<T, 1>::at(at, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum += wt[i] = weight(tile.v[0][i], me + i);
+  before += wg_scan<T>(sum, F.red, all);
+  if (before <= target && target < before + sum) {  // one thread
+    int i = 0;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      if (before + wt[e] > target) break;
+      before += wt[e];
+      i = e + 1;
+    }
+    const float x = i == 0 ? tile.v[0][0] : i == 1 ? tile.v[0][1] : i == 2 ? tile.v[0][2] : tile.v[0][3];
+    store_g(a.token + row, me + i);
+    if (a.prob) store_g(a.prob + row, (float)(weight_of(r, F.tab, x) * kFix / (double)total));
+    if (a.kept) store_g(a.kept + row, (int32_t)nkept);
   }
 }
 
@@ -871,7 +940,7 @@ __global__ __launch_bounds__(kFinishT) void finish_kernel(Launch L) {
 // many rows larger ones.
 int64_t tokens_per_chunk(int64_t M, int64_t N) {
   int64_t per = kChunkMin;
-  while (per < 16384 && M * ((N + per - 1) / per) > 2048) per *= 2;
+  while (per < kChunkMax && M * ((N + per - 1) / per) > 2048) per *= 2;
   return per;
 }
 
@@ -890,7 +959,7 @@ int64_t sample_workspace_bytes(int64_t M, int64_t N) {
 }
 int64_t sample_work_items(int64_t M, int64_t N) {
   const int64_t per = tokens_per_chunk(M, N);
-  return mul_sat(mul_sat(M, (N + per - 1) / per), kFinishT);
+  return mul_sat(mul_sat(M, (N + per - 1) / per), kFinishMany);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
@@ -902,11 +971,14 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   L.row_bytes = row_ws_bytes(L.chunks);
   L.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M == 1 || a.ldx % 4 == 0);
   const dim3 grid((unsigned)(a.M * L.chunks));
-  if (L.per > kChunkMin)
+  const dim3 rows((unsigned)a.M);
+  if (L.per > kChunkMin) {
     launch_chunks<4>(L, grid, s);
-  else
+    hipLaunchKernelGGL(finish_kernel<kFinishMany>, rows, dim3(kFinishMany), 0, s, L);
+  } else {
     launch_chunks<1>(L, grid, s);
-  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)a.M), dim3(kFinishT), 0, s, L);
+    hipLaunchKernelGGL(finish_kernel<kFinishFew>, rows, dim3(kFinishFew), 0, s, L);
+  }
   return hipGetLastError();
 }
 
