@@ -667,6 +667,29 @@ def suite(args):
             del b, g, xd, logits
         rec["note"] = "the other linears take independent synthetic activations (one per shared group)"
         emit(rec)
+        # the same step from the residual stream to the next token: the norm with its int8 output in the
+        # quantiser's place, and a token sampled from the head's logits
+        b = st.bind(M, share_inputs=True)
+        ldq = b.q[0].shape[1]
+        xd, rd = (torch.from_numpy(synth.make_hidden(5 + i, 0, 0, Kh, M)).to(dev) for i in range(2))
+        gain, hd = torch.rand(Kh, device=dev) + 0.5, torch.empty((M, Kh), device=dev)
+        logits = torch.empty((M, Nh), dtype=torch.float32, device=dev)
+        Td, ud = torch.full((M,), 0.8, device=dev), torch.rand(M, device=dev)
+        kd, pd = torch.full((M,), 50, dtype=torch.int32, device=dev), torch.full((M,), 0.95, device=dev)
+        tok = torch.empty(M, dtype=torch.int32, device=dev)
+        wsd = torch.empty(tern.tern_sample_workspace_bytes(M, Nh), dtype=torch.uint8, device=dev)
+
+        def sstep(i=0):
+            tern.tern_rmsnorm_quantize(xd, gain, 1e-6, M, Kh, Kh, b.q[0], ldq, b.s_act[0], b.z[0], res=rd, ldr=Kh,
+                                       h=hd, ldh=Kh)
+            b.run()
+            tern.tern_head_gemv(Whd, srhd, rshd, Nh, Kh, Kh, M, b.q[0], ldq, b.s_act[0], b.z[0], logits, Nh)
+            tern.tern_sample(logits, M, Nh, Nh, Td, ud, tok, wsd, top_k=kd, top_p=pd)
+        db = b.bytes + head_bytes + 13 * M * Kh + 4 * Kh + 8 * M + 4 * M * Nh
+        emit({"suite": "decode_step_sampled", "workload": "the decode step's linears at M = %d between the residual "
+              "stream and the next token: norm with int8 output, the 252-linear 8B stack, the int8 head, sampling "
+              "(top-k 50, top-p 0.95)" % M, "M": M, **_stats(_event_times(sstep, 20), db)})
+        del b, xd, rd, logits, wsd
     # --- the same 252-linear stack at 16 tokens (a longer verify pass), one launch
     b16 = st.bind(16)
     us = _event_times(lambda i: b16.run(), 20)
@@ -723,6 +746,72 @@ def suite(args):
         emit({"suite": "quantize", "workload": "per-token int8 quantisation of M x 4,096 fp32 "
               "activations, M = %d" % M, "M": M, "kernel": "quant_kernel", **st_,
               "cpu_oracle": {"us": round(ot * 1e6, 2), "cores": cores, "reps": oreps}})
+
+    # --- the calls between the linears
+    decode_operators(emit)
+
+
+def decode_operators(emit):
+    """The calls between the linears of a decode step, in the 8B's geometry
+    (one JSON line each; three rotating copies)."""
+    import torch
+    from packed_bit_gemv_tern_amd import tern
+    dev, K, V, HQ, H, D, P = "cuda:0", 4096, 151936, 32, 8, 128, 64
+    for M in (1, 8, 512):
+        bufs = [[torch.randn(M, K, device=dev) for _ in range(3)] + [
+            torch.empty((M, K), dtype=torch.int8, device=dev), torch.empty(M, device=dev),
+            torch.empty(M, dtype=torch.int32, device=dev)] for _ in range(3)]
+        gain = torch.rand(K, device=dev)
+
+        def norm(i):
+            x, r, h, q, s, z = bufs[i % 3]
+            tern.tern_rmsnorm_quantize(x, gain, 1e-6, M, K, K, q, K, s, z, res=r, ldr=K, h=h, ldh=K)
+        emit({"suite": "norm", "workload": "residual addition, RMS norm and int8 output of M x 4,096, M = %d" % M,
+              "M": M, **_stats(_event_times(norm, 50), 13 * M * K + 4 * K + 8 * M)})
+    # (sequences, context, new tokens)
+    for S, ctx, new in ((1, 4096, 1), (1, 32768, 8), (32, 4096, 1), (1, 4096, 2048)):
+        J = -(-ctx // P)
+        state = []
+        for _ in range(3):
+            k, v = (torch.randint(-127, 128, (S * J, H, P * D), dtype=torch.int8, device=dev) for _ in range(2))
+            ks, vs = (torch.rand(S * J, H, device=dev) * 0.02 + 0.005 for _ in range(2))
+            cache = tern.make_kv_cache(k, v, ks, vs, S * J, H, D, P)
+            table = torch.randperm(S * J, device=dev).to(torch.int32)
+            start = torch.arange(S + 1, dtype=torch.int32, device=dev) * new
+            length = torch.full((S,), ctx, dtype=torch.int32, device=dev)
+            batch = tern.make_kv_batch(table, J, start, length, S, S * new, new, ctx)
+            qkv = torch.randn(S * new, (HQ + 2 * H) * D, device=dev)
+            y = torch.empty(S * new, HQ * D, device=dev)
+            ws = torch.empty(tern.tern_attention_workspace_bytes(cache, batch, HQ), dtype=torch.uint8, device=dev)
+            state.append((cache, batch, qkv, y, ws, (k, v, ks, vs, table, start, length)))
+        ld = (HQ + 2 * H) * D
+
+        def append(i):
+            cache, batch, qkv = state[i % 3][:3]
+            tern.tern_kv_append(cache, batch, qkv[:, HQ * D:], ld, qkv[:, (HQ + H) * D:], ld)
+
+        def attend(i):
+            cache, batch, qkv, y, ws = state[i % 3][:5]
+            tern.tern_attention(cache, batch, qkv, ld, HQ, D ** -0.5, y, HQ * D, ws)
+        what = "%d sequence(s) of %d tokens, %d new each, 32 query and 8 KV heads of 128, pages of 64" % (S, ctx, new)
+        emit({"suite": "kv_append", "workload": "append to the int8 cache: " + what,
+              **_stats(_event_times(append, 50), 10 * S * new * H * D)})
+        nbytes = S * (2 * ctx * H * D + 8 * J * H + 4 * J) + 8 * S * new * HQ * D
+        rec = {"suite": "attention", "workload": "attention over the int8 cache: " + what,
+               **_stats(_event_times(attend, 50), nbytes)}
+        rec["TFLOPs"] = round(4 * HQ * D * S * new * (ctx - (new - 1) / 2) / rec["median_us"] / 1e6, 2)
+        emit(rec)
+        del state
+        torch.cuda.empty_cache()
+    for M in (1, 8, 64):
+        x = [torch.randn(M, V, device=dev) * 3 for _ in range(3)]
+        T, u = torch.full((M,), 0.8, device=dev), torch.rand(M, device=dev)
+        k, p = torch.full((M,), 50, dtype=torch.int32, device=dev), torch.full((M,), 0.95, device=dev)
+        token = torch.empty(M, dtype=torch.int32, device=dev)
+        ws = torch.empty(tern.tern_sample_workspace_bytes(M, V), dtype=torch.uint8, device=dev)
+        us = _event_times(lambda i: tern.tern_sample(x[i % 3], M, V, V, T, u, token, ws, top_k=k, top_p=p), 50)
+        emit({"suite": "sample", "workload": "sampling from M rows of 151,936 logits (top-k 50, top-p 0.95), M = %d" % M,
+              "M": M, **_stats(us, 4 * M * V)})
 
 
 def prefill_case(args, M: int):

@@ -936,13 +936,21 @@ __global__ __launch_bounds__(T) void finish_kernel(Launch L) {
   }
 }
 
-// Tokens per chunk: single rows need many small chunks to be read at once,
-// many rows larger ones.
-int64_t tokens_per_chunk(int64_t M, int64_t N) {
-  int64_t per = kChunkMin;
-  while (per < kChunkMax && M * ((N + per - 1) / per) > 2048) per *= 2;
+// Tokens per chunk.  A few rows: one tile per workgroup, so that a row is read
+// at once.  Where there is a histogram its workgroups all add into the row's
+// bins, and beyond 256 of them that costs more than longer chunks do (top-k
+// and top-p on 8 rows of 151,936: 47 us at 1,024 tokens, 35 at 2,048, 30 at
+// 4,096, 36 at 8,192; without a histogram 15.8 / 17.9 / 18.2 / 25.6); many
+// rows want no more than about 2,048 workgroups (64 rows: 61 us at 4,096, 56 at
+// 8,192, 59 at 16,384; 96 rows: 69 at 8,192, 81 at 16,384).
+int64_t tokens_per_chunk(int64_t M, int64_t N, bool cuts) {
+  auto chunks = [&](int64_t per) { return M * ((N + per - 1) / per); };
+  if (chunks(kChunkMin) <= (cuts ? 256 : 1280)) return kChunkMin;
+  int64_t per = 4 * kChunkMin;
+  while (per < kChunkMax && chunks(per) > 2048) per *= 2;
   return per;
 }
+static_assert(kChunkMin == 1024, "the figures above");
 
 template <int U>
 void launch_chunks(const Launch& L, dim3 grid, hipStream_t s) {
@@ -954,11 +962,11 @@ void launch_chunks(const Launch& L, dim3 grid, hipStream_t s) {
 }  // namespace
 
 int64_t sample_workspace_bytes(int64_t M, int64_t N) {
-  const int64_t per = tokens_per_chunk(M, N);
+  const int64_t per = tokens_per_chunk(M, N, false);  // (the more chunks of the two)
   return mul_sat(M, row_ws_bytes((N + per - 1) / per));
 }
 int64_t sample_work_items(int64_t M, int64_t N) {
-  const int64_t per = tokens_per_chunk(M, N);
+  const int64_t per = tokens_per_chunk(M, N, false);
   return mul_sat(mul_sat(M, (N + per - 1) / per), kFinishMany);
 }
 
@@ -966,7 +974,7 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   Launch L;
   L.a = a;
   L.ws = static_cast<uint8_t*>(workspace);
-  L.per = (int32_t)tokens_per_chunk(a.M, a.N);
+  L.per = (int32_t)tokens_per_chunk(a.M, a.N, a.top_k || a.top_p);
   L.chunks = (int32_t)((a.N + L.per - 1) / L.per);
   L.row_bytes = row_ws_bytes(L.chunks);
   L.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M == 1 || a.ldx % 4 == 0);
