@@ -473,7 +473,8 @@ int tern_rmsnorm_quantize(const float* x, int64_t ldx, const float* res, int64_t
  *            aligned;
  *   v        device, pages x heads x head_dim x page_tokens int8 (a page is
  *            stored transposed), 16-byte aligned;
- *   k_scale, v_scale  device, pages x heads floats >= 0.
+ *   k_scale, v_scale  device, pages x heads floats, 0 or from 2^-100 to 2^100
+ *            (tern_kv_append makes them; others lose accuracy).
  * page_tokens is 16, 32, 64 or 128 and head_dim 64 or 128, otherwise
  * TERN_ERR_UNSUPPORTED.  A fresh cache needs no initial contents.
  */
@@ -543,8 +544,9 @@ int tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, const
  *         ldy >= q_heads * head_dim (when rows > 1), 4-byte aligned; q finite;
  *         scale finite, q_heads a multiple of heads;
  *   workspace  device, 256-byte aligned, at least
- *         tern_attention_workspace_bytes(cache, batch, q_heads) bytes: partial
- *         results of a long context's pieces.  It carries nothing from call
+ *         tern_attention_workspace_bytes(cache, batch, q_heads) bytes (0 on bad
+ *         arguments; NULL will do where that is 256): partial results of a
+ *         long context's pieces.  It carries nothing from call
  *         to call; calls that may overlap need one each.
  */
 int64_t tern_attention_workspace_bytes(const tern_kv_cache* cache, const tern_kv_batch* batch, int64_t q_heads);

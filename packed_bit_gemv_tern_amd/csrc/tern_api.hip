@@ -392,7 +392,10 @@ int64_t tern_attention_workspace_bytes(const tern_kv_cache* cache, const tern_kv
   if (check_kv(cache, batch, &a) != TERN_OK || check_q_heads(a, q_heads) != TERN_OK) return 0;
   if (kv_empty(a)) return 256;
   const int cus = device_cus();
-  return cus <= 0 ? 0 : std::max<int64_t>(256, attn_plan(a, q_heads, cus).workspace);
+  if (cus <= 0) return 0;
+  const AttnPlan p = attn_plan(a, q_heads, cus);
+  if (p.work_items > kMaxDispatchItems || p.join_items > kMaxDispatchItems) return 0;
+  return std::max<int64_t>(256, p.workspace);
 }
 
 int tern_attention(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* q, int64_t ldq,

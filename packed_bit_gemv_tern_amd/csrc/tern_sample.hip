@@ -15,7 +15,7 @@
 // Weights are computed in fp64 and summed as integers of 2^-44, so a sum is
 // the same in whatever order it is taken (atomics included), and two rows
 // with the same logits draw the same token.  The largest weight is 1, so
-// 2^19 tokens sum to less than 2^63.
+// 2^19 tokens sum to at most 2^63.
 //
 // Nothing is sorted but a few tokens around the cut.  A row is split in
 // chunks, one workgroup each, and goes through up to four launches:

@@ -99,6 +99,12 @@ def test_norm_in_place(K, in_place):
     check(5, K, in_place=in_place, extra=3)
 
 
+@pytest.mark.parametrize("K", [5, 1024, 3000, 4096, 20000])
+@pytest.mark.parametrize("M", [2, 300])
+def test_norm_of_a_sum_that_is_not_kept(M, K):
+    check(M, K, with_h=False)
+
+
 def test_norm_eps_counts():
     check(2, 300, kind="tiny", eps=1e-3)
     check(2, 300, kind="normal", eps=2.0)

@@ -177,3 +177,36 @@ def test_cut_among_many_close_logits(n):
     draw(x, [1.0] * 3, u, top_k=[max(1, n // 2)] * 3)
     draw(x, [1.0] * 3, u, top_p=[0.4] * 3)
     draw(x, [1.0] * 3, u, top_k=[max(1, n - 1)] * 3, top_p=[0.7] * 3, min_p=[0.5] * 3)
+
+
+@pytest.mark.parametrize("names", ["none", "kp", "min_p"])
+def test_longest_rows_and_unaligned_ones(names):
+    rng = np.random.default_rng(10)
+    N = tern.TERN_SAMPLE_MAX_N
+    draw(logits(rng, 1, N), **params(rng, 1, FILTERS[names]))
+    # a row that starts 4 bytes past a 16-byte border
+    x, p = logits(rng, 1, 50001), params(rng, 1, FILTERS[names])
+    buf = torch.zeros(50005, device=DEV)
+    buf[1:50002] = to_dev(x[0])
+    dev = {k: to_dev(np.asarray(v, np.int32 if k == "top_k" else np.float32)) for k, v in p.items()}
+    token = torch.empty(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(tern.tern_sample_workspace_bytes(1, 50001), dtype=torch.uint8, device=DEV)
+    tern.tern_sample(buf[1:], 1, 50001, 50001, dev["T"], dev["u"], token, ws, top_k=dev.get("top_k"),
+                     top_p=dev.get("top_p"), min_p=dev.get("min_p"))
+    one = lambda k: None if k not in p else dev[k].cpu().numpy()[0]  # noqa: E731
+    assert int(token[0]) == decode.sample(x[0], one("T"), one("u"), one("top_k"), one("top_p"), one("min_p"))[0]
+
+
+def test_cuts_of_some_rows_and_not_of_others_at_every_chunk_length():
+    """One tile per chunk, four, and sixteen: rows with and without filters,
+    greedy and empty ones side by side."""
+    rng = np.random.default_rng(11)
+    for M, N in ((2, 100000), (40, 60000), (300, 33000)):
+        x = logits(rng, M, N)
+        x[1::9] = -np.inf
+        p = params(rng, M, ("top_k", "top_p", "min_p"))
+        p["top_k"][::2] = 0
+        p["top_p"][::3] = 1.0
+        p["min_p"][::5] = 0.0
+        p["T"][::7] = 0.0
+        draw(x, **p)
