@@ -14,7 +14,7 @@
 // fp16.  The other operand of each product is split in two fp16 numbers, hi
 // + lo, 22 bits together: q after a power of two that brings the row's
 // largest element under 2^9 (so that lo stays far above fp16's smallest
-// numbers), and w_j = e^(s_j - m) * vs_j / 2^e <= 2^15 (e: exponent of the
+// numbers), and w_j = e^(s_j - m) * vs_j * 2^(6 - e) < 2^7 (e: exponent of the
 // largest V scale met so far).  Errors are then those of fp32.
 //
 // Layout: in S^T a lane holds one query row (lane % 16) and 4 positions per
@@ -100,11 +100,12 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t w0, uint32_t w1) {
 }
 
 // Eight int8 codes as (code + 128) * 2^-24: u in the low byte of an fp16 is
-// the subnormal u * 2^-24, so nothing is subtracted here.  The first product
-// starts its sums at -128 times the sum of the query row instead; what that
-// costs is a rounding at about twice the magnitude.  (The second product
-// cannot: its sums, of many values of either sign, are small beside those of
-// values + 128.)
+// the subnormal u * 2^-24, so nothing is subtracted here (two instructions in
+// five less).  The prompt kernel's first product starts its sums at -128 times
+// the sum of the query row instead, which rounds at about twice the magnitude
+// (results 15 % further off; 2.5 % of its time).  Kernels that wait for memory
+// subtract, and the second product has to: its sums, of many values of either
+// sign, are small beside those of values + 128.
 __device__ __forceinline__ f16x8 codes_sub(uint32_t w0, uint32_t w1) {
   w0 ^= 0x80808080u;
   w1 ^= 0x80808080u;
@@ -185,28 +186,32 @@ __device__ __forceinline__ QueryScale query_scale(float scale, const float (&x)[
   amax = max_groups(amax);
   const int e = min(max((int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 127, -100), 120);
   const float up = scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
-  return {up, fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8) * 16777216.0f};
+  return {up, fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8)};
 }
-// One k step's operands, high and low, and their sums.
-__device__ __forceinline__ void split_query(const float (&x)[8], float up, f16x8& qh, f16x8& ql, float& sum_h,
-                                            float& sum_l) {
-  sum_h = sum_l = 0.0f;
+// One k step's operands, high and low; returns their sum.
+__device__ __forceinline__ float split_query(const float (&x)[8], float up, f16x8& qh, f16x8& ql) {
+  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f16x2 hi, lo;
     split2(x[2 * i] * up, x[2 * i + 1] * up, hi, lo);
     qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
     ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
-    sum_h += (float)hi[0] + (float)hi[1];
-    sum_l += (float)lo[0] + (float)lo[1];
+    sum += ((float)hi[0] + (float)hi[1]) + ((float)lo[0] + (float)lo[1]);
   }
+  return sum;
 }
 constexpr float kBias = -128.0f / 16777216.0f;  // times a row's sum: where its scores start (codes_sub)
 
 // The V scale of the lane's 16 positions in a step.  Weights take it with the
-// exponential: e^(s - m) vn = 2^(s' - m' + lv), vn = vs * 2^(14 - ve) = 2^lv
-// <= 2^15, and sums of weights are multiplied by rl = 2^-lv.  (Far below the
+// exponential: e^(s - m) vs 2^(kUp - ve) = 2^(s' - m' + lv + kUp), vs 2^-ve =
+// 2^lv < 2, and sums of weights are multiplied by rl = 2^-lv.  (Far below the
 // largest scale, 0 included, lv ends at -40: those weights are 0 as fp16.)
+// kUp keeps the low halves of small weights out of fp16's smallest numbers
+// (2^-31 of the largest weight); at 14 the exponents near it, and log2 of the
+// scales with it, were rounded at twice the size, and results were up to half
+// as far off again.
+constexpr int kUp = 6;
 struct VScale {
   float lv, rl;
 };
@@ -224,7 +229,7 @@ __device__ __forceinline__ VScale v_scale(float vs, int& ve, f32x4 (&o)[NT][DT])
       for (int d = 0; d < DT; ++d) o[u][d] *= f;
     ve = e;
   }
-  const float lv = fmaxf(__builtin_amdgcn_logf(vs * pow2i(14 - ve)), -40.0f);
+  const float lv = fmaxf(__builtin_amdgcn_logf(vs * pow2i(-ve)), -40.0f);
   return {lv, __builtin_amdgcn_exp2f(-lv)};
 }
 // One row's 16 scores of a step (times f: in units of log2): the running
@@ -254,7 +259,7 @@ __device__ __forceinline__ void row_maximum(f32x4 (&sc)[4], float& f, bool maske
 // and their weights, as operands of the second product (high and low).
 __device__ __forceinline__ void row_weights(const f32x4 (&sc)[4], float f, const VScale& v, float m, float& l,
                                             f16x8 (&hi)[2], f16x8 (&lo)[2]) {
-  const float off = v.lv - (m == kNegInf ? 0.0f : m);
+  const float off = v.lv + ((float)kUp - (m == kNegInf ? 0.0f : m));
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -296,8 +301,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   };
   __shared__ Share sh;
   __shared__ float sml[W][16 * NT][2];
-  // a row's |scale| * log2(e) * powers of two, and the sums of its operands
-  __shared__ float qfac[16 * NT], qsum[KS][16 * NT];
+  __shared__ float qfac[16 * NT];  // a row's |scale| * log2(e) * powers of two
   __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
   __shared__ float kscale[kGroups], vscale[kGroups];
 
@@ -345,7 +349,6 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < PREP; ++i) {
       f16x8 qh, ql;
-      float sum_h, sum_l;
       float part[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -353,15 +356,13 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
         for (int j = 1; j < KS / PREP; ++j) part[e] = pj == j * PREP ? x[8 * (j * PREP + i) + e] : part[e];
       }
-      split_query(part, f.up, qh, ql, sum_h, sum_l);
+      split_query(part, f.up, qh, ql);
       if constexpr (PACK) {
         sh.q[pu][pj + i][0][lane] = low ? ql : qh;
       } else {
         sh.q[pu][pj + i][0][lane] = qh;
         sh.q[pu][pj + i][1][lane] = ql;
       }
-      const float s = sum_groups(PACK ? (low ? sum_l : sum_h) : sum_h + sum_l);
-      if (g == 0) qsum[pj + i][16 * pu + n] = s;
     }
   };
   int32_t pos[NT];  // last position that the row sees (-1: none)
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[u][d] = {0.0f, 0.0f, 0.0f, 0.0f};
   }
-  int ve = -100;  // o holds sums of code * weight * 2^(14 - ve)
+  int ve = -100;  // o holds sums of code * weight * vs * 2^(kUp - ve), l of weight * 2^kUp
 
   // position of the tile that every row sees: below it no mask is needed
   const int64_t all_see = min(sv.len, sv.pos0 + (int)a.by_g.div(row_lo) + 1);
@@ -430,24 +431,16 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
     if (prepares) prepare_q();
   });
   __syncthreads();
-  float fac[NT], bias[NT];
+  float fac[NT];
 #pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    fac[u] = qfac[16 * u + n];
-    bias[u] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < KS; ++j) bias[u] += qsum[j][16 * u + n];
-    bias[u] *= kBias;
-  }
+  for (int u = 0; u < NT; ++u) fac[u] = qfac[16 * u + n];
   for (;;) {
     f32x4 sc[NT][4];
     auto scores = [&]() {
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        const float b = bias[u];
+      for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) sc[u][t] = {b, b, b, b};
-      }
+        for (int t = 0; t < 4; ++t) sc[u][t] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
         f16x8 q[NT][2];
@@ -459,7 +452,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
         f16x8 kf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          kf[t] = codes_sub(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
+          kf[t] = codes_f16(kw[t][j / 2][2 * (j % 2)], kw[t][j / 2][2 * (j % 2) + 1]);
 #pragma unroll
           for (int u = 0; u < NT; ++u) sc[u][t] = mfma(kf[t], q[u][0], sc[u][t]);
         }
@@ -547,10 +540,10 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
   }
 
   // join the waves, a tile at a time
-  const float back = pow2i(max(ve - 14, -126));
+  const float back = pow2i(max(ve - kUp, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]);
+    const float lt = sum_groups(l[u]) * pow2i(-kUp);
     if (g == 0) sml[wave][16 * u + n][0] = m[u], sml[wave][16 * u + n][1] = lt;
   }
 #pragma unroll
@@ -664,15 +657,14 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
 #pragma unroll
     for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
     const QueryScale f = query_scale<D>(a.scale, x);
-    qfac[u] = f.factor;
+    qfac[u] = f.factor * 16777216.0f;  // (of codes_sub)
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-      float part[8], sum_h, sum_l;
+      float part[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) part[e] = x[8 * j + e];
-      split_query(part, f.up, qh[u][j], ql[u][j], sum_h, sum_l);
-      sum += sum_h + sum_l;
+      sum += split_query(part, f.up, qh[u][j], ql[u][j]);
     }
     qbias[u] = kBias * sum_groups(sum);
   }
@@ -821,10 +813,10 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     }
   }
 
-  const float back = pow2i(max(ve - 14, -126));
+  const float back = pow2i(max(ve - kUp, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]);
+    const float lt = sum_groups(l[u]) * pow2i(-kUp);
     const int r = row_lo + 16 * (NT * wave + u) + n;
     if (r >= rows) continue;
     uint32_t rem;
