@@ -28,8 +28,10 @@ same gate projections in 2-bit and in 1.6-bit rows; the weight quantiser;
 one decode step (quantiser, stack, head) eager and replayed from a HIP
 graph, with the quantiser fused into the stack launch (two launches) and as
 a launch of its own (three); the whole 8B stack at M = 16; q/k/v and gate/up
-sharing inputs; block-wise scales inside the stack; and the activation
-quantiser.  Most lines carry the oracle timed on a bounded sample of the
+sharing inputs; block-wise scales inside the stack; the activation
+quantiser; and the calls between the linears (norm with int8 output, int8
+cache append and attention, sampling), alone and in a step from the residual
+stream to the sampled token.  Most lines carry the oracle timed on a bounded sample of the
 same workload.
 """
 from __future__ import annotations
