@@ -226,7 +226,7 @@ void launch_rows(bool vec, int64_t M, const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int64_t rmsnorm_work_items(int64_t M) { return M * kLongT; }
+int64_t rmsnorm_work_items(int64_t M) { return mul_sat(M, kLongT); }
 
 hipError_t launch_rmsnorm_quantize(const float* x, int64_t ldx, const float* res, int64_t ldr, const float* gain,
                                    float eps, int64_t M, int64_t K, float* h, int64_t ldh, int8_t* q,

@@ -866,7 +866,7 @@ __global__ __launch_bounds__(T) void finish_kernel(Launch L) {
     before += mine[e];
   }
   __syncthreads();
-  const int c = (int)F.out32[0];
+  const int c = (int)min(F.out32[0], (uint32_t)L.chunks - 1);
   before = F.out64;
 
   // the tile of that chunk, four tokens per thread, and the token in it
@@ -907,7 +907,7 @@ __global__ __launch_bounds__(T) void finish_kernel(Launch L) {
       }
     }
     __syncthreads();
-    for (;; at += kTile) {  // (every thread alike)
+    for (; at + kTile < j1; at += kTile) {  // (every thread alike; the last tile needs no look)
       u64 sum = 0;
 #pragma unroll
       for (int v = 0; v < T / 64; ++v) sum += F.tiles[(at - j0) / kTile][v];
@@ -944,7 +944,7 @@ __global__ __launch_bounds__(T) void finish_kernel(Launch L) {
 // rows want no more than about 2,048 workgroups (64 rows: 61 us at 4,096, 56 at
 // 8,192, 59 at 16,384; 96 rows: 69 at 8,192, 81 at 16,384).
 int64_t tokens_per_chunk(int64_t M, int64_t N, bool cuts) {
-  auto chunks = [&](int64_t per) { return M * ((N + per - 1) / per); };
+  auto chunks = [&](int64_t per) { return mul_sat(M, (N + per - 1) / per); };
   if (chunks(kChunkMin) <= (cuts ? 256 : 1280)) return kChunkMin;
   int64_t per = 4 * kChunkMin;
   while (per < kChunkMax && chunks(per) > 2048) per *= 2;

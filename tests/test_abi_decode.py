@@ -112,3 +112,11 @@ def test_sample_refusals(lib):
     assert sample(lib, M=0, x=None, token=None) == OK
     assert lib.tern_sample_workspace_bytes(-1, 100) == 0
     assert lib.tern_sample_workspace_bytes(4, tern.TERN_SAMPLE_MAX_N + 1) == 0
+
+
+def test_sizes_that_do_not_fit_64_bits(lib):
+    """Row counts whose work-items pass 2^64 are refused too."""
+    assert norm(lib, M=2 ** 54 + 1) == RANGE
+    for M in (2 ** 44, 2 ** 54 + 1, 2 ** 62):
+        assert sample(lib, M=M) == RANGE
+        assert lib.tern_sample_workspace_bytes(M, 151936) == 0
