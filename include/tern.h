@@ -539,9 +539,10 @@ int tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, const
  *     y   = sum_j e^(a_j - max a) v_j / sum_j e^(a_j - max a)
  * to the accuracy of fp32 (codes and both factors beside them enter the
  * matrix cores at 22 bits or more; statistics and sums are fp32).  A row that
- * sees no position is 0.  Rows of no sequence are left as they were.
+ * sees no position is 0.  Rows of no sequence are left as they were.  A row
+ * of q that is not finite spoils its own row and head of y alone.
  *   q, y  device, rows x (q_heads * head_dim) floats, row strides ldq and
- *         ldy >= q_heads * head_dim (when rows > 1), 4-byte aligned; q finite;
+ *         ldy >= q_heads * head_dim (when rows > 1), 4-byte aligned;
  *         scale finite, q_heads a multiple of heads;
  *   workspace  device, 256-byte aligned, at least
  *         tern_attention_workspace_bytes(cache, batch, q_heads) bytes (0 on bad

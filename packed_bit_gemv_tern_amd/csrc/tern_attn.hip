@@ -41,9 +41,9 @@ namespace {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 64;  // positions per step of a wave
+constexpr int kWaves = 4;  // of a workgroup
 constexpr int kJoinWaves = 4;
 
 // n / d for 0 <= n < 2^31 by a multiplication (an integer division is some
@@ -282,11 +282,12 @@ __device__ __forceinline__ int swizzle(int g) { return (0x84C0 >> (4 * g)) & 15;
 
 // One workgroup: one (sequence, KV head), 16 * NT rows (row i: new token i /
 // G, query head i % G of the KV head's), one chunk of the positions, whose
-// steps the W waves take in turn.  PACK: 8 rows, whose high and low
+// steps the four waves take in turn.  PACK: 8 rows, whose high and low
 // operands are the columns 0-7 and 8-15 of one matrix operand, so a product
 // takes one instruction where two tiles would take two.
-template <int D, int NT, bool PACK, int W>
-__global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
+template <int D, int NT, bool PACK>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
+  constexpr int W = kWaves;
   constexpr int KS = D / 32;  // k steps of the first product
   constexpr int DT = D / 16;  // 16-dim tiles of the output
   constexpr int LD = D + 4;
@@ -578,7 +579,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
       const int64_t row = sv.row0 + a.by_g.divmod(row_lo + r, rem), hq = h * G + rem;
       if (a.nchunk == 1) {
         float* y = a.y + row * a.ldy + hq * D + d;
-        os *= ls > 0.0f ? 1.0f / ls : 0.0f;
+        os *= ls == 0.0f ? 0.0f : 1.0f / ls;
         if (a.y16) {
           store_g(reinterpret_cast<f32x4*>(y), os);
         } else {
@@ -611,8 +612,8 @@ __global__ __launch_bounds__(64 * W, 2) void attn_kernel(AttnArgs a) {
 // exponentials.  Matrix bound: four products (two halves each of Q and P)
 // where 16-bit attention takes two.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
-  constexpr int KS = D / 32, DT = D / 16, NT = 2, W = 4, ROWS = 16 * NT * W;
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a) {
+  constexpr int KS = D / 32, DT = D / 16, NT = 2, W = kWaves, ROWS = 16 * NT * W;
   constexpr int kGroups = 64 * W, kWindow = 16 * kGroups;
   constexpr int NP = D / 64;  // 16-code pieces of K, and of V, per thread
   __shared__ f16x8 kf[2][4][KS][64];
@@ -823,7 +824,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     const int64_t row = sv.row0 + a.by_g.divmod(r, rem), hq = h * G + rem;
     const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
     const bool whole = a.nchunk == 1;
-    const float f = whole ? (lt > 0.0f ? back / lt : 0.0f) : back;
+    const float f = whole ? (lt == 0.0f ? 0.0f : back / lt) : back;
     float* out = whole ? a.y + row * a.ldy + hq * D : a.part + at * D;
     if (!whole && g == 0) {
       store_g(a.part_ml + 2 * at, m[u]);
@@ -868,8 +869,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) 
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor(mn, d, 64));
     mn = fmaxf(mn, m);
-    if (mn == kNegInf) continue;  // (nothing seen yet)
-    const float al = __builtin_amdgcn_exp2f(m - mn), f = __builtin_amdgcn_exp2f(mc - mn);
+    const float from = mn == kNegInf ? 0.0f : mn;  // (nothing seen yet: factors of 0)
+    const float al = __builtin_amdgcn_exp2f(m - from), f = __builtin_amdgcn_exp2f(mc - from);
     m = mn;
     float ls = lc * f;
 #pragma unroll
@@ -900,22 +901,35 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) 
       ls = __builtin_fmaf(sml[w][1], f, ls);
       os = __builtin_fmaf(so[w][d], f, os);
     }
-    store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls > 0.0f ? os / ls : 0.0f);
+    store_g(a.y + row * a.ldy + (int64_t)hq * D + d, ls == 0.0f ? 0.0f : os / ls);
   }
 }
 
-// 16-row tiles per workgroup (or per wave, for prompts).
-AttnKind attn_kind(int64_t rows) {
-  return rows <= 8 ? ATTN_PACKED : rows <= 16 ? ATTN_16 : rows <= 64 ? ATTN_32 : ATTN_PROMPT;
-}
 int attn_rows(AttnKind k) { return k == ATTN_PACKED ? 8 : k == ATTN_16 ? 16 : k == ATTN_32 ? 32 : 128; }
+
+// Which kernel, by a sequence's rows per KV head.  Up to 32 the smallest tile
+// that holds them (32 ragged contexts to 4,096, 8 KV heads: 8 rows 46.7 us
+// packed, 47.3 by 16; 16 rows 52 by 16, 60 by 32, 77 by two of 8; 32 rows 67 by
+// 32, 82 by two of 16; eight of 2,048, 24 rows: 17.9 by 32, 18.2 by 16).  Beyond
+// 128 the prompt kernel pays once it has its two workgroups on every CU (8 x
+// 1,024 tokens from nothing: 183 us, 248 by 32; 4 x 512 on 4,096 194 and 197),
+// the contexts are so long that they can be split for that (1,024 on 32,768:
+// 864, 1,028), or they are so short that starting counts (8 x 128: 16, 23).
+// Else tiles of 32 spread better (512 on 4,096: 75, 93; 4 x 256 on 4,096: 148,
+// 168; up to 128 rows always: 8 x 32 on 2,048 28, 42).
+AttnKind attn_kind(int64_t rows, int64_t groups, int64_t len, int cus) {
+  if (rows <= 32) return rows <= 8 ? ATTN_PACKED : rows <= 16 ? ATTN_16 : ATTN_32;
+  const int64_t units = mul_sat(groups, (rows + 127) / 128);
+  const bool prompt = units >= 2 * cus || len > 16384 || (units >= cus && len <= 512);
+  return rows > 128 && prompt ? ATTN_PROMPT : ATTN_32;
+}
 
 template <int D>
 void launch_kind(AttnKind k, dim3 grid, dim3 block, const AttnArgs& a, hipStream_t s) {
   switch (k) {
-    case ATTN_PACKED: hipLaunchKernelGGL((attn_kernel<D, 1, true, 4>), grid, block, 0, s, a); break;
-    case ATTN_16: hipLaunchKernelGGL((attn_kernel<D, 1, false, 4>), grid, block, 0, s, a); break;
-    case ATTN_32: hipLaunchKernelGGL((attn_kernel<D, 2, false, 4>), grid, block, 0, s, a); break;
+    case ATTN_PACKED: hipLaunchKernelGGL((attn_kernel<D, 1, true>), grid, block, 0, s, a); break;
+    case ATTN_16: hipLaunchKernelGGL((attn_kernel<D, 1, false>), grid, block, 0, s, a); break;
+    case ATTN_32: hipLaunchKernelGGL((attn_kernel<D, 2, false>), grid, block, 0, s, a); break;
     case ATTN_PROMPT: hipLaunchKernelGGL((attn_prompt_kernel<D>), grid, block, 0, s, a); break;
   }
 }
@@ -925,24 +939,39 @@ void launch_kind(AttnKind k, dim3 grid, dim3 block, const AttnArgs& a, hipStream
 AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   AttnPlan p;
   const int64_t G = Hq / kv.H, rows = kv.max_new * G;
-  p.kind = attn_kind(rows);
-  const int64_t tile = attn_rows(p.kind);
-  p.row_tiles = (rows + tile - 1) / tile;
   const int64_t most = kv.ld_table << kv.log_p;
   const int64_t len = kv.max_len > 0 ? std::min(kv.max_len, most) : most;
+  p.kind = attn_kind(rows, kv.S * kv.H, len, cus);
+  const int64_t tile = attn_rows(p.kind);
+  p.row_tiles = (rows + tile - 1) / tile;
   const int64_t units = mul_sat(kv.S * kv.H, p.row_tiles);
-  p.waves = 4;
-  const int64_t step = kStep * p.waves;
-  // Positions per workgroup.  One sequence: what gives every CU one workgroup;
-  // several, ragged as a rule: two, and pieces short enough to even them out.
-  const int64_t want = std::max<int64_t>(1, cus * (kv.S > 1 ? 2 : 1) / units);
+  // Pieces of a context.  Together one workgroup per CU: a second round of
+  // workgroups, each three trips to memory before its first product, costs more
+  // than it evens out (32 ragged contexts to 4,096: whole 36 us, halves 41,
+  // quarters 44; 16 to 2,048 in 1, 2, 4, 8 pieces: 19.1, 17.2, 17.4, 20.5), and
+  // more than 64 pieces cost more to join (one KV head, 32,768 positions: 64
+  // pieces 17.7 us, 128 19.8).  Two per CU where products count: prompts (1,024
+  // rows on 32,768: 246 us, 344 with one), 32 rows on long contexts (256 rows on
+  // 32,768: 84, 97), if that is at most 32 pieces (32 rows: 28 in 32, 40 in 64).
+  const bool two = p.kind == ATTN_PROMPT || (p.kind == ATTN_32 && len > 4096);
+  int64_t want = cus / units;
+  if (two && 2 * cus / units <= 32) want = 2 * cus / units;
+  // Short ones whole, without the joining launch (512 positions: 9.3 us whole, 11.0
+  // in two; 1,024 with a workgroup on half of the CUs 12.9, 14.0).
+  if (len <= 512 || (len <= 1024 && units >= cus / 2) || (len <= 4096 && units >= cus)) want = 1;
+  want = std::min<int64_t>(std::max<int64_t>(want, 1), 64);
   int64_t chunk = (len + want - 1) / want;
-  if (units < 4 * cus && kv.S > 1) chunk = std::min(chunk, std::max<int64_t>(1280, len / 8));
-  if (units >= cus / 2 && len <= 1024) chunk = len;
+  // A batch of long contexts of single tokens is taken to be ragged, and cut finer
+  // to even it out (lengths up to 8,192 over 48 sequences: 80 us, 103 whole; to
+  // 16,384 over 32: 119, 132; where all are as long as the longest that costs:
+  // 154, 148 and 192, 180).  With more rows the pieces' starts cost more than
+  // that (8 x 64 rows on 8,192 each: 55 us in 4, 69 in 7).
+  if (kv.S > 1 && rows <= 16 && len > 4096 && units < 4 * cus) chunk = std::min(chunk, std::max<int64_t>(1280, len / 8));
+  const int64_t step = kStep * kWaves;
   chunk = std::max<int64_t>(step, (chunk + step - 1) / step * step);
   p.chunk = std::min<int64_t>(chunk, 1ll << 30);
   p.nchunk = std::max<int64_t>(1, (len + p.chunk - 1) / p.chunk);
-  p.work_items = mul_sat(mul_sat(units, p.nchunk), 64 * p.waves);
+  p.work_items = mul_sat(mul_sat(units, p.nchunk), 64 * kWaves);
   p.join_items = p.nchunk > 1 ? mul_sat(mul_sat(kv.S * kv.max_new, Hq), 64 * kJoinWaves) : 0;
   p.workspace = p.nchunk > 1 ? mul_sat((int64_t)kv.rows * Hq, p.nchunk * (kv.D + 2) * 4) : 0;
   return p;
@@ -972,7 +1001,7 @@ hipError_t launch_attention(const KvArgs& kv, const AttnPlan& p, const float* q,
   };
   a.q16 = rows16(q, ldq);
   a.y16 = rows16(y, ldy);
-  const dim3 grid((unsigned)(p.work_items / (64 * p.waves))), block(64 * p.waves), jblock(64 * kJoinWaves);
+  const dim3 grid((unsigned)(p.work_items / (64 * kWaves))), block(64 * kWaves), jblock(64 * kJoinWaves);
   if (kv.D == 64)
     launch_kind<64>(p.kind, grid, block, a, s);
   else

@@ -301,7 +301,6 @@ hipError_t launch_kv_append(const KvArgs& a, const float* k, int64_t ldk, const 
 enum AttnKind { ATTN_PACKED, ATTN_16, ATTN_32, ATTN_PROMPT };  // 8, 16, 32, 128 rows per workgroup
 struct AttnPlan {
   AttnKind kind;
-  int waves;          // waves of a workgroup
   int64_t row_tiles;  // row tiles of a sequence and KV head
   int64_t chunk, nchunk;
   int64_t work_items, join_items, workspace;

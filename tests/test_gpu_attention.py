@@ -180,3 +180,62 @@ def test_prompt_with_bad_pages_and_scales():
     pg.table[0, [0, 3, 7]], pg.table[1, :] = -1, pg.host.pages
     got = attend(pg, [40, 70, 90], [300, 200, 90], 8, rows=230)
     assert (got[40:110] == 0).all() and (got[200:] == 77).all()
+
+
+def pad_table(pg, positions):
+    """More columns than the sequences need: what the split is chosen by where
+    no longest length is given."""
+    columns = -(-positions // pg.P)
+    pg.table = np.pad(pg.table, ((0, 0), (0, columns - pg.table.shape[1])), constant_values=-1)
+
+
+@pytest.mark.parametrize("new,length,heads,group,P,D", [
+    ([130, 1, 77], [130, 40, 300], 2, 4, 16, 128), ([33, 64], [700, 64], 1, 4, 64, 64),
+    ([200], [4500], 1, 2, 32, 128), ([65, 128], [5000, 4097], 1, 2, 128, 128), ([17, 40], [17, 1000], 2, 8, 64, 64),
+    ([300], [300], 1, 5, 16, 64)])
+def test_prompts_in_long_tables(new, length, heads, group, P, D):
+    """Tables of 20,000 positions and more: tiles of 128 rows, in pieces, most
+    of them empty."""
+    pg = Paged(len(new), -(-max(length) // P), heads, D, P, seed=15).upload()
+    pad_table(pg, 20000)
+    attend(pg, new, length, heads * group)
+    pad_table(pg, 100000)
+    attend(pg, new, length, heads * group, extra=3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_among_idle_slots(D):
+    """Enough workgroups for tiles of 128 rows over whole contexts: windows of
+    pages, a last tile of two rows, idle slots."""
+    pg = Paged(520, 2, 1, D, 64, seed=16).upload()
+    pg.table = np.pad(pg.table, ((0, 0), (0, 78)), constant_values=-1)
+    pg.table[0] = pg.table[: 80, 0]
+    pg.table[519] = pg.table[100: 180, 1]
+    got = attend(pg, [130] + [1] * 517 + [2, 65], [5101] + [0] * 517 + [2, 4096], 2)
+    assert (got[130: 647] == 0).all()
+
+
+def test_many_short_prompts():
+    pg = Paged(16, 5, 8, 64, 32, seed=17).upload()
+    attend(pg, [17, 33] * 8, [150, 33] * 8, 32)
+
+
+@pytest.mark.parametrize("new,columns", [(1, 5), (1, 40), (3, 40), (6, 40), (20, 40), (50, 40), (50, 320)])
+def test_queries_that_are_not_finite(new, columns):
+    """NaN and infinity in a row of q stay in its row and head, whatever the
+    tile and the split."""
+    pg = Paged(2, 5, 1, 64, 64, seed=18).upload()
+    pad_table(pg, 64 * columns)
+    q = pg.rng.normal(0, 2, (2 * new, 4, 64)).astype(np.float32)
+    length = [300, 200]
+    good = attend(pg, [new, new], length, 4, q=q)
+    b = pg.batch([new, new], length)
+    q[0, 1, 5], q[2 * new - 1, 2, 63] = np.nan, np.inf
+    qd, y = to_dev(q), torch.full((2 * new, 256), 77.0, device=DEV)
+    ws = torch.empty(tern.tern_attention_workspace_bytes(pg.cache, b, 4), dtype=torch.uint8, device=DEV)
+    tern.tern_attention(pg.cache, b, qd, 256, 4, 64 ** -0.5, y, 256, ws)
+    got = y.cpu().numpy().reshape(2 * new, 4, 64)
+    spoilt = np.zeros((2 * new, 4), bool)
+    spoilt[0, 1] = spoilt[2 * new - 1, 2] = True
+    assert np.isnan(got[spoilt]).all()
+    assert (got[~spoilt] == good[~spoilt]).all()
