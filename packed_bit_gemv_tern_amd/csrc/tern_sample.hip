@@ -540,9 +540,13 @@ __device__ Cut find_cut(const Row& r, const Bins<T>& bins, CutLds& S) {
 
 // A logit that every token of the kept and listed bins reaches: one comparison
 // passes over the others (most of a row).  Bin b ends at v = (3 b + 2.5) ln 2 /
-// 64; half a step more, and two fp32 steps, are over any rounding.
+// 64; half a step more, and two fp32 steps, are over any rounding.  Of the
+// kept bins, min-p ends the last (that of -64 log2 min_p + 1/2 steps, with a
+// slack of most of a bin).
 __device__ __forceinline__ float cut_logit(const Row& r, const Cut& c) {
-  const int last = max(max(c.sure - 1, c.p2), c.kbin < kBins ? c.kbin : 0);
+  const float steps = -64.0f * __builtin_amdgcn_logf((float)r.min_p);  // (inf: no limit)
+  const int kept = min(c.sure - 1, (int)fminf(steps / 3.0f + 1.0f, (float)kBins));
+  const int last = max(max(kept, c.p2), c.kbin < kBins ? c.kbin : 0);
   if (last >= kBins - 1 || !(r.mx < __builtin_inff())) return -__builtin_inff();
   const double x = (double)r.mx - (3 * last + 3) * 0x1.62e42fefa39efp-7 / r.inv_t;
   return (float)(x - 3e-7 * fabs(x));
