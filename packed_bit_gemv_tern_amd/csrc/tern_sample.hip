@@ -54,6 +54,7 @@ constexpr int kT = 256;          // threads of launches 1 to 3
 constexpr int kFinishFew = 256, kFinishMany = 1024;
 constexpr int kBins = 1024;      // of 3 steps of 2^(-1/64) each; the last one holds all that is further below
 constexpr uint32_t kListMax = 2048;
+constexpr uint32_t kMine = kListMax;  // those that one chunk lists
 constexpr int kChunkMin = 4 * kT;
 constexpr int kChunkMax = 16384;
 constexpr int kChunksMax = TERN_SAMPLE_MAX_N / kChunkMin;
@@ -561,6 +562,10 @@ __global__ __launch_bounds__(kT) void gather_kernel(Launch L) {
   __shared__ double tab[64];
   __shared__ u64 red[32];
   __shared__ CutLds S;
+  // listed tokens gather here first: a wave that asks memory for each one's
+  // place waits for every answer
+  __shared__ u64 mine[kMine];
+  __shared__ uint32_t mine_n, mine_at;
   const int c = blockIdx.x % L.chunks;
   const int64_t row = blockIdx.x / L.chunks;
   const RowWs w = row_ws(L, row);
@@ -571,6 +576,7 @@ __global__ __launch_bounds__(kT) void gather_kernel(Launch L) {
   const Row r = load_row<kT>(L, w, row, red);
   if (r.greedy || r.live == 0) return;
   if (threadIdx.x < 64) tab[threadIdx.x] = kExp2[threadIdx.x];
+  if (threadIdx.x == 0) mine_n = 0;
   __syncthreads();
   const Cut cut = find_cut<kT>(r, bins, S);
   const float least = cut_logit(r, cut);
@@ -586,12 +592,18 @@ __global__ __launch_bounds__(kT) void gather_kernel(Launch L) {
         ++kept;
       }
     } else if (listed(cut, b)) {
-      const uint32_t at = atomicAdd(w.list_n, 1u);
-      if (at < kListMax) store_g(w.list + at, pack_token(logit_key(x), j));
+      const uint32_t at = atomicAdd(&mine_n, 1u);
+      if (at < kMine) mine[at] = pack_token(logit_key(x), j);
     }
   });
+  __syncthreads();
+  const uint32_t found = mine_n;
+  if (threadIdx.x == 0 && found) mine_at = atomicAdd(w.list_n, found);
   u64 total, n;
   wg_scan2<kT>(sum, kept, S.wave, total, n);
+  // (where the tokens here are too many for the list, it is not read)
+  for (uint32_t i = threadIdx.x; i < min(found, kMine); i += kT)
+    if (mine_at + i < kListMax) store_g(w.list + mine_at + i, mine[i]);
   if (threadIdx.x == 0) {
     store_g(w.chunk_mass + c, total);
     store_g(w.chunk_kept + c, (uint32_t)n);
