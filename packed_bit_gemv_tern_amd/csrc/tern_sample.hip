@@ -32,10 +32,14 @@
 // 0.5 ms).
 //
 // Times of the launches for 151,936 tokens: one row with top-k and top-p 2.9 +
-// 8.1 + 5.6 + 8.0 us, each a launch and one or two trips to memory, bins and
-// scans between barriers; 96 rows of mixed filters 12.6 + 22 + 22 + 17 us, where
-// the row maxima run at 4.6 TB/s and the two other passes at 2.7: two LDS
-// additions a token in one, a weight in fp64 of the kept ones in the other.
+// 8.2 + 5.6 + 7.9 us, each a launch and one or two trips to memory, bins and
+// scans between barriers; 96 rows of mixed filters 12.4 + 22 + 20 + 17 us.  There
+// the maxima run at 4.7 TB/s, and so would the histogram without its weights:
+// those, some seventeen fp64 instructions a token, take 10 of its 22 us (its
+// additions in LDS 2).  Not better: the steps below the maximum in fp32 with
+// the rounding made up for in the series (1 us more), a series of twelve terms
+// in place of the table (5 us more), tiles of 32 tokens a thread, the next tile
+// ahead.
 #include "tern.h"
 #include "tern_device.h"
 
