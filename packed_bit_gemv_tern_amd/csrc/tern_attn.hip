@@ -286,8 +286,8 @@ __device__ __forceinline__ int swizzle(int g) { return (0x84C0 >> (4 * g)) & 15;
 // operands are the columns 0-7 and 8-15 of one matrix operand, so a product
 // takes one instruction where two tiles would take two.
 // HBM bound for many sequences: 48 contexts to 8,192 (363 MB of codes) in 72
-// us, 5.0 TB/s.  Short of that a chain bounds it: three trips to memory (the
-// sequence; page ids and q; scales, K and V), 1.8 us per step of a wave, the
+// us, 5.0 TB/s.  Short of that a chain bounds it: two trips to memory (the
+// sequence and page ids; q, scales, K and V), 1.8 us per step of a wave, the
 // join: one token on 4,099 positions 7.9 + 4.5 us (8.4 MB: 1.7 at HBM's rate),
 // eight on 32,771 23 + 5 (67 MB: 14).
 template <int D, int NT, bool PACK>
@@ -316,13 +316,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   const int s = (int)a.by_tiles.divmod(a.by_chunks.divmod(a.by_h.divmod(blockIdx.x, h), cu), tile);
   const int c = (int)cu, G = (int)a.by_g.d;
   const int rt = a.row_tiles - 1 - (int)tile;
+  const int64_t c0 = (int64_t)c * a.chunk;
+  // (asked for before the sequence is known: its length only says which count)
+  int32_t entry = page_entry(kv, s, (c0 + 16 * (int)threadIdx.x) >> kv.log_p);
   const SeqView sv = seq_view(kv, s);
   const int rows = min(sv.n, (int)kv.max_new) * G, row_lo = rt * ROWS;
   if (row_lo >= rows) return;
   // positions that some row of the tile sees: up to the last row's own
   const int64_t last_pos = sv.pos0 + (int)a.by_g.div(min(row_lo + ROWS - 1, rows - 1));
   const int64_t end = min(sv.len, last_pos + 1);
-  const int64_t c0 = (int64_t)c * a.chunk;
   const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
   // (chunk 0 always writes: it is the one that the joining pass counts on)
   if (c0 >= c1 && c > 0) return;
@@ -332,8 +334,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   const int nr = PACK ? n & 7 : n;  // the lane's row of a tile
   const bool low = PACK && n >= 8;  // the lane holds low operands
 
-  // Loads in three trips to memory: the sequence; page ids and query rows;
-  // scales, K and V.  The query operands are prepared by all the waves, some k
+  // Loads in two trips to memory: the sequence and page ids; query rows, scales,
+  // K and V.  The query operands are prepared by all the waves, some k
   // steps of one tile each, while the first K and V are under way.
   constexpr int PREP = NT * KS > W ? NT * KS / W : 1;  // operands per wave
   const int pu = wave * PREP / KS, pj = wave * PREP % KS;
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   // is done while those are on their way.
   auto open_window = [&](auto meanwhile) {
     const int64_t j = w0 + 16 * (int)threadIdx.x;
-    const int32_t id = j < sv.len ? page_of(kv, s, j >> kv.log_p) : -1;
+    const int32_t id = j < sv.len ? valid_page(kv, entry) : -1;
     const int64_t si = (int64_t)max(id, 0) * kv.H + h;
     const float ks = load_g(kv.k_scale + si), vs = load_g(kv.v_scale + si);
     page[threadIdx.x] = id;
@@ -540,6 +542,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
     }
     w0 += kWindow;
     if (w0 >= c1) break;
+    entry = page_entry(kv, s, (w0 + 16 * (int)threadIdx.x) >> kv.log_p);
     __syncthreads();  // (the window before has been read)
     open_window([]() {});
     __syncthreads();
@@ -956,7 +959,7 @@ AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   p.row_tiles = (rows + tile - 1) / tile;
   const int64_t units = mul_sat(kv.S * kv.H, p.row_tiles);
   // Pieces of a context.  Together one workgroup per CU: a second round of
-  // workgroups, each three trips to memory before its first product, costs more
+  // workgroups, each two trips to memory before its first product, costs more
   // than it evens out (32 ragged contexts to 4,096: whole 36 us, halves 41,
   // quarters 44; 16 to 2,048 in 1, 2, 4, 8 pieces: 19.1, 17.2, 17.4, 20.5), and
   // more than 64 pieces cost more to join (one KV head, 32,768 positions: 64

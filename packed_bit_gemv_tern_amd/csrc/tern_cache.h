@@ -28,11 +28,14 @@ __device__ __forceinline__ SeqView seq_view(const KvArgs& a, int s) {
   return v;
 }
 
-// Page `j` of a sequence, or -1 (past the table, or an id outside the cache).
+// Page `j` of a sequence as the table has it (-1 past the table), and that or -1
+// where it is an id outside the cache.
+__device__ __forceinline__ int32_t page_entry(const KvArgs& a, int s, int64_t j) {
+  return j < 0 || j >= a.ld_table ? -1 : load_g(a.table + (int64_t)s * a.ld_table + j);
+}
+__device__ __forceinline__ int32_t valid_page(const KvArgs& a, int32_t id) { return id >= 0 && id < a.pages ? id : -1; }
 __device__ __forceinline__ int32_t page_of(const KvArgs& a, int s, int64_t j) {
-  if (j < 0 || j >= a.ld_table) return -1;
-  const int32_t id = load_g(a.table + (int64_t)s * a.ld_table + j);
-  return id >= 0 && id < a.pages ? id : -1;
+  return valid_page(a, page_entry(a, s, j));
 }
 
 }  // namespace tern
