@@ -288,8 +288,8 @@ __device__ __forceinline__ int swizzle(int g) { return (0x84C0 >> (4 * g)) & 15;
 // HBM bound for many sequences: 48 contexts to 8,192 (363 MB of codes) in 72
 // us, 5.0 TB/s.  Short of that a chain bounds it: two trips to memory (the
 // sequence and page ids; q, scales, K and V), 1.8 us per step of a wave, the
-// join: one token on 4,099 positions 7.9 + 4.5 us (8.4 MB: 1.7 at HBM's rate),
-// eight on 32,771 23 + 5 (67 MB: 14).
+// join: one token on 4,099 positions 7.4 + 3.9 us (8.4 MB: 1.7 at HBM's rate),
+// eight on 32,771 22 + 4.7 (67 MB: 14).
 template <int D, int NT, bool PACK>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   constexpr int W = kWaves;
@@ -855,8 +855,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 }
 
 // Joins the chunks of each (row, query head): a workgroup of four waves each,
-// wave w the chunks w, w + 4, ...  Two trips to memory: 4.5 us with its launch
-// (32 heads of 17 chunks), 5 for 256.
+// wave w the chunks w, w + 4, ...  Two trips to memory: 3.9 us with its launch
+// (32 heads of 17 chunks), 4.7 for 256 of 26.
 template <int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) {
   __shared__ float so[kJoinWaves][D], sml[kJoinWaves][2];
@@ -874,6 +874,14 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) 
   float m = kNegInf, l = 0.0f, o[D / 64];
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) o[d] = 0.0f;
+  // (the first sums are asked for with their maxima; 0 where there is none)
+  constexpr int kAhead = 8;
+  float ahead[kAhead][D / 64];
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e)
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+      ahead[e][d] = wave + kJoinWaves * e < nc ? load_g(a.part + (at + wave + kJoinWaves * e) * D + lane + 64 * d) : 0.0f;
   for (int b = wave; b < nc; b += 64 * kJoinWaves) {
     const int c = b + kJoinWaves * lane;
     const float mc = c < nc ? load_g(a.part_ml + 2 * (at + c)) : kNegInf;
@@ -891,14 +899,19 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) 
     l = __builtin_fmaf(l, al, ls);
 #pragma unroll
     for (int d = 0; d < D / 64; ++d) o[d] *= al;
-    const int cn = min(64, (nc - b + kJoinWaves - 1) / kJoinWaves);
-#pragma unroll 4
-    for (int e = 0; e < cn; ++e) {
+    auto add = [&](int e, auto value) {
       const float fe = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), e));
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d)
-        o[d] = __builtin_fmaf(load_g(a.part + (at + b + kJoinWaves * e) * D + lane + 64 * d), fe, o[d]);
+      for (int d = 0; d < D / 64; ++d) o[d] = __builtin_fmaf(value(d), fe, o[d]);
+    };
+    const int cn = min(64, (nc - b + kJoinWaves - 1) / kJoinWaves);
+    if (b == wave) {
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) add(e, [&](int d) { return ahead[e][d]; });
     }
+#pragma unroll 4
+    for (int e = b == wave ? kAhead : 0; e < cn; ++e)
+      add(e, [&](int d) { return load_g(a.part + (at + b + kJoinWaves * e) * D + lane + 64 * d); });
   }
   if (lane == 0) sml[wave][0] = m, sml[wave][1] = l;
 #pragma unroll
