@@ -620,9 +620,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
 // exponentials.  Bound by matrix and vector instructions, which add up: four
 // products (two halves each of Q and P) where 16-bit attention takes two keep
 // the matrix cores busy 53 % of the time, exponentials and conversions the
-// rest.  2 x 2,048 tokens on 4,096 positions, 32 heads: 234 us, 575 TFLOP/s of
-// the definition's products, 1,150 of those done (a library product of
-// 8,192^3 in bf16: 1,250).
+// rest.  2 x 2,048 tokens on 4,096 positions, 32 heads: 233 to 251 us on
+// different cards, up to 575 TFLOP/s of the definition's products, 1,150 of
+// those done (a library product of 8,192^3 in bf16: 1,250).
 template <int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a) {
   constexpr int KS = D / 32, DT = D / 16, NT = 2, W = kWaves, ROWS = 16 * NT * W;
