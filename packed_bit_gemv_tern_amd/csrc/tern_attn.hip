@@ -12,7 +12,7 @@
 // Matrix form, per step of 64 positions (v_mfma_f32_16x16x32_f16, fp32
 // accumulators):  S^T = K Q^T,  O^T += V^T P^T.  The codes are exact in
 // fp16.  The other operand of each product is split in two fp16 numbers, hi
-// + lo, 22 bits together: q after a power of two that brings the row's
+// + lo, 23 bits together: q after a power of two that brings the row's
 // largest element under 2^9 (so that lo stays far above fp16's smallest
 // numbers), and w_j = e^(s_j - m) * vs_j * 2^(6 - e) < 2^7 (e: exponent of the
 // largest V scale met so far).  Errors are then those of fp32.
@@ -39,6 +39,7 @@ namespace tern {
 
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -84,6 +85,10 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
 }
 
 // Eight int8 codes as fp16, exactly: 0x6400 | u is 1024 + u, u = code + 128.
+// (Codes + 128 as subnormals, and scores that start at -128 times the sum of the
+// query row, cost two instructions in five less and 1 % of the prompts' time, but
+// such scores round at the size of 128 |sum q|: with one key channel far above the
+// others and a query row of one sign that was 60 times as far off.)
 __device__ __forceinline__ f16x8 codes_f16(uint32_t w0, uint32_t w1) {
   const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
   union {
@@ -99,21 +104,6 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t w0, uint32_t w1) {
   return o.v;
 }
 
-// Eight int8 codes as (code + 128) * 2^-24: u in the low byte of an fp16 is
-// the subnormal u * 2^-24, so nothing is subtracted here (two instructions in
-// five less).  The prompt kernel's first product starts its sums at -128 times
-// the sum of the query row instead, which rounds at about twice the magnitude
-// (results 15 % further off; 2.5 % of its time).  Kernels that wait for memory
-// subtract, and the second product has to: its sums, of many values of either
-// sign, are small beside those of values + 128.
-__device__ __forceinline__ f16x8 codes_sub(uint32_t w0, uint32_t w1) {
-  w0 ^= 0x80808080u;
-  w1 ^= 0x80808080u;
-  const u32x4 o = {__builtin_amdgcn_perm(0u, w0, 0x0c010c00u), __builtin_amdgcn_perm(0u, w0, 0x0c030c02u),
-                   __builtin_amdgcn_perm(0u, w1, 0x0c010c00u), __builtin_amdgcn_perm(0u, w1, 0x0c030c02u)};
-  return __builtin_bit_cast(f16x8, o);
-}
-
 // v - hi of one half of a pair: one instruction that reads the fp16 as it is.
 template <bool HIGH>
 __device__ __forceinline__ float minus_half(float v, f16x2 h) {
@@ -124,10 +114,10 @@ __device__ __forceinline__ float minus_half(float v, f16x2 h) {
     asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(v));
   return r;
 }
-// v = hi + lo to 22 bits (hi rounded toward zero: lo has its sign).
+// v = hi + lo, each rounded to nearest: to 23 bits while lo is normal.
 __device__ __forceinline__ void split2(float a, float b, f16x2& hi, f16x2& lo) {
-  hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
-  lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(minus_half<false>(a, hi), minus_half<true>(b, hi)));
+  hi = __builtin_convertvector(f32x2{a, b}, f16x2);
+  lo = __builtin_convertvector(f32x2{minus_half<false>(a, hi), minus_half<true>(b, hi)}, f16x2);
 }
 
 // The value of the lane eight columns on (the other half of a packed tile).
@@ -188,20 +178,16 @@ __device__ __forceinline__ QueryScale query_scale(float scale, const float (&x)[
   const float up = scale < 0.0f ? -pow2i(8 - e) : pow2i(8 - e);
   return {up, fabsf(scale) * 1.44269504088896340736f * pow2i(e - 8)};
 }
-// One k step's operands, high and low; returns their sum.
-__device__ __forceinline__ float split_query(const float (&x)[8], float up, f16x8& qh, f16x8& ql) {
-  float sum = 0.0f;
+// One k step's operands, high and low.
+__device__ __forceinline__ void split_query(const float (&x)[8], float up, f16x8& qh, f16x8& ql) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f16x2 hi, lo;
     split2(x[2 * i] * up, x[2 * i + 1] * up, hi, lo);
     qh[2 * i] = hi[0], qh[2 * i + 1] = hi[1];
     ql[2 * i] = lo[0], ql[2 * i + 1] = lo[1];
-    sum += ((float)hi[0] + (float)hi[1]) + ((float)lo[0] + (float)lo[1]);
   }
-  return sum;
 }
-constexpr float kBias = -128.0f / 16777216.0f;  // times a row's sum: where its scores start (codes_sub)
 
 // The V scale of the lane's 16 positions in a step.  Weights take it with the
 // exponential: e^(s - m) vs 2^(kUp - ve) = 2^(s' - m' + lv + kUp), vs 2^-ve =
@@ -656,7 +642,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   if ((blockIdx.x >> 8) & 1) __builtin_amdgcn_s_setprio(1);
 
   f16x8 qh[NT][KS], ql[NT][KS];
-  float qfac[NT], qbias[NT];
+  float qfac[NT];
   int32_t pos[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
@@ -670,16 +656,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 #pragma unroll
     for (int j = 0; j < D / 4; ++j) x[j] = live ? x[j] : 0.0f;
     const QueryScale f = query_scale<D>(a.scale, x);
-    qfac[u] = f.factor * 16777216.0f;  // (of codes_sub)
-    float sum = 0.0f;
+    qfac[u] = f.factor;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
       float part[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) part[e] = x[8 * j + e];
-      sum += split_query(part, f.up, qh[u][j], ql[u][j]);
+      split_query(part, f.up, qh[u][j], ql[u][j]);
     }
-    qbias[u] = kBias * sum_groups(sum);
   }
 
   f32x4 o[NT][DT];
@@ -725,8 +709,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
       k_piece(e, tok, i);
       const int r = tok & 15, kn = 4 * (tok >> 4) + (r & 3);
       const int at = 16 * pg + (kn ^ swizzle(pg));
-      kf[buf][r >> 2][2 * i][at] = codes_sub(kraw[e][0], kraw[e][1]);
-      kf[buf][r >> 2][2 * i + 1][at] = codes_sub(kraw[e][2], kraw[e][3]);
+      kf[buf][r >> 2][2 * i][at] = codes_f16(kraw[e][0], kraw[e][1]);
+      kf[buf][r >> 2][2 * i + 1][at] = codes_f16(kraw[e][2], kraw[e][3]);
       const int d = (t >> 2) + 64 * e;
       const int vt = 16 * pg + ((d & 15) ^ swizzle(pg));
       vf[buf][d >> 4][0][vt] = codes_f16(vraw[e][0], vraw[e][1]);
@@ -773,7 +757,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 #pragma unroll
       for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[u][e] = {qbias[u], qbias[u], qbias[u], qbias[u]};
+        for (int e = 0; e < 4; ++e) sc[u][e] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
         if (j + 1 < KS) {

@@ -1,0 +1,54 @@
+"""Scores whose terms are far apart: key channels far larger than the others
+with queries that do not average to 0, query elements far apart, and queries
+near the largest fp32 numbers.  The error of each row against 64 bits is
+measured by the sums of |q k| position by position, through every tile."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+pytest.importorskip("torch")
+from attention_util import TILES, attend, pad_table  # noqa: E402
+from kv_util import Paged  # noqa: E402
+
+
+def pages(new, columns, n, D, seed):
+    pg = Paged(2, -(-n // 16), 1, D, 16, seed=seed, scales=lambda rng, shape: rng.uniform(0.005, 0.03, shape))
+    if columns:
+        pad_table(pg, columns)
+    return pg
+
+
+@pytest.mark.parametrize("n", [50, 300])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,group,columns", TILES)
+def test_key_channel_far_above_the_others(new, group, columns, D, n):
+    """A page's scale belongs to its largest channel: the others' codes are
+    small; queries are all positive."""
+    pg = pages(new, columns, n, D, 1)
+    k = np.where(pg.rng.random(pg.host.k.shape) < 0.3, pg.rng.choice([-1, 1], pg.host.k.shape), 0)
+    k[..., 7] = pg.rng.choice([-127, 126, 127], k.shape[:-1])
+    pg.host.k[:] = k
+    q = (3 + 0.3 * pg.rng.normal(0, 1, (2 * new, group, D))).astype(np.float32)
+    attend(pg.upload(), [new, new], [n, n - 7], q, scale=1.0)
+
+
+@pytest.mark.parametrize("new,group,columns", TILES)
+@pytest.mark.parametrize("q_size,scale", [(1e37, 1e-10), (1e-30, 1e25)])
+def test_queries_of_extreme_size(new, group, columns, q_size, scale):
+    """Queries near the ends of fp32, with scales that bring the scores back to
+    ordinary ones."""
+    pg = pages(new, columns, 100, 64, 2)
+    pg.host.k_scale *= np.float32(2e-28 if q_size > 1 else 20)
+    q = (q_size * pg.rng.normal(0, 3, (2 * new, group, 64))).astype(np.float32)
+    attend(pg.upload(), [new, new], [100, 93], q, scale=scale)
+
+
+@pytest.mark.parametrize("new,group,columns", TILES)
+def test_query_element_far_above_the_others(new, group, columns):
+    """One element of q 2^12 times the others, in a channel where the codes
+    are 0: the scores are the others'."""
+    pg = pages(new, columns, 200, 128, 3)
+    pg.host.k[..., 5] = 0
+    q = pg.rng.normal(0, 3, (2 * new, group, 128)).astype(np.float32)
+    q[..., 5] *= 4096
+    attend(pg.upload(), [new, new], [200, 150], q)
