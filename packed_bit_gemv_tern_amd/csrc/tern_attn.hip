@@ -6,16 +6,25 @@
 //
 //     s_j = scale * (q_r . k_j),  y_r = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
-// in one pass over the positions with the running maximum m and sum.  A
-// row with no position to see is 0.
+// in one pass over the positions with a running maximum (here the units of the
+// sums) and sum.  A row with no position to see is 0.
 //
 // Matrix form, per step of 64 positions (v_mfma_f32_16x16x32_f16, fp32
 // accumulators):  S^T = K Q^T,  O^T += V^T P^T.  The codes are exact in
 // fp16.  The other operand of each product is split in two fp16 numbers, hi
 // + lo, 23 bits together: q after a power of two that brings the row's
 // largest element under 2^9 (so that lo stays far above fp16's smallest
-// numbers), and w_j = e^(s_j - m) * vs_j * 2^(6 - e) < 2^7 (e: exponent of the
-// largest V scale met so far).  Errors are then those of fp32.
+// numbers), and the weights w_j = e^(s_j) vs_j 2^-R.  Errors are then those of
+// fp32.
+//
+// Small weights are what the split has to get right: a position that takes
+// nearly all of a row's softmax may hold values near 0, and pages with large V
+// scales may have hardly any of it, so the weights that make up y can be far
+// below the largest.  hi + lo is good to 23 bits of a weight from 2^-3 on and to
+// 2^-25 below that.  With the largest weight brought to 2^9 .. 2^15 that is enough
+// for a row whose largest sum ends at 2^8 or more (2^-33 of it for each
+// weight).  A workgroup with other rows takes its positions again for those, in
+// bands of 18 octaves of weight, each in units of its own (next_band).
 //
 // Layout: in S^T a lane holds one query row (lane % 16) and 4 positions per
 // 16 x 16 tile.  Row i of K tile t is position 16 * (i / 4) + 4 t + i % 4 of
@@ -189,78 +198,145 @@ __device__ __forceinline__ void split_query(const float (&x)[8], float up, f16x8
   }
 }
 
-// The V scale of the lane's 16 positions in a step.  Weights take it with the
-// exponential: e^(s - m) vs 2^(kUp - ve) = 2^(s' - m' + lv + kUp), vs 2^-ve =
-// 2^lv < 2, and sums of weights are multiplied by rl = 2^-lv.  (Far below the
-// largest scale, 0 included, lv ends at -40: those weights are 0 as fp16.)
-// kUp keeps the low halves of small weights out of fp16's smallest numbers
-// (2^-31 of the largest weight); at 14 the exponents near it, and log2 of the
-// scales with it, were rounded at twice the size, and results were up to half
-// as far off again.
-constexpr int kUp = 6;
+// The V scale of the lane's 16 positions in a step: vs = 2^(lm + e), lm in
+// [-1, 0), and 2^-lm (e = -infinity for a scale of 0).  Weights take it with
+// the exponential.
 struct VScale {
-  float lv, rl;
+  float lm, e, rm;
 };
-// `ve` is the exponent of the largest V scale met: where this step's is
-// larger, the sums so far move to its power of two.
-template <int DT, int NT>
-__device__ __forceinline__ VScale v_scale(float vs, int& ve, f32x4 (&o)[NT][DT]) {
-  const int e = __builtin_amdgcn_readfirstlane(
-      min((int)(__builtin_bit_cast(uint32_t, max_groups(vs)) >> 23) - 127, 120));
-  if (e > ve) {
-    const float f = ve - e < -126 ? 0.0f : pow2i(ve - e);
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[u][d] *= f;
-    ve = e;
-  }
-  const float lv = fmaxf(__builtin_amdgcn_logf(vs * pow2i(-ve)), -40.0f);
-  return {lv, __builtin_amdgcn_exp2f(-lv)};
+__device__ __forceinline__ VScale v_scale(float vs) {
+  const float mant = vs == 0.0f ? 1.0f : __builtin_amdgcn_frexp_mantf(vs);
+  return {__builtin_amdgcn_logf(mant), vs == 0.0f ? kNegInf : (float)__builtin_amdgcn_frexp_expf(vs),
+          __builtin_amdgcn_rcpf(mant)};
 }
-// One row's 16 scores of a step (times f: in units of log2): the running
-// maximum m, which l and o follow.  Where `masked`, only positions up to
-// `last` of the lane's 16 count.
+
+// What a row has summed: o holds sums of code * e^s vs in units of 2^R, l the
+// sum of e^s in units of 2^L; R and L are whole numbers, so changing units
+// is exact.  R grows where a weight would pass 2^15 (fp16 ends at 2^16), L where
+// an e^s would pass 2^24.
+constexpr float kNoUnit = -3.0e38f;  // nothing summed yet (finite: differences with -infinity stay that)
+constexpr float kTop = 15.0f;
+constexpr float kReset = 10.0f;  // a new R brings the step's largest weight to 2^9 .. 2^10
+struct RowUnits {
+  float R, L;
+};
+__device__ __forceinline__ float pow2_of(float e) {  // 2^e of a whole number, 0 below 2^-126
+  return e < -126.0f ? 0.0f : pow2i((int)fminf(e, 120.0f));
+}
 template <int DT>
-__device__ __forceinline__ void row_maximum(f32x4 (&sc)[4], float& f, bool masked, int last, float& m, float& l,
-                                            f32x4 (&o)[DT]) {
-  if (masked) {
+__device__ __forceinline__ void change_unit(float to, RowUnits& r, f32x4 (&o)[DT]) {
+  const float al = pow2_of(r.R - to);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
-    f = 1.0f;
-  }
+  for (int d = 0; d < DT; ++d) o[d] *= al;
+  r.R = to;
+}
+
+// One row's 16 scores of a step times f (units of log2), of which only the
+// positions up to `last` of the lane's 16 count.
+__device__ __forceinline__ void mask_scores(f32x4 (&sc)[4], float& f, int last) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
+  f = 1.0f;
+}
+// Brings the row's units to the step.  Returns the exponent that the lane's weights
+// take from the V scale (v.e; -infinity where their e^s had to be summed here).
+template <int DT>
+__device__ __forceinline__ float row_units(const f32x4 (&sc)[4], float f, const VScale& v, RowUnits& r, float& l,
+                                           f32x4 (&o)[DT]) {
   float mx = sc[0][0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
-  mx = max_groups(mx * f);
-  if (__any(mx > m)) {
-    const float mn = fmaxf(m, mx);
-    const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-    m = mn;
-    l *= al;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[d] *= al;
+  mx *= f;
+  const float tl = mx + (v.lm + v.e);  // the lane's largest weight
+  const float t = max_groups(tl);
+  float e = v.e;
+  if (__any(t > r.R + kTop || mx > r.L + 24.0f)) {
+    const float ms = __builtin_ceilf(max_groups(mx));
+    if (ms > r.L + 24.0f) {
+      l *= pow2_of(r.L - ms);
+      r.L = ms;
+    }
+    change_unit(t > r.R + kTop ? __builtin_ceilf(t) - kReset : r.R, r, o);
   }
+  // A lane whose weights vanish beside the row's (a V scale of 0, or 2^-90 of
+  // the others'): its e^s count all the same.
+  const bool own = tl < r.R - 90.0f;
+  if (__any(own && mx > kNegInf)) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 2][i & 3], f, -r.L));
+    l += own ? sum : 0.0f;
+    e = own ? kNegInf : e;
+  }
+  return e;
 }
-// and their weights, as operands of the second product (high and low).
-__device__ __forceinline__ void row_weights(const f32x4 (&sc)[4], float f, const VScale& v, float m, float& l,
-                                            f16x8 (&hi)[2], f16x8 (&lo)[2]) {
-  const float off = v.lv + ((float)kUp - (m == kNegInf ? 0.0f : m));
+// and their weights, as operands of the second product (high and low); returns
+// the sum of their e^s in units of 2^L.
+__device__ __forceinline__ float row_weights(const f32x4 (&sc)[4], float f, const VScale& v, float e, const RowUnits& r,
+                                             f16x8 (&hi)[2], f16x8 (&lo)[2]) {
+  const float d = e - r.R, off = v.lm + d;
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = 8 * k + 2 * i;
-      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e >> 2][e & 3], f, off));
-      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e >> 2][(e & 3) + 1], f, off));
+      const int x = 8 * k + 2 * i;
+      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 2][x & 3], f, off));
+      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 2][(x & 3) + 1], f, off));
       sum += p0 + p1;
       f16x2 h, r;
       split2(p0, p1, h, r);
       hi[k][2 * i] = h[0], hi[k][2 * i + 1] = h[1];
       lo[k][2 * i] = r[0], lo[k][2 * i + 1] = r[1];
     }
-  l = __builtin_fmaf(sum, v.rl, l);
+  return __builtin_ldexpf(sum * v.rm, (int)(-d - r.L));
+}
+
+// The weights that a band takes, e^s vs from 2^from up to 2^to (-infinity, and
+// below: none), and a row's next one: after the first pass of all weights, from
+// the border of fp16's full precision up, then 18 octaves at a time, with
+// smaller units, until the sums have passed 2^8 (or 60 octaves are done): the
+// rest at once.  Returns whether the row takes part.
+struct Band {
+  float from, to;
+};
+constexpr float kInf = __builtin_inff();
+constexpr float kFull = -3.0f, kBand = 18.0f, kSettled = 256.0f;
+static_assert(kFull + kBand == kTop, "a band's weights are those that fit its units");
+template <int DT, bool PACK>
+__device__ bool next_band(int pass, bool live, RowUnits& r, f32x4 (&o)[DT], Band& b) {
+  float big = 0.0f;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(o[d][i]));
+  big = max_groups(big);
+  if constexpr (PACK) big = fmaxf(big, other_half(big));
+  const bool settled = !(big < kSettled);
+  Band n = {kInf, kNegInf};
+  if (pass == 0) {
+    if (live && !settled && r.R > kNoUnit) {
+      n = {r.R + kFull, kInf};
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  } else if (fabsf(b.from) < kInf) {
+    n = {kNegInf, b.from};
+    if (!settled && pass < 4) {
+      change_unit(r.R - kBand, r, o);
+      n.from = r.R + kFull;
+    }
+  }
+  b = n;
+  return n.from < kInf;
+}
+__device__ __forceinline__ void band_scores(f32x4 (&sc)[4], float& f, const VScale& v, const Band& b) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float s = sc[i >> 2][i & 3] * f, t = s + (v.lm + v.e);
+    sc[i >> 2][i & 3] = t >= b.from && t < b.to ? s : kNegInf;
+  }
+  f = 1.0f;
 }
 
 // see attn_prompt_kernel
@@ -295,7 +371,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   __shared__ float sml[W][16 * NT][2];
   __shared__ float qfac[16 * NT];  // a row's |scale| * log2(e) * powers of two
   __shared__ int32_t page[kGroups];  // of a group of 16 positions (-1: none there)
-  __shared__ float kscale[kGroups], vscale[kGroups];
+  __shared__ float kscale[kGroups];
+  __shared__ VScale vscale[kGroups];
+  __shared__ Band band[W][16 * NT];
+  __shared__ int again;  // some row needs another pass
 
   const KvArgs& kv = a.kv;
   uint32_t h, cu, tile;
@@ -315,7 +394,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   // (chunk 0 always writes: it is the one that the joining pass counts on)
   if (c0 >= c1 && c > 0) return;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int nr = PACK ? n & 7 : n;  // the lane's row of a tile
   const bool low = PACK && n >= 8;  // the lane holds low operands
@@ -367,15 +446,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   }
 
   f32x4 o[NT][DT];
-  float m[NT], l[NT];
+  float l[NT];
+  RowUnits units[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    m[u] = kNegInf;
+    units[u] = {kNoUnit, kNoUnit};
     l[u] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[u][d] = {0.0f, 0.0f, 0.0f, 0.0f};
   }
-  int ve = -100;  // o holds sums of code * weight * vs * 2^(kUp - ve), l of weight * 2^kUp
 
   // position of the tile that every row sees: below it no mask is needed
   const int64_t all_see = min(sv.len, sv.pos0 + (int)a.by_g.div(row_lo) + 1);
@@ -410,6 +489,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
     const int64_t si = (int64_t)max(id, 0) * kv.H + h;
     const float ks = load_g(kv.k_scale + si), vs = load_g(kv.v_scale + si);
     page[threadIdx.x] = id;
+    if (threadIdx.x == 0) again = 0;
     __syncthreads();
     steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
     if (wave < steps) {
@@ -419,7 +499,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
     meanwhile();
     // (this waits for K and V too: loads return in order, and not every wave has some)
     kscale[threadIdx.x] = id < 0 ? 0.0f : ks;
-    vscale[threadIdx.x] = id < 0 ? 0.0f : vs;
+    vscale[threadIdx.x] = v_scale(id < 0 ? 0.0f : vs);
   };
   open_window([&]() {
     if (prepares) prepare_q();
@@ -428,6 +508,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   float fac[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) fac[u] = qfac[16 * u + n];
+  int pass = 0;  // over the positions (see next_band)
   for (;;) {
     f32x4 sc[NT][4];
     auto scores = [&]() {
@@ -469,16 +550,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
       const int64_t j0 = w0 + kStep * st;
       const int32_t jv = (int32_t)j0 + 16 * g;
       const bool here = page[4 * st + g] >= 0;
-      const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
-      const VScale v = v_scale<DT>(vs, ve, o);
+      const float ks = kscale[4 * st + g];
+      const VScale v = vscale[4 * st + g];
       const bool masked = j0 + kStep > all_see || __any(!here);
       f16x8 pb[NT][2][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float f = fac[u] * ks;
-        row_maximum<DT>(sc[u], f, masked, here ? pos[u] - jv : -1, m[u], l[u], o[u]);
+        if (masked) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
         f16x8 hi[2], lo[2];
-        row_weights(sc[u], f, v, m[u], l[u], hi, lo);
+        if (pass == 0) {
+          const float e = row_units(sc[u], f, v, units[u], l[u], o[u]);
+          l[u] += row_weights(sc[u], f, v, e, units[u], hi, lo);
+        } else {
+          band_scores(sc[u], f, v, band[wave][16 * u + n]);
+          row_weights(sc[u], f, v, v.e, units[u], hi, lo);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if constexpr (PACK) {
@@ -527,7 +614,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
       weigh_and_sum(st);
     }
     w0 += kWindow;
-    if (w0 >= c1) break;
+    if (w0 >= c1) {
+      bool more = false;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) more |= next_band<DT, PACK>(pass, pos[u] >= 0, units[u], o[u], band[wave][16 * u + n]);
+      if (more) again = 1;
+      __syncthreads();
+      if (!again) break;
+      ++pass;
+      w0 = c0;
+    }
     entry = page_entry(kv, s, (w0 + 16 * (int)threadIdx.x) >> kv.log_p);
     __syncthreads();  // (the window before has been read)
     open_window([]() {});
@@ -535,21 +631,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   }
 
   // join the waves, a tile at a time
-  const float back = pow2i(max(ve - kUp, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]) * pow2i(-kUp);
-    if (g == 0) sml[wave][16 * u + n][0] = m[u], sml[wave][16 * u + n][1] = lt;
+    const float lt = sum_groups(l[u]);
+    if (g == 0) sml[wave][16 * u + n][0] = lt == 0.0f ? kNegInf : units[u].L, sml[wave][16 * u + n][1] = lt;
   }
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    __syncthreads();  // (the operands, or the tile before, have been read)
+    if (u) __syncthreads();  // (the tile before has been read)
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      f32x4 v = o[u][d] * back;
-      if constexpr (PACK) {
+      f32x4 v = o[u][d];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += other_half(v[i]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (PACK) v[i] += other_half(v[i]);
+        v[i] = __builtin_ldexpf(v[i], (int)(units[u].R - units[u].L));
       }
       *reinterpret_cast<f32x4*>(&sh.o[wave][n][16 * d + 4 * g]) = v;
     }
@@ -617,7 +713,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   __shared__ f16x8 kf[2][4][KS][64];
   __shared__ f16x8 vf[2][DT][2][64];
   __shared__ int32_t page[kGroups];
-  __shared__ float kscale[kGroups], vscale[kGroups];
+  __shared__ float kscale[kGroups];
+  __shared__ VScale vscale[kGroups];
+  __shared__ Band band[ROWS];
+  __shared__ int again;  // some row needs another pass
 
   const KvArgs& kv = a.kv;
   uint32_t h, cu, tile;
@@ -633,7 +732,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   const int64_t c1 = c == a.nchunk - 1 ? end : min(end, c0 + a.chunk);
   if (c0 >= c1 && c > 0) return;
 
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int slot = 16 * g + (n ^ swizzle(g));
 
@@ -667,15 +766,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   }
 
   f32x4 o[NT][DT];
-  float m[NT], l[NT];
+  float l[NT];
+  RowUnits units[NT];
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    m[u] = kNegInf;
+    units[u] = {kNoUnit, kNoUnit};
     l[u] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[u][d] = {0.0f, 0.0f, 0.0f, 0.0f};
   }
-  int ve = -100;
   const int64_t all_see = min(sv.len, sv.pos0 + (int)a.by_g.div(row_lo + 16 * NT * wave) + 1);
   const int P = 1 << kv.log_p;
 
@@ -718,7 +817,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
     }
   };
 
-  for (; w0 < c1; w0 += kWindow) {
+  int pass = 0;  // over the positions (see next_band)
+  while (w0 < c1) {
     {
       const int64_t j = w0 + 16 * t;
       const int32_t id = j < sv.len ? page_of(kv, s, j >> kv.log_p) : -1;
@@ -726,8 +826,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
       const float ks = load_g(kv.k_scale + si), vs = load_g(kv.v_scale + si);
       __syncthreads();  // (the window before has been read)
       page[t] = id;
+      if (t == 0) again = 0;
       kscale[t] = id < 0 ? 0.0f : ks;
-      vscale[t] = id < 0 ? 0.0f : vs;
+      vscale[t] = v_scale(id < 0 ? 0.0f : vs);
       __syncthreads();
     }
     const int steps = (int)((min(c1 - w0, (int64_t)kWindow) + kStep - 1) / kStep);
@@ -742,12 +843,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
       const int64_t j0 = w0 + kStep * st;
       const int32_t jv = (int32_t)j0 + 16 * g;
       const bool here = page[4 * st + g] >= 0;
-      const float ks = kscale[4 * st + g], vs = vscale[4 * st + g];
-      const VScale v = v_scale<DT>(vs, ve, o);
+      const float ks = kscale[4 * st + g];
+      const VScale v = vscale[4 * st + g];
       const bool masked = j0 + kStep > all_see || __any(!here);
       f32x4 sc[NT][4];
       f16x8 hi[NT][2], lo[NT][2];
-      float f[NT];
       // Both products: the next four operands are read while the matrix
       // instructions of these four run (sixteen; the high halves first, so
       // that none waits for the one before it).
@@ -781,9 +881,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
       load_codes(min(st + 2, steps - 1));
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        f[u] = qfac[u] * ks;
-        row_maximum<DT>(sc[u], f[u], masked, here ? pos[u] - jv : -1, m[u], l[u], o[u]);
-        row_weights(sc[u], f[u], v, m[u], l[u], hi[u], lo[u]);
+        float f = qfac[u] * ks;
+        if (masked) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
+        if (pass == 0) {
+          const float e = row_units(sc[u], f, v, units[u], l[u], o[u]);
+          l[u] += row_weights(sc[u], f, v, e, units[u], hi[u], lo[u]);
+        } else {
+          band_scores(sc[u], f, v, band[16 * (NT * wave + u) + n]);
+          row_weights(sc[u], f, v, v.e, units[u], hi[u], lo[u]);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) fr[0][e] = vf[buf][e][0][slot];
@@ -808,31 +914,45 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    w0 += kWindow;
+    if (w0 >= c1) {
+      bool more = false;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) more |= next_band<DT, false>(pass, pos[u] >= 0, units[u], o[u], band[16 * (NT * wave + u) + n]);
+      if (more) again = 1;
+      __syncthreads();
+      if (!again) break;
+      ++pass;
+      w0 = c0;
+    }
   }
 
-  const float back = pow2i(max(ve - kUp, -126));
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]) * pow2i(-kUp);
+    const float lt = sum_groups(l[u]);
     const int r = row_lo + 16 * (NT * wave + u) + n;
     if (r >= rows) continue;
     uint32_t rem;
     const int64_t row = sv.row0 + a.by_g.divmod(r, rem), hq = h * G + rem;
     const int64_t at = (row * a.Hq + hq) * a.nchunk + c;
     const bool whole = a.nchunk == 1;
-    const float f = whole ? (lt == 0.0f ? 0.0f : back / lt) : back;
+    const float f = whole ? (lt == 0.0f ? 0.0f : 1.0f / lt) : 1.0f;
+    const int back = (int)(units[u].R - units[u].L);
     float* out = whole ? a.y + row * a.ldy + hq * D : a.part + at * D;
     if (!whole && g == 0) {
-      store_g(a.part_ml + 2 * at, m[u]);
+      store_g(a.part_ml + 2 * at, lt == 0.0f ? kNegInf : units[u].L);
       store_g(a.part_ml + 2 * at + 1, lt);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
+      f32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_ldexpf(o[u][d][i] * f, back);
       if (a.y16 || !whole) {
-        store_g(reinterpret_cast<f32x4*>(out + 16 * d + 4 * g), o[u][d] * f);
+        store_g(reinterpret_cast<f32x4*>(out + 16 * d + 4 * g), v);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_g(out + 16 * d + 4 * g + i, o[u][d][i] * f);
+        for (int i = 0; i < 4; ++i) store_g(out + 16 * d + 4 * g + i, v[i]);
       }
     }
   }

@@ -12,7 +12,11 @@ Per row, head and dim d, with weights w_j = e^(a_j - max a), W their sum, A_j =
   - the exponential, the two fp16 numbers, the V scale's logarithm and reciprocal
     and the product with it: 2^-23 each, 6 of them;
   - sums of weights and of weighted values: one rounding per 16 positions and
-    lane and per joining step, at most (n / 64 + 32) * 4 roundings of 2^-24.
+    lane and per joining step, at most (n / 64 + 32) * 4 roundings of 2^-24;
+  - a weight far below a row's largest is off by up to 2^-25 in units in which the
+    row's largest sum is 2^8 or more, that is by 2^-33 of sum_j w_j max_d |v_jd|, with a
+    standard deviation of 2^-25.8; many of them add as independent errors (six
+    deviations are allowed), and weights 2^-60 of the largest may be missing.
 Numerator and denominator carry these."""
 import numpy as np
 import torch
@@ -48,10 +52,14 @@ def reference(pg, q, scale):
                 delta = A * 26 * 2 ** -24 + np.log(2) * 2 ** -24 * (5 * S + 3 * Z + 36) + 6 * 2 ** -23
                 c = (m / 64 + 32) * 4 * 2 ** -24
                 size, num = w @ np.abs(vv) / W, w @ vv / W
+                wz = w * z
+                codes = np.abs(vv) / np.where(z > 0, z, 1)[:, None]
                 rows = slice(h * G, (h + 1) * G)
+                floor = (6 * 2 ** -33.8 * np.sqrt((codes ** 2).sum(0)) * (w @ np.abs(vv).max(1))[:, None]
+                         + 2 ** -60 * wz.max(1, keepdims=True) * codes.sum(0)) / W
                 y[r0 + i, rows] = num
                 tol[r0 + i, rows] = ((w * delta) @ np.abs(vv) / W + np.abs(num) * ((w * delta).sum(1, keepdims=True) / W)
-                                     + c * (size + np.abs(num)))
+                                     + c * (size + np.abs(num)) + floor)
     return y, tol
 
 
