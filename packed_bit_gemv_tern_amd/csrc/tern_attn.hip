@@ -231,32 +231,58 @@ __device__ __forceinline__ void change_unit(float to, RowUnits& r, f32x4 (&o)[DT
   r.R = to;
 }
 
-// One row's 16 scores of a step times f (units of log2), of which only the
-// positions up to `last` of the lane's 16 count.
-__device__ __forceinline__ void mask_scores(f32x4 (&sc)[4], float& f, int last) {
+// Scores beyond 2^20, of which fp32 holds too few digits for units: the row's are
+// counted from a base, the largest when that was met (Far: what a wave keeps of it).
+constexpr float kFar = 1048576.0f;
+struct Far {
+  float* base;  // of the wave's rows, in LDS
+  bool any;     // some row has one
+};
+// One row's 16 scores of a step times f (units of log2), less their base, of which
+// only the positions up to `last` of the lane's 16 count.
+__device__ __forceinline__ void mask_scores(f32x4 (&sc)[4], float& f, int last, float base) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
+  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f - base : kNegInf;
   f = 1.0f;
+}
+__device__ __forceinline__ float largest_score(const f32x4 (&sc)[4], float f) {
+  float mx = sc[0][0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
+  return mx * f;
 }
 // Brings the row's units to the step.  Returns the exponent that the lane's weights
 // take from the V scale (v.e; -infinity where their e^s had to be summed here).
 template <int DT>
-__device__ __forceinline__ float row_units(const f32x4 (&sc)[4], float f, const VScale& v, RowUnits& r, float& l,
-                                           f32x4 (&o)[DT]) {
-  float mx = sc[0][0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
-  mx *= f;
-  const float tl = mx + (v.lm + v.e);  // the lane's largest weight
-  const float t = max_groups(tl);
+__device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScale& v, RowUnits& r, float& l,
+                                           f32x4 (&o)[DT], Far& far, int row) {
+  float mx = largest_score(sc, f);
+  float tl = mx + (v.lm + v.e);  // the lane's largest weight
+  float t = max_groups(tl);
   float e = v.e;
-  if (__any(t > r.R + kTop || mx > r.L + 24.0f)) {
-    const float ms = __builtin_ceilf(max_groups(mx));
-    if (ms > r.L + 24.0f) {
+  if (__any(t - r.R > kTop || mx - r.L > 24.0f)) {
+    float ms = __builtin_ceilf(max_groups(mx));
+    const bool beyond = ms - r.L > 24.0f && fabsf(ms) > kFar;
+    if (__any(beyond)) {  // (what the row has summed vanishes beside e^ms)
+      far.any = true;
+      if (beyond) {
+        far.base[row] += ms;  // (the row's lanes alike)
+        r = {kNoUnit, kNoUnit};
+        l = 0.0f;
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= beyond ? 0.0f : 1.0f;
+      mask_scores(sc, f, 15, beyond ? ms : 0.0f);
+      mx = largest_score(sc, f);
+      tl = mx + (v.lm + v.e);
+      t = max_groups(tl);
+      ms = __builtin_ceilf(max_groups(mx));
+    }
+    if (ms - r.L > 24.0f) {
       l *= pow2_of(r.L - ms);
       r.L = ms;
     }
-    change_unit(t > r.R + kTop ? __builtin_ceilf(t) - kReset : r.R, r, o);
+    change_unit(t - r.R > kTop ? __builtin_ceilf(t) - kReset : r.R, r, o);
   }
   // A lane whose weights vanish beside the row's (a V scale of 0, or 2^-90 of
   // the others'): its e^s count all the same.
@@ -374,6 +400,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   __shared__ float kscale[kGroups];
   __shared__ VScale vscale[kGroups];
   __shared__ Band band[W][16 * NT];
+  __shared__ float base[W][16 * NT];
   __shared__ int again;  // some row needs another pass
 
   const KvArgs& kv = a.kv;
@@ -448,6 +475,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   f32x4 o[NT][DT];
   float l[NT];
   RowUnits units[NT];
+  Far far = {base[wave], false};
+  if ((int)threadIdx.x < W * 16 * NT) base[0][threadIdx.x] = 0.0f;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     units[u] = {kNoUnit, kNoUnit};
@@ -557,10 +586,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float f = fac[u] * ks;
-        if (masked) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
+        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1, far.any ? far.base[16 * u + n] : 0.0f);
         f16x8 hi[2], lo[2];
         if (pass == 0) {
-          const float e = row_units(sc[u], f, v, units[u], l[u], o[u]);
+          const float e = row_units(sc[u], f, v, units[u], l[u], o[u], far, 16 * u + n);
           l[u] += row_weights(sc[u], f, v, e, units[u], hi, lo);
         } else {
           band_scores(sc[u], f, v, band[wave][16 * u + n]);
@@ -634,7 +663,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     const float lt = sum_groups(l[u]);
-    if (g == 0) sml[wave][16 * u + n][0] = lt == 0.0f ? kNegInf : units[u].L, sml[wave][16 * u + n][1] = lt;
+    if (g == 0) sml[wave][16 * u + n][0] = lt == 0.0f ? kNegInf : units[u].L + (far.any ? far.base[16 * u + n] : 0.0f), sml[wave][16 * u + n][1] = lt;
   }
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
@@ -716,6 +745,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   __shared__ float kscale[kGroups];
   __shared__ VScale vscale[kGroups];
   __shared__ Band band[ROWS];
+  __shared__ float base[ROWS];
   __shared__ int again;  // some row needs another pass
 
   const KvArgs& kv = a.kv;
@@ -768,6 +798,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
   f32x4 o[NT][DT];
   float l[NT];
   RowUnits units[NT];
+  Far far = {base + 16 * NT * wave, false};
+  if (t < ROWS) base[t] = 0.0f;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
     units[u] = {kNoUnit, kNoUnit};
@@ -882,9 +914,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float f = qfac[u] * ks;
-        if (masked) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
+        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1, far.any ? far.base[16 * u + n] : 0.0f);
         if (pass == 0) {
-          const float e = row_units(sc[u], f, v, units[u], l[u], o[u]);
+          const float e = row_units(sc[u], f, v, units[u], l[u], o[u], far, 16 * u + n);
           l[u] += row_weights(sc[u], f, v, e, units[u], hi[u], lo[u]);
         } else {
           band_scores(sc[u], f, v, band[16 * (NT * wave + u) + n]);
@@ -940,7 +972,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
     const int back = (int)(units[u].R - units[u].L);
     float* out = whole ? a.y + row * a.ldy + hq * D : a.part + at * D;
     if (!whole && g == 0) {
-      store_g(a.part_ml + 2 * at, lt == 0.0f ? kNegInf : units[u].L);
+      store_g(a.part_ml + 2 * at, lt == 0.0f ? kNegInf : units[u].L + (far.any ? far.base[16 * u + n] : 0.0f));
       store_g(a.part_ml + 2 * at + 1, lt);
     }
 #pragma unroll

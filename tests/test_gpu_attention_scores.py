@@ -52,3 +52,39 @@ def test_query_element_far_above_the_others(new, group, columns):
     q = pg.rng.normal(0, 3, (2 * new, group, 128)).astype(np.float32)
     q[..., 5] *= 4096
     attend(pg.upload(), [new, new], [200, 150], q)
+
+
+@pytest.mark.parametrize("new,group,columns", TILES)
+@pytest.mark.parametrize("size", [1e4, 1e7, 1e8, 1e10, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_finite_size(new, group, columns, size, sign):
+    """One key, held at several positions of pages with different V scales,
+    scores above all others by a hundredth of scores of `size`, which are all
+    positive or all negative; every third row has ordinary queries.  The rows of
+    such scores are the mean of its values: each weight is off by 2^-20 at most
+    (equal scores, the exponential, the split), sums by the roundings of
+    attention_util.  Scores s / ln 2 below 2^20 share their exponent's digits with the V
+    scale's logarithm: its rounding is ln 2 * 2^-24 * 5 |s| at most, as there."""
+    n = 900
+    pg = pages(new, columns, n, 64, 4)
+    way = pg.rng.choice(np.array([-1.0, 1.0]), 64)
+    pg.host.k[:] = (sign * 60 * way + pg.rng.integers(-3, 4, pg.host.k.shape)).astype(np.int8)
+    pg.host.k_scale[:] = np.float32(1 / 127)
+    top = [5, 16, 70, 71, 300, 640, 820]
+    for s in range(2):
+        for j in top:
+            pg.host.k[pg.table[s, j // 16], 0, j % 16] = (sign * 60 + 6) * way
+    length = [n, n - 70]
+    q = np.empty((2 * new, group, 64), np.float32)
+    q[:] = size * way / 30
+    ordinary = np.arange(2 * new) % 3 == 2
+    q[ordinary] = pg.rng.normal(0, 1, q[ordinary].shape)
+    got = attend(pg.upload(), [new, new], length, q, scale=1.0)
+    for r in np.flatnonzero(~ordinary):
+        s = r // new
+        v = np.array([pg.host.v[pg.table[s, j // 16], 0, :, j % 16] * float(pg.host.v_scale[pg.table[s, j // 16], 0])
+                      for j in top if j < length[s] - new + 1 + r % new])
+        S = np.abs(q[r, 0] * 66 / 127).sum() / np.log(2)
+        exponent = np.log(2) * 2 ** -24 * 5 * S if S < 2 ** 20 else 0
+        tol = (2 ** -19 + exponent + (n / 64 + 32) * 8 * 2 ** -24) * np.abs(v).mean(0)
+        assert (np.abs(got[r] - v.mean(0)) <= tol).all(), r
