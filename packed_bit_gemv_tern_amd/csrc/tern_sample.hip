@@ -27,9 +27,14 @@
 //      holds in the bins above;
 //   4. one workgroup per row orders the listed tokens, fixes the cut exactly,
 //      finds the chunk that the random number falls in, and walks that chunk.
-// A row whose cut bins hold more than kListMax tokens (many equal logits) is
-// cut by the bits of its keys instead, by that one workgroup (slow_cut; some
-// 0.5 ms).
+// A row whose cut bins hold more than kListMax tokens is cut by the bits of its
+// keys instead, by that one workgroup in up to ten passes over the row
+// (slow_cut).  Many equal logits do that, and so do many close ones: a bin is
+// 0.0325 T wide, so 151,936 normal logits of deviation 1.5 at T = 2 put 2,300 in
+// the bin where top-p 0.9 ends, and where top-k splits a bin top-p may end in
+// several.  Rows of 151,936 like that take 0.6 to 1.0 ms alone and 0.3 to 0.6 in
+// batches of 8 and 96 (1,024 threads a row against 256), rows of equal logits
+// 0.7 to 1.5.
 //
 // Times of the launches for 151,936 tokens: one row with top-k and top-p 2.9 +
 // 8.2 + 5.6 + 7.9 us, each a launch and one or two trips to memory, bins and
@@ -698,7 +703,7 @@ __device__ KeyBorder key_border(const Launch& L, const Row& r, KeyBorder in, uin
   return out;
 }
 
-// Cuts a row of too many equal logits, and redoes its chunks' sums.
+// Cuts a row of too many equal or close logits, and redoes its chunks' sums.
 template <int T>
 __device__ Keep slow_cut(const Launch& L, const RowWs& w, const Row& r, FinishLds<T>& F) {
   KeyBorder cut = {1u, 0xffffffffu};
