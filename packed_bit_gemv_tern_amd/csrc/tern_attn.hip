@@ -376,8 +376,10 @@ __device__ __forceinline__ int swizzle(int g) { return (0x84C0 >> (4 * g)) & 15;
 // HBM bound for many sequences: 48 contexts to 8,192 (363 MB of codes) in 72
 // us, 5.0 TB/s.  Short of that a chain bounds it: two trips to memory (the
 // sequence and page ids; q, scales, K and V), 1.8 us per step of a wave, the
-// join: one token on 4,099 positions 7.4 + 3.9 us (8.4 MB: 1.7 at HBM's rate),
-// eight on 32,771 22 + 4.7 (67 MB: 14).
+// join: one token on 4,099 positions 7.6 + 3.8 us (8.4 MB: 1.7 at HBM's rate),
+// eight on 32,771 23.9 + 4.6 (67 MB: 14).  Rows that take another pass (next_band)
+// cost it: one zero-valued position that takes the weight three more, 21.8 us
+// for one token, 72 for the eight.
 template <int D, int NT, bool PACK>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   constexpr int W = kWaves;
@@ -731,9 +733,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
 // exponentials.  Bound by matrix and vector instructions, which add up: four
 // products (two halves each of Q and P) where 16-bit attention takes two keep
 // the matrix cores busy 53 % of the time, exponentials and conversions the
-// rest.  2 x 2,048 tokens on 4,096 positions, 32 heads: 233 to 251 us on
-// different cards, up to 575 TFLOP/s of the definition's products, 1,150 of
-// those done (a library product of 8,192^3 in bf16: 1,250).
+// rest.  2 x 2,048 tokens on 4,096 positions, 32 heads: 237 to 257 us on
+// different cards, up to 570 TFLOP/s of the definition's products, 1,140 of
+// those done (a library product of 8,192^3 in bf16: 1,250); 900 us where a
+// position of value 0 takes the weight of every row (next_band).
 template <int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a) {
   constexpr int KS = D / 32, DT = D / 16, NT = 2, W = kWaves, ROWS = 16 * NT * W;
@@ -1070,15 +1073,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a) 
 int attn_rows(AttnKind k) { return k == ATTN_PACKED ? 8 : k == ATTN_16 ? 16 : k == ATTN_32 ? 32 : 128; }
 
 // Which kernel, by a sequence's rows per KV head.  Up to 32 the smallest tile
-// that holds them (32 ragged contexts to 4,096, 8 KV heads: 8 rows 46.7 us
-// packed, 47.3 by 16; 16 rows 52 by 16, 60 by 32, 77 by two of 8; 32 rows 67 by
-// 32, 82 by two of 16; eight of 2,048, 24 rows: 17.9 by 32, 18.2 by 16).  Beyond
-// 128 the prompt kernel pays once it has its two workgroups on every CU (8 x
-// 1,024 tokens from nothing: 183 us, 248 by 32; 4 x 512 on 4,096 194 and 197),
+// that holds them (32 ragged contexts to 4,096, 8 KV heads: 8 rows 38.1 us
+// packed, 38.7 by 16; 16 rows 39.6 by 16, 48.3 by 32, 45.4 by two of 8; 32 rows
+// 50.1 by 32, 57.7 by two of 16; eight of 2,048, 24 rows: 18.3 by 32, 19.1 by 16).
+// Beyond 128 the prompt kernel pays once it has its two workgroups on every CU
+// (8 x 1,024 tokens from nothing: 176 us, 263 by 32; 4 x 512 on 4,096 226 and 266),
 // the contexts are so long that they can be split for that (1,024 on 32,768:
-// 864, 1,028), or they are so short that starting counts (8 x 128: 16, 23).
-// Else tiles of 32 spread better (512 on 4,096: 75, 93; 4 x 256 on 4,096: 148,
-// 168; up to 128 rows always: 8 x 32 on 2,048 28, 42).
+// 889, 1,015), or they are so short that starting counts (8 x 128: 17.5, 24.5).
+// Else tiles of 32 spread better (512 on 4,096: 76, 96; 4 x 256 on 4,096: 144,
+// 149; up to 128 rows always: 8 x 32 on 2,048 30, 47).
 AttnKind attn_kind(int64_t rows, int64_t groups, int64_t len, int cus) {
   if (rows <= 32) return rows <= 8 ? ATTN_PACKED : rows <= 16 ? ATTN_16 : ATTN_32;
   const int64_t units = mul_sat(groups, (rows + 127) / 128);
@@ -1110,24 +1113,25 @@ AttnPlan attn_plan(const KvArgs& kv, int64_t Hq, int cus) {
   // Pieces of a context.  Together one workgroup per CU: a second round of
   // workgroups, each two trips to memory before its first product, costs more
   // than it evens out (32 ragged contexts to 4,096: whole 36 us, halves 41,
-  // quarters 44; 16 to 2,048 in 1, 2, 4, 8 pieces: 19.1, 17.2, 17.4, 20.5), and
+  // quarters 45; 16 to 2,048 in 1, 2, 4, 8 pieces: 18.7, 17.5, 17.6, 20.2), and
   // more than 64 pieces cost more to join (one KV head, 32,768 positions: 64
-  // pieces 17.7 us, 128 19.8).  Two per CU where products count: prompts (1,024
-  // rows on 32,768: 246 us, 344 with one), 32 rows on long contexts (256 rows on
-  // 32,768: 84, 97), if that is at most 32 pieces (32 rows: 28 in 32, 40 in 64).
+  // pieces 15.2 us, 128 17.4).  Two per CU where products count: prompts (1,024
+  // rows on 32,768: 242 to 265 us, 303 with one), 32 rows and more on long contexts
+  // (256 rows on 32,768: 79 in 32 pieces, 157 in 8), if that is at most 32 pieces
+  // (32 rows: 25.5 in 32, 28.1 in 64).
   const bool two = p.kind == ATTN_PROMPT || (p.kind == ATTN_32 && len > 4096);
   int64_t want = cus / units;
   if (two && 2 * cus / units <= 32) want = 2 * cus / units;
-  // Short ones whole, without the joining launch (512 positions: 9.3 us whole, 11.0
-  // in two; 1,024 with a workgroup on half of the CUs 12.9, 14.0).
+  // Short ones whole, without the joining launch (512 positions: 9.4 us whole, 11.8
+  // in two; 1,024 with a workgroup on half of the CUs 12.9, 15.6).
   if (len <= 512 || (len <= 1024 && units >= cus / 2) || (len <= 4096 && units >= cus)) want = 1;
   want = std::min<int64_t>(std::max<int64_t>(want, 1), 64);
   int64_t chunk = (len + want - 1) / want;
   // A batch of long contexts of single tokens is taken to be ragged, and cut finer
-  // to even it out (lengths up to 8,192 over 48 sequences: 80 us, 103 whole; to
-  // 16,384 over 32: 119, 132; where all are as long as the longest that costs:
-  // 154, 148 and 192, 180).  With more rows the pieces' starts cost more than
-  // that (8 x 64 rows on 8,192 each: 55 us in 4, 69 in 7).
+  // to even it out (lengths up to 8,192 over 48 sequences: 77 us, 102 whole; to
+  // 16,384 over 32: 116, 131; where all are as long as the longest that costs a
+  // little: 147.7, 147.3 and 187, 180).  With more rows the pieces' starts cost more
+  // than that (8 x 64 rows on 8,192 each: 56 us in 4, 67 in 7).
   if (kv.S > 1 && rows <= 16 && len > 4096 && units < 4 * cus) chunk = std::min(chunk, std::max<int64_t>(1280, len / 8));
   const int64_t step = kStep * kWaves;
   chunk = std::max<int64_t>(step, (chunk + step - 1) / step * step);

@@ -16,8 +16,12 @@
 // so that both matrix operands read 16 contiguous codes per lane.  One
 // workgroup takes one (sequence, page, head) of K or of V: it is the only
 // writer of that page and head.  Roofline: HBM (5 bytes a value): three prompts
-// to 2,047 tokens, 8 heads of 128, 16 us (a copy of as much takes 11.5); for
-// single tokens the launch and two trips to memory, 24 tokens 5.8 us.
+// to 2,047 tokens, 8 heads of 128, 16.1 us (a copy of as much takes 11.5).  K's
+// workgroups alone take 12.2 of those and V's 14.8: most of it is each
+// workgroup's chain (two trips to memory, the page's maximum, V's codes through
+// LDS) and not bytes.  Single tokens: the launch and that chain, 24 tokens 5.4 us,
+// 6.0 where every page's scale grows; 48 tokens after 96 held ones in pages of
+// 128 10.2, and 14.2 where all of those are requantised.
 #include "tern_cache.h"
 
 namespace tern {

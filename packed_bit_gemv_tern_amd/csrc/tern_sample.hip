@@ -971,10 +971,10 @@ __global__ __launch_bounds__(T) void finish_kernel(Launch L) {
 // Tokens per chunk.  A few rows: one tile per workgroup, so that a row is read
 // at once.  Where there is a histogram its workgroups all add into the row's
 // bins, and beyond 256 of them that costs more than longer chunks do (top-k
-// and top-p on 8 rows of 151,936: 47 us at 1,024 tokens, 35 at 2,048, 30 at
-// 4,096, 36 at 8,192; without a histogram 15.8 / 17.9 / 18.2 / 25.6); many
-// rows want no more than about 2,048 workgroups (64 rows: 61 us at 4,096, 56 at
-// 8,192, 59 at 16,384; 96 rows: 69 at 8,192, 81 at 16,384).
+// and top-p on 8 rows of 151,936: 47 us at 1,024 tokens, 35 at 2,048, 32 at
+// 4,096, 37 at 8,192; without a histogram 17.8 / 19.8 / 19.8 / 25.9); many
+// rows want no more than about 2,048 workgroups (64 rows: 59 us at 4,096, 57 at
+// 8,192, 64 at 16,384; 96 rows: 81 at 8,192, 91 at 16,384).
 int64_t tokens_per_chunk(int64_t M, int64_t N, bool cuts) {
   auto chunks = [&](int64_t per) { return mul_sat(M, (N + per - 1) / per); };
   if (chunks(kChunkMin) <= (cuts ? 256 : 1280)) return kChunkMin;
