@@ -213,9 +213,10 @@ __device__ __forceinline__ VScale v_scale(float vs) {
 // What a row has summed: o holds sums of code * e^s vs in units of 2^R, l the
 // sum of e^s in units of 2^L; R and L are whole numbers, so changing units
 // is exact.  R grows where a weight would pass 2^15 (fp16 ends at 2^16), L where
-// an e^s would pass 2^24.
+// an e^s would pass 2^24 (in waves with a base: 1).
 constexpr float kNoUnit = -3.0e38f;  // nothing summed yet (finite: differences with -infinity stay that)
 constexpr float kTop = 15.0f;
+constexpr float kLead = 24.0f;  // octaves that an e^s may be above L
 constexpr float kReset = 10.0f;  // a new R brings the step's largest weight to 2^9 .. 2^10
 struct RowUnits {
   float R, L;
@@ -260,9 +261,10 @@ __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScal
   float tl = mx + (v.lm + v.e);  // the lane's largest weight
   float t = max_groups(tl);
   float e = v.e;
-  if (__any(t - r.R > kTop || mx - r.L > 24.0f)) {
+  const float ahead = far.any ? 0.0f : kLead;
+  if (__any(t - r.R > kTop || mx - r.L > ahead)) {
     float ms = __builtin_ceilf(max_groups(mx));
-    const bool beyond = ms - r.L > 24.0f && fabsf(ms) > kFar;
+    const bool beyond = ms - r.L > ahead && fabsf(ms) > kFar;
     if (__any(beyond)) {  // (what the row has summed vanishes beside e^ms)
       far.any = true;
       if (beyond) {
@@ -278,7 +280,7 @@ __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScal
       t = max_groups(tl);
       ms = __builtin_ceilf(max_groups(mx));
     }
-    if (ms - r.L > 24.0f) {
+    if (ms - r.L > ahead) {
       l *= pow2_of(r.L - ms);
       r.L = ms;
     }
@@ -316,6 +318,18 @@ __device__ __forceinline__ float row_weights(const f32x4 (&sc)[4], float f, cons
       lo[k][2 * i] = r[0], lo[k][2 * i + 1] = r[1];
     }
   return __builtin_ldexpf(sum * v.rm, (int)(-d - r.L));
+}
+
+// The row's sum of e^s, and its unit's exponent for the join.  The unit brings the
+// sum to 1/2 .. 1, so that sums of values are no larger than the values (a base
+// has no digits for that: there the unit is the largest e^s as it is).
+__device__ __forceinline__ float whole_sum(float l, RowUnits& r, const Far& far, int row, float& m) {
+  l = sum_groups(l);
+  const float base = far.any ? far.base[row] : 0.0f;
+  const int e = l > 0.0f && base == 0.0f ? __builtin_amdgcn_frexp_expf(l) : 0;
+  r.L += (float)e;
+  m = l == 0.0f ? kNegInf : base + r.L;
+  return __builtin_ldexpf(l, -e);
 }
 
 // The weights that a band takes, e^s vs from 2^from up to 2^to (-infinity, and
@@ -664,8 +678,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
   // join the waves, a tile at a time
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]);
-    if (g == 0) sml[wave][16 * u + n][0] = lt == 0.0f ? kNegInf : units[u].L + (far.any ? far.base[16 * u + n] : 0.0f), sml[wave][16 * u + n][1] = lt;
+    float m;
+    const float lt = whole_sum(l[u], units[u], far, 16 * u + n, m);
+    if (g == 0) sml[wave][16 * u + n][0] = m, sml[wave][16 * u + n][1] = lt;
   }
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
@@ -964,7 +979,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const float lt = sum_groups(l[u]);
+    float m;
+    const float lt = whole_sum(l[u], units[u], far, 16 * u + n, m);
     const int r = row_lo + 16 * (NT * wave + u) + n;
     if (r >= rows) continue;
     uint32_t rem;
@@ -975,7 +991,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
     const int back = (int)(units[u].R - units[u].L);
     float* out = whole ? a.y + row * a.ldy + hq * D : a.part + at * D;
     if (!whole && g == 0) {
-      store_g(a.part_ml + 2 * at, lt == 0.0f ? kNegInf : units[u].L + (far.any ? far.base[16 * u + n] : 0.0f));
+      store_g(a.part_ml + 2 * at, m);
       store_g(a.part_ml + 2 * at + 1, lt);
     }
 #pragma unroll

@@ -128,3 +128,20 @@ def test_whole_contexts_in_tiles_of_128(D):
     pg.table = np.concatenate([pg.table[:1], idle, pg.table[1:]])
     got = attend(pg.upload(), [140] + [1] * 254 + [66], [310] + [0] * 254 + [300], q, scale=14 / 128, max_len=320)
     assert (got[140: 394] == 0).all()
+
+
+@pytest.mark.parametrize("gap", [5, 11, 14, 16])
+@pytest.mark.parametrize("scale", [1e30, 1e-30])
+@pytest.mark.parametrize("new,group,columns", TILES)
+def test_scores_that_grow_beside_extreme_scales(new, group, columns, scale, gap):
+    """V scales at either end of the range, the first 64 positions' scores
+    below the others' by `gap`."""
+    n = 900
+    pg, way, q = setup(new, group, columns, n, seed=gap, scales=lambda rng, shape: rng.uniform(0.5, 1.0, shape))
+    pg.host.v_scale *= np.float32(scale)
+    pg.host.k_scale[:] = 1.0 / 127
+    pg.host.k //= 8
+    for s in range(2):
+        for j in range(64, n - 20 * s):
+            pg.host.k[pg.table[s, j // 16], :, j % 16] = 100 * way + pg.rng.integers(-20, 20, 128)
+    attend(pg.upload(), [new, new], [n, n - 20], q, scale=gap / 100)
