@@ -265,15 +265,12 @@ __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScal
   if (__any(t - r.R > kTop || mx - r.L > ahead)) {
     float ms = __builtin_ceilf(max_groups(mx));
     const bool beyond = ms - r.L > ahead && fabsf(ms) > kFar;
-    if (__any(beyond)) {  // (what the row has summed vanishes beside e^ms)
+    if (__any(beyond)) {
       far.any = true;
       if (beyond) {
         far.base[row] += ms;  // (the row's lanes alike)
-        r = {kNoUnit, kNoUnit};
-        l = 0.0f;
+        r = {fmaxf(r.R - ms, kNoUnit), fmaxf(r.L - ms, kNoUnit)};
       }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] *= beyond ? 0.0f : 1.0f;
       mask_scores(sc, f, 15, beyond ? ms : 0.0f);
       mx = largest_score(sc, f);
       tl = mx + (v.lm + v.e);

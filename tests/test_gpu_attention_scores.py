@@ -6,8 +6,10 @@ import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
-pytest.importorskip("torch")
+torch = pytest.importorskip("torch")
+from packed_bit_gemv_tern_amd import tern  # noqa: E402
 from attention_util import TILES, attend, pad_table  # noqa: E402
+from gpu_util import DEV, to_dev  # noqa: E402
 from kv_util import Paged  # noqa: E402
 
 
@@ -88,3 +90,40 @@ def test_scores_of_any_finite_size(new, group, columns, size, sign):
         exponent = np.log(2) * 2 ** -24 * 5 * S if S < 2 ** 20 else 0
         tol = (2 ** -19 + exponent + (n / 64 + 32) * 8 * 2 ** -24) * np.abs(v).mean(0)
         assert (np.abs(got[r] - v.mean(0)) <= tol).all(), r
+
+
+@pytest.mark.parametrize("new,group", [(1, 4), (3, 4), (6, 4), (40, 4)])
+def test_scores_that_pass_the_border_in_small_steps(new, group):
+    """Two keys whose scores lie just under and just over 2^20 (times ln 2), two
+    octaves apart, in steps of one wave, beside rows of far larger scores: both
+    count, as 1 to 4.  A score there is rounded to 2^-4 some five times (two
+    products' sums, three factors), which moves a weight of 1/5 by less than 0.06."""
+    n = 400
+    pg = pages(new, 0, n, 64, 5)
+    pad_table(pg, 100000)
+    way = pg.rng.choice(np.array([-1.0, 1.0]), 64)
+    pg.host.k[:] = -60 * way
+    pg.host.k_scale[:] = np.float32(1 / 64)
+    a, b = 3, 266  # the same wave's, whichever tile
+    for s in range(2):
+        for j, c in ((a, -60), (b, 60)):
+            page = pg.table[s, j // 16]
+            pg.host.k[page, 0, j % 16] = 64 * way
+            pg.host.k[page, 0, j % 16, 0] = c
+    q = np.empty((2 * new, group, 64), np.float32)
+    q[:] = 2 ** 20 * np.log(2) / 63 * way  # 63 channels of one: a score of 2^20
+    q[..., 0] = 2 * np.log(2) / (120 / 64)
+    far = np.arange(2 * new * group).reshape(2 * new, group) % 2 == 1
+    q[far] *= 1000
+    length = [n, n - 20]
+    bt = pg.upload().batch([new, new], length)
+    y = torch.empty((2 * new, group * 64), device=DEV)
+    ws = torch.empty(tern.tern_attention_workspace_bytes(pg.cache, bt, group), dtype=torch.uint8, device=DEV)
+    tern.tern_attention(pg.cache, bt, to_dev(q.reshape(2 * new, -1)), group * 64, group, 1.0, y, group * 64, ws)
+    got = y.cpu().numpy().reshape(q.shape)
+    for r in range(2 * new):
+        s = r // new
+        v = [pg.host.v[pg.table[s, j // 16], 0, :, j % 16] * float(pg.host.v_scale[pg.table[s, j // 16], 0]) for j in (a, b)]
+        near = ~far[r]
+        assert (np.abs(got[r, near] - (0.2 * v[0] + 0.8 * v[1])) <= 0.06 * np.abs(v[0] - v[1]) + 1e-5).all(), r
+        assert (np.abs(got[r, far[r]] - v[1]) <= 1e-5).all(), r
