@@ -233,17 +233,19 @@ __device__ __forceinline__ void change_unit(float to, RowUnits& r, f32x4 (&o)[DT
 }
 
 // Scores beyond 2^20, of which fp32 holds too few digits for units: the row's are
-// counted from a base, the largest when that was met (Far: what a wave keeps of it).
+// counted from a base, the largest when that was met (Far: what a wave keeps of
+// it).  Scores are rounded before the base is taken off, as a plain form rounds
+// them, so those near the base are exact beside it.
 constexpr float kFar = 1048576.0f;
 struct Far {
   float* base;  // of the wave's rows, in LDS
   bool any;     // some row has one
 };
-// One row's 16 scores of a step times f (units of log2), less their base, of which
-// only the positions up to `last` of the lane's 16 count.
-__device__ __forceinline__ void mask_scores(f32x4 (&sc)[4], float& f, int last, float base) {
+// One row's 16 scores of a step times f (units of log2), of which only the
+// positions up to `last` of the lane's 16 count.
+__device__ __forceinline__ void mask_scores(f32x4 (&sc)[4], float& f, int last) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f - base : kNegInf;
+  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] = i <= last ? sc[i >> 2][i & 3] * f : kNegInf;
   f = 1.0f;
 }
 __device__ __forceinline__ float largest_score(const f32x4 (&sc)[4], float f) {
@@ -252,32 +254,40 @@ __device__ __forceinline__ float largest_score(const f32x4 (&sc)[4], float f) {
   for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
   return mx * f;
 }
+// Scores (f is 1) from the row's base, a new one where they pass it by 2^20.
+__device__ __forceinline__ void from_base(f32x4 (&sc)[4], RowUnits& r, const Far& far, int row) {
+  const float ms = __builtin_ceilf(max_groups(largest_score(sc, 1.0f)));
+  float base = far.base[row];
+  if (ms - base > r.L && fabsf(ms - base) > kFar) {
+    r = {fmaxf(r.R - (ms - base), kNoUnit), fmaxf(r.L - (ms - base), kNoUnit)};
+    far.base[row] = base = ms;  // (the row's lanes alike)
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] -= base;
+}
 // Brings the row's units to the step.  Returns the exponent that the lane's weights
 // take from the V scale (v.e; -infinity where their e^s had to be summed here).
 template <int DT>
 __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScale& v, RowUnits& r, float& l,
                                            f32x4 (&o)[DT], Far& far, int row) {
+  if (far.any) from_base(sc, r, far, row);
   float mx = largest_score(sc, f);
   float tl = mx + (v.lm + v.e);  // the lane's largest weight
   float t = max_groups(tl);
   float e = v.e;
-  const float ahead = far.any ? 0.0f : kLead;
-  if (__any(t - r.R > kTop || mx - r.L > ahead)) {
+  const float lead = far.any ? 0.0f : kLead;
+  if (__any(t - r.R > kTop || mx - r.L > lead)) {
     float ms = __builtin_ceilf(max_groups(mx));
-    const bool beyond = ms - r.L > ahead && fabsf(ms) > kFar;
-    if (__any(beyond)) {
+    if (!far.any && __any(ms - r.L > lead && fabsf(ms) > kFar)) {
       far.any = true;
-      if (beyond) {
-        far.base[row] += ms;  // (the row's lanes alike)
-        r = {fmaxf(r.R - ms, kNoUnit), fmaxf(r.L - ms, kNoUnit)};
-      }
-      mask_scores(sc, f, 15, beyond ? ms : 0.0f);
+      mask_scores(sc, f, 15);
+      from_base(sc, r, far, row);
       mx = largest_score(sc, f);
       tl = mx + (v.lm + v.e);
       t = max_groups(tl);
       ms = __builtin_ceilf(max_groups(mx));
     }
-    if (ms - r.L > ahead) {
+    if (ms - r.L > lead) {
       l *= pow2_of(r.L - ms);
       r.L = ms;
     }
@@ -367,10 +377,10 @@ __device__ bool next_band(int pass, bool live, RowUnits& r, f32x4 (&o)[DT], Band
   b = n;
   return n.from < kInf;
 }
-__device__ __forceinline__ void band_scores(f32x4 (&sc)[4], float& f, const VScale& v, const Band& b) {
+__device__ __forceinline__ void band_scores(f32x4 (&sc)[4], float& f, const VScale& v, const Band& b, float base) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float s = sc[i >> 2][i & 3] * f, t = s + (v.lm + v.e);
+    const float s = sc[i >> 2][i & 3] * f - base, t = s + (v.lm + v.e);
     sc[i >> 2][i & 3] = t >= b.from && t < b.to ? s : kNegInf;
   }
   f = 1.0f;
@@ -599,13 +609,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a) {
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float f = fac[u] * ks;
-        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1, far.any ? far.base[16 * u + n] : 0.0f);
+        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
         f16x8 hi[2], lo[2];
         if (pass == 0) {
           const float e = row_units(sc[u], f, v, units[u], l[u], o[u], far, 16 * u + n);
           l[u] += row_weights(sc[u], f, v, e, units[u], hi, lo);
         } else {
-          band_scores(sc[u], f, v, band[wave][16 * u + n]);
+          band_scores(sc[u], f, v, band[wave][16 * u + n], far.any ? far.base[16 * u + n] : 0.0f);
           row_weights(sc[u], f, v, v.e, units[u], hi, lo);
         }
 #pragma unroll
@@ -929,12 +939,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a)
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float f = qfac[u] * ks;
-        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1, far.any ? far.base[16 * u + n] : 0.0f);
+        if (masked || far.any) mask_scores(sc[u], f, here ? pos[u] - jv : -1);
         if (pass == 0) {
           const float e = row_units(sc[u], f, v, units[u], l[u], o[u], far, 16 * u + n);
           l[u] += row_weights(sc[u], f, v, e, units[u], hi[u], lo[u]);
         } else {
-          band_scores(sc[u], f, v, band[16 * (NT * wave + u) + n]);
+          band_scores(sc[u], f, v, band[16 * (NT * wave + u) + n], far.any ? far.base[16 * u + n] : 0.0f);
           row_weights(sc[u], f, v, v.e, units[u], hi[u], lo[u]);
         }
       }

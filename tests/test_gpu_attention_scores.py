@@ -127,3 +127,36 @@ def test_scores_that_pass_the_border_in_small_steps(new, group):
         near = ~far[r]
         assert (np.abs(got[r, near] - (0.2 * v[0] + 0.8 * v[1])) <= 0.06 * np.abs(v[0] - v[1]) + 1e-5).all(), r
         assert (np.abs(got[r, far[r]] - v[1]) <= 1e-5).all(), r
+
+
+@pytest.mark.parametrize("new,group", [(1, 4), (3, 4), (6, 4), (40, 4)])
+@pytest.mark.parametrize("first,then", [(1e8, 3.3e8), (1e10, 7.7e10), (3e6, 1e9), (2 ** 20, 2 ** 21), (1e30, 2.9e30)])
+def test_far_scores_that_grow(new, group, first, then):
+    """A row's largest score is met first in one step of a wave, one some times as
+    large in a later step of it, and the same key twice more after that: the row is
+    the mean of the values of those three (each weight to 2^-20, see above)."""
+    n = 1800
+    pg = pages(new, 0, n, 64, 6)
+    pad_table(pg, 100000)
+    way = pg.rng.choice(np.array([-1.0, 1.0]), 64)
+    pg.host.k[:] = -60 * way
+    pg.host.k_scale[:] = np.float32(1 / 127)
+    top = [266, 520, 780]
+    for s in range(2):
+        for j in [3] + top:
+            page = pg.table[s, j // 16]
+            pg.host.k[page, 0, j % 16] = (127 if j in top else max(1, round(127 * first / then))) * way
+    q = np.empty((2 * new, group, 64), np.float32)
+    q[:] = then / 64 * way * pg.rng.uniform(0.9, 1.1, (2 * new, group, 1))
+    length = [n, n - 20]
+    bt = pg.upload().batch([new, new], length)
+    y = torch.empty((2 * new, group * 64), device=DEV)
+    ws = torch.empty(tern.tern_attention_workspace_bytes(pg.cache, bt, group), dtype=torch.uint8, device=DEV)
+    tern.tern_attention(pg.cache, bt, to_dev(q.reshape(2 * new, -1)), group * 64, group, 1.0, y, group * 64, ws)
+    got = y.cpu().numpy().reshape(q.shape)
+    for r in range(2 * new):
+        s = r // new
+        v = np.array([pg.host.v[pg.table[s, j // 16], 0, :, j % 16] * float(pg.host.v_scale[pg.table[s, j // 16], 0])
+                      for j in top])
+        tol = (2 ** -19 + (n / 64 + 32) * 8 * 2 ** -24) * np.abs(v).mean(0)
+        assert (np.abs(got[r] - v.mean(0)) <= tol).all(), r
