@@ -540,8 +540,8 @@ int tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, const
  * to the accuracy of fp32, measured by sum_d |q_d k_jd| and sum_j w_j |v_j|:
  * codes enter the matrix cores exactly, elements of q at 23 bits (or to 2^-33 of
  * their row's largest), weights with their V scale at 23 bits (or to 2^-33 of the
- * row's largest sum, however far below the largest weight that is); statistics and
- * sums are fp32.  A row that sees no position is 0.  Rows of no sequence are left as they were.  A row
+ * row's largest sum, however far below the largest weight that is, while e^(a_j -
+ * max a) is 2^-126 or more); statistics and sums are fp32.  A row that sees no position is 0.  Rows of no sequence are left as they were.  A row
  * of q that is not finite spoils its own row and head of y alone.
  *   q, y  device, rows x (q_heads * head_dim) floats, row strides ldq and
  *         ldy >= q_heads * head_dim (when rows > 1), 4-byte aligned;

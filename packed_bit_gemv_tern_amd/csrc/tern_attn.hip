@@ -291,7 +291,9 @@ __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScal
       l *= pow2_of(r.L - ms);
       r.L = ms;
     }
-    change_unit(t - r.R > kTop ? __builtin_ceilf(t) - kReset : r.R, r, o);
+    // (far below a base whose own values are 0, fp32's steps may be wider than kReset)
+    const float to = __builtin_ceilf(t) - kReset;
+    change_unit(t - r.R > kTop ? (t - to > kTop ? t : to) : r.R, r, o);
   }
   // A lane whose weights vanish beside the row's (a V scale of 0, or 2^-90 of
   // the others'): its e^s count all the same.
@@ -362,7 +364,7 @@ __device__ bool next_band(int pass, bool live, RowUnits& r, f32x4 (&o)[DT], Band
   const bool settled = !(big < kSettled);
   Band n = {kInf, kNegInf};
   if (pass == 0) {
-    if (live && !settled && r.R > kNoUnit) {
+    if (live && !settled && r.R - r.L > -200.0f) {  // (below that y is 0 in fp32)
       n = {r.R + kFull, kInf};
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};

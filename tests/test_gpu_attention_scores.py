@@ -160,3 +160,25 @@ def test_far_scores_that_grow(new, group, first, then):
                       for j in top])
         tol = (2 ** -19 + (n / 64 + 32) * 8 * 2 ** -24) * np.abs(v).mean(0)
         assert (np.abs(got[r] - v.mean(0)) <= tol).all(), r
+
+
+@pytest.mark.parametrize("new,group,columns", TILES)
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e7, 3e7, 1e8, 1e9, 1e20])
+def test_far_scores_on_values_of_0(new, group, columns, size):
+    """The keys of the largest scores lie on pages whose V scale is 0, and the others
+    far below them: those rows are 0, ordinary ones beside them as ever."""
+    n = 700
+    pg = pages(new, columns, n, 64, 7)
+    way = pg.rng.choice(np.array([-1.0, 1.0]), 64)
+    pg.host.k[:] = (-60 * way + pg.rng.integers(-30, 30, pg.host.k.shape)).astype(np.int8)
+    pg.host.k_scale[:] = np.float32(1 / 127)
+    for s in range(2):
+        for j in (5, 70, 300, 301, 600):
+            pg.host.k[pg.table[s, j // 16], 0, j % 16] = 127 * way
+            pg.host.v_scale[pg.table[s, j // 16]] = 0
+    q = np.empty((2 * new, group, 64), np.float32)
+    q[:] = size * way / 30 * pg.rng.uniform(0.5, 1.5, (2 * new, group, 1))
+    ordinary = np.arange(2 * new) % 3 == 2
+    q[ordinary] = pg.rng.normal(0, 1, q[ordinary].shape)
+    got = attend(pg.upload(), [new, new], [n, n - 70], q, scale=1.0)
+    assert (got[~ordinary] == 0).all()
