@@ -217,6 +217,7 @@ __device__ __forceinline__ VScale v_scale(float vs) {
 constexpr float kNoUnit = -3.0e38f;  // nothing summed yet (finite: differences with -infinity stay that)
 constexpr float kTop = 15.0f;
 constexpr float kLead = 24.0f;  // octaves that an e^s may be above L
+constexpr float kDeep = 200.0f;  // R is not further below L: such weights give 0 in fp32
 constexpr float kReset = 10.0f;  // a new R brings the step's largest weight to 2^9 .. 2^10
 struct RowUnits {
   float R, L;
@@ -291,9 +292,7 @@ __device__ __forceinline__ float row_units(f32x4 (&sc)[4], float& f, const VScal
       l *= pow2_of(r.L - ms);
       r.L = ms;
     }
-    // (far below a base whose own values are 0, fp32's steps may be wider than kReset)
-    const float to = __builtin_ceilf(t) - kReset;
-    change_unit(t - r.R > kTop ? (t - to > kTop ? t : to) : r.R, r, o);
+    change_unit(fmaxf(t - r.R > kTop ? __builtin_ceilf(t) - kReset : r.R, r.L - kDeep), r, o);
   }
   // A lane whose weights vanish beside the row's (a V scale of 0, or 2^-90 of
   // the others'): its e^s count all the same.
@@ -364,7 +363,7 @@ __device__ bool next_band(int pass, bool live, RowUnits& r, f32x4 (&o)[DT], Band
   const bool settled = !(big < kSettled);
   Band n = {kInf, kNegInf};
   if (pass == 0) {
-    if (live && !settled && r.R - r.L > -200.0f) {  // (below that y is 0 in fp32)
+    if (live && !settled && r.R > r.L - kDeep) {
       n = {r.R + kFull, kInf};
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};

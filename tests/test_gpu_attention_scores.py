@@ -182,3 +182,26 @@ def test_far_scores_on_values_of_0(new, group, columns, size):
     q[ordinary] = pg.rng.normal(0, 1, q[ordinary].shape)
     got = attend(pg.upload(), [new, new], [n, n - 70], q, scale=1.0)
     assert (got[~ordinary] == 0).all()
+
+
+@pytest.mark.parametrize("new,group,columns", TILES)
+@pytest.mark.parametrize("size", [1e6, 1e7, 3e7, 6e7, 1e8, 3e8, 1e9])
+@pytest.mark.parametrize("seed", [8, 9])
+def test_equal_far_scores_below_values_of_0(new, group, columns, size, seed):
+    """The same as above where the others' scores are equal and their V scales
+    octaves apart: their weights' ratios are ordinary, 10^6 octaves and more below
+    the base."""
+    n = 700
+    pg = pages(new, columns, n, 64, seed)
+    way = pg.rng.choice(np.array([-1.0, 1.0]), 64)
+    pg.host.k[:] = -60 * way
+    pg.host.k_scale[:] = np.float32(1 / 127)
+    pg.host.v_scale[:] = 2.0 ** pg.rng.uniform(-12, 12, pg.host.v_scale.shape)
+    for s in range(2):
+        for j in (5, 70, 300, 301, 600):
+            pg.host.k[pg.table[s, j // 16], 0, j % 16] = 127 * way
+            pg.host.v_scale[pg.table[s, j // 16]] = 0
+    q = np.empty((2 * new, group, 64), np.float32)
+    q[:] = size * way / 30 * pg.rng.uniform(0.5, 1.5, (2 * new, group, 1))
+    got = attend(pg.upload(), [new, new], [n, n - 70], q, scale=1.0)
+    assert (got == 0).all()
