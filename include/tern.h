@@ -440,6 +440,57 @@ int tern_head_gemv(const int8_t* W, const float* s_row, const int32_t* rowsum, i
                    const int32_t* z, float* y, int64_t ldy, int32_t* acc, hipStream_t stream);
 
 /*
+ * tern_linear_epilogue -- a ternary linear with what follows it, in one launch:
+ * bias, activation, the product with a second linear (a gated feed-forward's
+ * gate and up projections: model card "Architecture", SwiGLU) and the residual.
+ * With v and v_up the outputs of tern_gemm_smallM for w and up, each plus its
+ * bias where it has one (fp32 sum, one rounding),
+ *     h[m][i] = act(v[m][i])                  up NULL
+ *             = act(v[m][i]) * v_up[m][i]     otherwise
+ *     y[m][i] = h[m][i]                       res NULL
+ *             = res[m][i] + h[m][i]           otherwise
+ * each one fp32 rounding.  act: TERN_ACT_NONE; TERN_ACT_SILU, x / (1 + e^-x) in
+ * the steps of the stack launch's gate (x_up of tern_linear_desc), so a gated
+ * linear gives what the two linears and that gate give, bit for bit;
+ * TERN_ACT_GELU, the tanh form x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
+ * The activations only see finite values if scales, biases and inputs are.
+ *   w, up  host structures of device arrays: packed (N rows of
+ *          tern_row_bytes(K) bytes, 16-byte aligned), s_row, rowsum (N each)
+ *          and bias (N floats, or NULL);  up NULL: no gate;
+ *   q, ldq, s_act, z, y, ldy  as for tern_gemm_smallM, any M; only the K
+ *          columns of a q row are read;
+ *   res    device, M x N floats, row stride ldr >= N (when M > 1), or NULL; may
+ *          be y itself (same address and stride: in place), and must not
+ *          overlap it otherwise.
+ */
+enum { TERN_ACT_NONE = 0, TERN_ACT_SILU = 1, TERN_ACT_GELU = 2 };
+typedef struct {
+  const uint8_t* packed;
+  const float* s_row;
+  const int32_t* rowsum;
+  const float* bias;
+} tern_weights;
+int tern_linear_epilogue(const tern_weights* w, const tern_weights* up, int64_t N, int64_t K, int64_t M,
+                         const int8_t* q, int64_t ldq, const float* s_act, const int32_t* z, int act,
+                         const float* res, int64_t ldr, float* y, int64_t ldy, hipStream_t stream);
+
+/*
+ * tern_embed -- rows of the int8 embedding table (model card, "Token
+ * embeddings": one scale per row, the head's format; with tied embeddings the
+ * head's own table), the first operator of a step:
+ *     x[m][j] = (W[id][j] * s_row[id]) * scale      id = ids[m]  (fp32, RNE, in
+ *                                                                 this order)
+ * and a row of zeros where ids[m] is not in [0, N): an idle slot, or tern_sample's
+ * -1.
+ *   W      device, N x K int8, row stride ldw >= K (any alignment; rows of whole
+ *          dwords, x in rows of 16 bytes and K a multiple of 4 are faster);
+ *   s_row  device, N floats;  ids  device, M int32;  scale finite;
+ *   x      device, M x K floats, row stride ldx >= K when M > 1 (written).
+ */
+int tern_embed(const int8_t* W, const float* s_row, int64_t N, int64_t K, int64_t ldw, const int32_t* ids, int64_t M,
+               float scale, float* x, int64_t ldx, hipStream_t stream);
+
+/*
  * tern_rmsnorm_quantize -- the residual's addition, the root-mean-square norm
  * and the quantisation of its result, for the linears and the head that read
  * a layer's normalised hidden state (Neutrino-1 8B model card,
@@ -556,6 +607,128 @@ int64_t tern_attention_workspace_bytes(const tern_kv_cache* cache, const tern_kv
 int tern_attention(const tern_kv_cache* cache, const tern_kv_batch* batch, const float* q, int64_t ldq,
                    int64_t q_heads, float scale, float* y, int64_t ldy, void* workspace, int64_t workspace_bytes,
                    hipStream_t stream);
+
+/*
+ * tern_qk_norm_rope -- the per-head RMS norm of q and k and their rotary
+ * positions (model card, "Architecture": QK-norm, RoPE), between the q/k/v
+ * linears and tern_kv_append / tern_attention.  For each head's row x of
+ * head_dim elements of a sequence's i-th new row, at position p = len[s] - n + i,
+ *     n_j = x_j * gain_j / sqrt(mean_j(x_j^2) + eps)       (gain NULL: n = x)
+ *     a_i = p * inv_freq[i]                                i < rot_dim / 2
+ *     y_i               = magnitude * (n_i cos a_i - n_(i + rot_dim/2) sin a_i)
+ *     y_(i + rot_dim/2) = magnitude * (n_(i + rot_dim/2) cos a_i + n_i sin a_i)
+ *     y_j = n_j                                            j >= rot_dim
+ * in fp64 with one rounding to fp32 (angles to 2^31, so |inv_freq| <= 1 for any
+ * position).
+ *   batch     table, ld_table and max_len are not used (table may be NULL); rows
+ *             of no sequence, past max_new, or at a negative position (an idle
+ *             slot) are left as they were, and a row that several sequences
+ *             claim takes the first one's position;
+ *   head_dim  64 or 128, rot_dim a multiple of 8 in [0, head_dim], otherwise
+ *             TERN_ERR_UNSUPPORTED;  inv_freq  device, rot_dim / 2 floats;
+ *   q, q_out  device, rows x (q_heads * head_dim) floats, row strides ldq, ldqo
+ *             >= that (when rows > 1), 4-byte aligned; q_out may be q itself
+ *             (same address and stride: in place), and must not overlap it
+ *             otherwise;  q_gain  device, head_dim floats, or NULL;  q_heads = 0:
+ *             no q;
+ *   k, ...    the same for k with `heads` heads;
+ *   eps > 0 and finite, magnitude finite (1, or a stretched context's factor).
+ */
+int tern_qk_norm_rope(const tern_kv_batch* batch, int64_t head_dim, const float* inv_freq, int64_t rot_dim,
+                      float magnitude, const float* q, int64_t ldq, int64_t q_heads, const float* q_gain, float* q_out,
+                      int64_t ldqo, const float* k, int64_t ldk, int64_t heads, const float* k_gain, float* k_out,
+                      int64_t ldko, float eps, hipStream_t stream);
+
+/*
+ * Pages under the cache: a pool of `pages` pages, of which the table's rows (the
+ * table of tern_kv_batch, one row for each of S slots) hold some.  refs[p] is the
+ * number of entries that hold page p (0: free); the calls below keep it, and a
+ * fresh pool is refs of zeros.  A page may be held by several rows (a prompt that
+ * several answers share); nothing writes into a page that others hold, if
+ * tern_kv_reserve precedes every tern_kv_append.  Per step:
+ *     want = len + new tokens;  tern_kv_reserve(len, want);  tern_kv_copy of what
+ *     it lists, in every layer;  append and attention with length want;  after
+ *     verification tern_kv_truncate(want, kept).
+ *   refs   device, pages int32;  table  device, S x ld_table int32;
+ *   page_tokens 16, 32, 64 or 128 (otherwise TERN_ERR_UNSUPPORTED).
+ * len (device, S int32) is the number of tokens that a row has pages for: what
+ * the last reserve granted or the last truncate kept (0 or less: none).  The
+ * device arrays are not read on the host; entries outside [0, pages) hold nothing,
+ * and nothing reaches past the buffers.  refs that do not count the entries give
+ * unspecified ids.  Results do not depend on any order of execution.  Calls on
+ * one pool must be ordered (one stream, or waits).
+ */
+typedef struct {
+  int32_t* refs;
+  int32_t* table;
+  int64_t pages, ld_table, S, page_tokens;
+} tern_kv_pool;
+
+/* Bytes of the workspace (device, 256-byte aligned) of tern_kv_reserve and
+ * tern_kv_compact; it carries nothing from call to call.  0 on bad arguments. */
+int64_t tern_kv_pool_workspace_bytes(const tern_kv_pool* pool);
+
+/*
+ * tern_kv_fork -- for i < n: row dst[i] takes the pages of row src[i] (of its
+ * first len[src[i]] tokens), each counted once more.  The row must hold no
+ * pages (a fresh one, or truncated to 0); its entries past those are left.  A
+ * pair is passed over if a row is not in [0, S), if its dst is the src of any
+ * pair, or if a later pair has the same dst.
+ *   src, dst  device, n int32.
+ */
+int tern_kv_fork(const tern_kv_pool* pool, const int32_t* len, const int32_t* src, const int32_t* dst, int64_t n,
+                 hipStream_t stream);
+
+/*
+ * tern_kv_truncate -- each row s keeps its first keep[s] tokens: entries from
+ * page ceil(keep[s] / page_tokens) to the last of len[s] become -1 and their
+ * pages are counted down (free at 0).  keep[s] <= 0 frees the row, keep[s] >=
+ * len[s] leaves it.
+ */
+int tern_kv_truncate(const tern_kv_pool* pool, const int32_t* len, const int32_t* keep, hipStream_t stream);
+
+/*
+ * tern_kv_reserve -- pages for the tokens len[s] .. want[s] - 1 of every row s
+ * (none where want[s] <= len[s]).  A row needs one page for each that those
+ * tokens reach past its last one, and one more, first, if its part-filled last
+ * page is also held by others: that one replaces it, to be copied (of rows that
+ * write into one page in this call and are all that hold it, the last keeps it).
+ * The needs are met in the order of the rows, each with the lowest free pages in
+ * order; the first row whose need exceeds what is left, and every later one that
+ * needs a page or keeps a shared one, gets nothing.  A row that wants more tokens than the
+ * table has pages for gets nothing, and needs none.
+ *   want     device, S int32;
+ *   granted  device, S int32 (written): 1, or 0 for a row that got nothing;
+ *   from, to device, S int32 each (written): row s's part-filled page and its
+ *            copy, -1 and -1 without one: for tern_kv_copy.
+ */
+int tern_kv_reserve(const tern_kv_pool* pool, const int32_t* len, const int32_t* want, int32_t* granted, int32_t* from,
+                    int32_t* to, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * tern_kv_compact -- moves the pages in use together, to ids below their number:
+ * the k-th lowest free page below it takes the k-th highest page in use, for k <
+ * moves (pages / 2 moves always do; with fewer, the highest pages go first).
+ * refs and the entries of the first len[s] tokens of every row are rewritten.
+ *   from, to  device, `moves` int32 each (written): the pages' old and new ids, -1
+ *             and -1 past the last: for tern_kv_copy;
+ *   live      device, one int32 (written): the number of pages in use.
+ */
+int tern_kv_compact(const tern_kv_pool* pool, const int32_t* len, int32_t* from, int32_t* to, int64_t moves,
+                    int32_t* live, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * tern_kv_copy -- for i < n, in every layer l: page to[i] of dst[l] becomes page
+ * from[i] of src[l], codes and scales.  Pairs with an id outside its cache are
+ * passed over.  src may be dst (pages within a cache) if no page of `to` is in
+ * `to` or `from` again; two caches (another number of pages) move a pool's
+ * contents to a larger or smaller one.
+ *   dst, src  host, `layers` caches each, all of the same heads, head_dim and
+ *             page_tokens, otherwise TERN_ERR_INVALID_ARG;
+ *   from, to  device, n int32 each.
+ */
+int tern_kv_copy(const tern_kv_cache* dst, const tern_kv_cache* src, int64_t layers, const int32_t* from,
+                 const int32_t* to, int64_t n, hipStream_t stream);
 
 /*
  * tern_sample -- a token from each row of logits (the head's y), with a given

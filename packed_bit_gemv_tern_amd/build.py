@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtern.so")
 SOURCES = ["tern_api.hip", "tern_pack.hip", "tern_valu.hip", "tern_mfma.hip", "tern_gemm.hip",
            "tern_head.hip", "tern_quant.hip", "tern_block.hip", "tern_packed5.hip", "tern_probe.hip",
-           "tern_norm.hip", "tern_cache.hip", "tern_attn.hip", "tern_sample.hip"]
+           "tern_norm.hip", "tern_cache.hip", "tern_attn.hip", "tern_sample.hip",
+           "tern_epilogue.hip", "tern_embed.hip", "tern_rope.hip", "tern_pages.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <vector>
@@ -205,6 +206,35 @@ int check_kv(const tern_kv_cache* c, const tern_kv_batch* b, KvArgs* a) {
         std::min(b->max_new, b->rows), b->max_len, (int32_t)c->pages, (int32_t)c->heads, (int32_t)c->head_dim,
         (int32_t)log_p, (int32_t)b->rows};
   return TERN_OK;
+}
+
+// The pool as the kernels take it; sizes here, pointers by the calls.
+int check_pool(const tern_kv_pool* c, PoolArgs* p) {
+  if (!c) return TERN_ERR_INVALID_ARG;
+  if (c->pages < 0 || c->S < 0 || c->ld_table < 0) return TERN_ERR_INVALID_ARG;
+  int log_p = 0;
+  while (log_p < 8 && (1 << log_p) != c->page_tokens) ++log_p;
+  if (log_p < 4 || log_p > 7) return TERN_ERR_UNSUPPORTED;
+  if (c->pages > kI32Max || c->S > kI32Max || c->ld_table > (TERN_KV_MAX_LEN >> log_p)) return TERN_ERR_RANGE;
+  *p = {c->refs, c->table, c->pages, c->ld_table, c->S, (int32_t)log_p};
+  return pool_work_items(*p) > kMaxDispatchItems ? TERN_ERR_RANGE : TERN_OK;
+}
+
+bool pool_empty(const PoolArgs& p) { return p.S == 0 || p.pages == 0 || p.ld_table == 0; }
+
+// The pool's arrays and a call's own, all int32.
+int check_pool_buffers(const PoolArgs& p, std::initializer_list<const void*> own) {
+  if (!p.refs || !p.table) return TERN_ERR_INVALID_ARG;
+  for (const void* q : own)
+    if (!q) return TERN_ERR_INVALID_ARG;
+  if (!aligned(p.refs, 4) || !aligned(p.table, 4)) return TERN_ERR_ALIGNMENT;
+  for (const void* q : own)
+    if (!aligned(q, 4)) return TERN_ERR_ALIGNMENT;
+  return TERN_OK;
+}
+
+bool pool_workspace_ok(const PoolArgs& p, const void* workspace, int64_t bytes) {
+  return workspace && bytes >= pool_workspace_bytes(p) && aligned(workspace, 256);
 }
 
 bool kv_empty(const KvArgs& a) { return a.S == 0 || a.rows == 0 || a.max_new == 0; }
@@ -445,6 +475,177 @@ int tern_sample(const float* logits, int64_t M, int64_t N, int64_t ldl, const fl
   const SampleArgs a = {logits, M, N, ldl, u, temperature, top_p, min_p, top_k, token, prob, kept};
   hipError_t e = launch_sample(a, workspace, stream);
   return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_linear_epilogue(const tern_weights* w, const tern_weights* up, int64_t N, int64_t K, int64_t M,
+                         const int8_t* q, int64_t ldq, const float* s_act, const int32_t* z, int act,
+                         const float* res, int64_t ldr, float* y, int64_t ldy, hipStream_t stream) {
+  if (!w || act < TERN_ACT_NONE || act > TERN_ACT_GELU) return TERN_ERR_INVALID_ARG;
+  EpilogueArgs a;
+  memset(&a, 0, sizeof(a));
+  for (int i = 0; i < (up ? 2 : 1); ++i) {
+    const tern_weights& t = i ? *up : *w;
+    const int st = check_linear(t.packed, t.s_row, t.rowsum, N, K, M, q, ldq, s_act, z, y, ldy, nullptr);
+    if (st != TERN_OK) return st;
+    if (!aligned(t.bias, 4)) return TERN_ERR_ALIGNMENT;
+    a.w[i] = {t.packed, t.s_row, t.rowsum, t.bias};
+  }
+  if (res && M > 1 && ldr < N) return TERN_ERR_INVALID_ARG;
+  if (N == 0 || M == 0) return TERN_OK;
+  if (!aligned(res, 4)) return TERN_ERR_ALIGNMENT;
+  a.q = q, a.s_act = s_act, a.z = z, a.res = res, a.y = y;
+  a.ldq = ldq, a.ldr = ldr, a.ldy = ldy;
+  a.N = (int32_t)N, a.K = (int32_t)K, a.ld = (int32_t)row_bytes(K), a.nch = a.ld / 16, a.M = (int32_t)M, a.act = act;
+  // (the most workgroups the call can take, on any device)
+  if (epilogue_work_items(a) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  const int cus = device_cus();
+  if (cus <= 0) return hip_fail(hipErrorNoDevice);
+  const hipError_t e = launch_epilogue(a, cus, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_embed(const int8_t* W, const float* s_row, int64_t N, int64_t K, int64_t ldw, const int32_t* ids, int64_t M,
+               float scale, float* x, int64_t ldx, hipStream_t stream) {
+  if (N < 1 || K < 1 || M < 0 || ldw < K || (M > 1 && ldx < K)) return TERN_ERR_INVALID_ARG;
+  if (!(scale > -3.4e38f && scale < 3.4e38f)) return TERN_ERR_INVALID_ARG;
+  if (N > kI32Max || K > TERN_MAX_K || embed_work_items(M, K) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  if (M == 0) return TERN_OK;
+  if (!W || !s_row || !ids || !x) return TERN_ERR_INVALID_ARG;
+  if (!aligned(s_row, 4) || !aligned(ids, 4) || !aligned(x, 4)) return TERN_ERR_ALIGNMENT;
+  const EmbedArgs a = {W, s_row, ids, x, N, K, ldw, M, ldx, scale};
+  const hipError_t e = launch_embed(a, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_qk_norm_rope(const tern_kv_batch* b, int64_t head_dim, const float* inv_freq, int64_t rot_dim,
+                      float magnitude, const float* q, int64_t ldq, int64_t q_heads, const float* q_gain, float* q_out,
+                      int64_t ldqo, const float* k, int64_t ldk, int64_t heads, const float* k_gain, float* k_out,
+                      int64_t ldko, float eps, hipStream_t stream) {
+  if (!b || b->S < 0 || b->rows < 0 || b->max_new < 0 || q_heads < 0 || heads < 0) return TERN_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return TERN_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0) return TERN_ERR_UNSUPPORTED;
+  if (!(eps > 0.0f) || eps > 3.4e38f || !(magnitude > -3.4e38f && magnitude < 3.4e38f)) return TERN_ERR_INVALID_ARG;
+  if (b->S > kI32Max || b->rows > kI32Max || b->max_new > kI32Max || q_heads > 65536 || heads > 65536)
+    return TERN_ERR_RANGE;
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.start = b->start, a.len = b->len, a.inv_freq = inv_freq;
+  a.x[0] = q, a.x[1] = k, a.gain[0] = q_gain, a.gain[1] = k_gain, a.y[0] = q_out, a.y[1] = k_out;
+  a.ldx[0] = ldq, a.ldx[1] = ldk, a.ldy[0] = ldqo, a.ldy[1] = ldko;
+  a.heads[0] = (int32_t)q_heads, a.heads[1] = (int32_t)heads;
+  a.S = (int32_t)b->S, a.rows = (int32_t)b->rows, a.max_new = (int32_t)b->max_new, a.D = (int32_t)head_dim;
+  a.R = (int32_t)rot_dim, a.eps = eps, a.magnitude = magnitude;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t width = a.heads[i] * head_dim;
+    if (a.rows > 1 && (a.ldx[i] < width || a.ldy[i] < width)) return TERN_ERR_INVALID_ARG;
+  }
+  if (a.S == 0 || a.rows == 0 || a.max_new == 0 || a.heads[0] + a.heads[1] == 0) return TERN_OK;
+  if (!a.start || !a.len || (a.R && !inv_freq)) return TERN_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    if (a.heads[i] && (!a.x[i] || !a.y[i])) return TERN_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a.start, (const void*)a.len, (const void*)inv_freq, (const void*)q, (const void*)k,
+                        (const void*)q_gain, (const void*)k_gain, (const void*)q_out, (const void*)k_out})
+    if (!aligned(p, 4)) return TERN_ERR_ALIGNMENT;
+  if (rope_work_items(a) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  const hipError_t e = launch_rope(a, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int64_t tern_kv_pool_workspace_bytes(const tern_kv_pool* pool) {
+  PoolArgs p;
+  if (check_pool(pool, &p) != TERN_OK) return 0;
+  return std::max<int64_t>(256, pool_workspace_bytes(p));
+}
+
+int tern_kv_fork(const tern_kv_pool* pool, const int32_t* len, const int32_t* src, const int32_t* dst, int64_t n,
+                 hipStream_t stream) {
+  PoolArgs p;
+  int st = check_pool(pool, &p);
+  if (st != TERN_OK) return st;
+  if (n < 0) return TERN_ERR_INVALID_ARG;
+  if (n > kMaxDispatchItems / kPoolThreads) return TERN_ERR_RANGE;
+  if (pool_empty(p) || n == 0) return TERN_OK;
+  if ((st = check_pool_buffers(p, {len, src, dst})) != TERN_OK) return st;
+  const hipError_t e = launch_kv_fork(p, len, src, dst, n, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_kv_truncate(const tern_kv_pool* pool, const int32_t* len, const int32_t* keep, hipStream_t stream) {
+  PoolArgs p;
+  int st = check_pool(pool, &p);
+  if (st != TERN_OK) return st;
+  if (pool_empty(p)) return TERN_OK;
+  if ((st = check_pool_buffers(p, {len, keep})) != TERN_OK) return st;
+  const hipError_t e = launch_kv_truncate(p, len, keep, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_kv_reserve(const tern_kv_pool* pool, const int32_t* len, const int32_t* want, int32_t* granted, int32_t* from,
+                    int32_t* to, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  PoolArgs p;
+  int st = check_pool(pool, &p);
+  if (st != TERN_OK) return st;
+  if (p.S == 0) return TERN_OK;
+  if (p.pages < 1 || p.ld_table < 1) return TERN_ERR_INVALID_ARG;
+  if ((st = check_pool_buffers(p, {len, want, granted, from, to})) != TERN_OK) return st;
+  if (!pool_workspace_ok(p, workspace, workspace_bytes)) return TERN_ERR_WORKSPACE;
+  const hipError_t e = launch_kv_reserve(p, len, want, granted, from, to, workspace, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_kv_compact(const tern_kv_pool* pool, const int32_t* len, int32_t* from, int32_t* to, int64_t moves,
+                    int32_t* live, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  PoolArgs p;
+  int st = check_pool(pool, &p);
+  if (st != TERN_OK) return st;
+  if (moves < 0) return TERN_ERR_INVALID_ARG;
+  if (moves > kI32Max) return TERN_ERR_RANGE;
+  if (p.S == 0) return TERN_OK;
+  if (p.pages < 1 || p.ld_table < 1) return TERN_ERR_INVALID_ARG;
+  if ((st = check_pool_buffers(p, {len, live})) != TERN_OK) return st;
+  if (moves > 0 && (!from || !to)) return TERN_ERR_INVALID_ARG;
+  if (!aligned(from, 4) || !aligned(to, 4)) return TERN_ERR_ALIGNMENT;
+  if (!pool_workspace_ok(p, workspace, workspace_bytes)) return TERN_ERR_WORKSPACE;
+  const hipError_t e = launch_kv_compact(p, len, from, to, moves, live, workspace, stream);
+  return e == hipSuccess ? TERN_OK : hip_fail(e);
+}
+
+int tern_kv_copy(const tern_kv_cache* dst, const tern_kv_cache* src, int64_t layers, const int32_t* from,
+                 const int32_t* to, int64_t n, hipStream_t stream) {
+  if (layers < 0 || n < 0) return TERN_ERR_INVALID_ARG;
+  if (layers == 0 || n == 0) return TERN_OK;
+  if (!dst || !src || !from || !to) return TERN_ERR_INVALID_ARG;
+  if (!aligned(from, 4) || !aligned(to, 4)) return TERN_ERR_ALIGNMENT;
+  const tern_kv_batch none = {};
+  for (int64_t l = 0; l < layers; ++l) {
+    for (const tern_kv_cache* c : {&dst[l], &src[l]}) {
+      KvArgs a;
+      const int st = check_kv(c, &none, &a);
+      if (st != TERN_OK) return st;
+      if (c->heads != src->heads || c->head_dim != src->head_dim || c->page_tokens != src->page_tokens ||
+          c->pages != (c == &dst[l] ? dst : src)->pages)
+        return TERN_ERR_INVALID_ARG;
+      if (!c->k || !c->v || !c->k_scale || !c->v_scale) return TERN_ERR_INVALID_ARG;
+      if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return TERN_ERR_ALIGNMENT;
+    }
+  }
+  CopyArgs a;
+  a.from = from, a.to = to, a.n = n;
+  a.page_bytes = src->heads * src->head_dim * src->page_tokens;
+  a.pages_from = (int32_t)src->pages, a.pages_to = (int32_t)dst->pages, a.H = (int32_t)src->heads;
+  if (kv_copy_work_items(a.page_bytes, n, std::min<int64_t>(layers, kCopyLayers)) > kMaxDispatchItems)
+    return TERN_ERR_RANGE;
+  for (int64_t l0 = 0; l0 < layers; l0 += kCopyLayers) {
+    a.layers = (int32_t)std::min<int64_t>(kCopyLayers, layers - l0);
+    for (int32_t l = 0; l < a.layers; ++l) {
+      const tern_kv_cache &s = src[l0 + l], &d = dst[l0 + l];
+      a.layer[l] = {s.k, s.v, s.k_scale, s.v_scale, d.k, d.v, d.k_scale, d.v_scale};
+    }
+    const hipError_t e = launch_kv_copy(a, stream);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  return TERN_OK;
 }
 
 int64_t tern_row_bytes5(int64_t K) { return K < 1 ? 0 : 16 * ((K + 79) / 80); }

@@ -323,4 +323,85 @@ int64_t sample_workspace_bytes(int64_t M, int64_t N);
 int64_t sample_work_items(int64_t M, int64_t N);
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s);
 
+// rows of the int8 embedding table (tern_embed.hip)
+struct EmbedArgs {
+  const int8_t* W;
+  const float* s_row;
+  const int32_t* ids;
+  float* x;
+  int64_t N, K, ldw, M, ldx;
+  float scale;
+};
+int64_t embed_work_items(int64_t M, int64_t K);
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t s);
+
+// per-head norm and rotary positions of queries and keys (tern_rope.hip);
+// part 0 is q, part 1 is k (heads 0: left out)
+struct RopeArgs {
+  const int32_t *start, *len;
+  const float* inv_freq;
+  const float* x[2];
+  const float* gain[2];
+  float* y[2];
+  int64_t ldx[2], ldy[2];
+  int32_t heads[2];
+  int32_t S, rows, max_new, D, R;
+  float eps, magnitude;
+};
+int64_t rope_work_items(const RopeArgs& a);
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
+// a ternary linear (with a gate: two of one shape) with its epilogue
+// (tern_epilogue.hip)
+struct EpilogueArgs {
+  struct {
+    const uint8_t* packed;
+    const float* s_row;
+    const int32_t* rowsum;
+    const float* bias;
+  } w[2];
+  const int8_t* q;
+  const float* s_act;
+  const int32_t* z;
+  const float* res;
+  float* y;
+  int64_t ldq, ldr, ldy;
+  int32_t N, K, ld, nch, M, act;
+};
+int64_t epilogue_work_items(const EpilogueArgs& a);
+hipError_t launch_epilogue(const EpilogueArgs& a, int cus, hipStream_t s);
+
+constexpr int kPoolThreads = 256;
+// pages of the cache: who holds them, and their contents (tern_pages.hip)
+struct PoolArgs {
+  int32_t *refs, *table;
+  int64_t pages, ld_table, S;
+  int32_t log_p;
+};
+int64_t pool_workspace_bytes(const PoolArgs& p);
+int64_t pool_work_items(const PoolArgs& p);
+hipError_t launch_kv_fork(const PoolArgs& p, const int32_t* len, const int32_t* src, const int32_t* dst, int64_t n,
+                          hipStream_t s);
+hipError_t launch_kv_truncate(const PoolArgs& p, const int32_t* len, const int32_t* keep, hipStream_t s);
+hipError_t launch_kv_reserve(const PoolArgs& p, const int32_t* len, const int32_t* want, int32_t* granted,
+                             int32_t* from, int32_t* to, void* workspace, hipStream_t s);
+hipError_t launch_kv_compact(const PoolArgs& p, const int32_t* len, int32_t* from, int32_t* to, int64_t moves,
+                             int32_t* live, void* workspace, hipStream_t s);
+// one layer of a copy: pages of page_bytes of K and of V, H scales of each
+struct CopyLayer {
+  const int8_t *k, *v;
+  const float *k_scale, *v_scale;
+  int8_t *k_to, *v_to;
+  float *k_scale_to, *v_scale_to;
+};
+constexpr int kCopyLayers = 40;  // of one launch (2.5 KB of arguments)
+struct CopyArgs {
+  CopyLayer layer[kCopyLayers];
+  const int32_t *from, *to;
+  int64_t n, page_bytes;
+  int32_t pages_from, pages_to, H, layers;
+};
+int64_t kv_copy_work_items(int64_t page_bytes, int64_t n, int64_t layers);
+hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
+
 }  // namespace tern

@@ -43,12 +43,12 @@ __device__ __forceinline__ float wave_max_f(float v) {
 //   product with k is exact, and an fp32 tail) and the Taylor series of e^r
 //   through r^7 by Horner's rule, scaled by 2^k (+inf past 88.7);
 //   silu = g / (1 + e), correctly rounded; h = silu * u.
-__device__ __forceinline__ float swiglu32(float g, float u) {
+__device__ __forceinline__ float exp32(float t) {
   constexpr double kLn2 = 0.69314718055994530942;
   constexpr float kInvLn2 = (float)(1.0 / kLn2);
   constexpr float kHead = 0.693145751953125f;
   constexpr float kTail = (float)(kLn2 - 0.693145751953125);
-  const float t = fminf(fmaxf(-g, -87.0f), 100.0f);
+  t = fminf(fmaxf(t, -87.0f), 100.0f);
   const float k = __builtin_rintf(__fmul_rn(t, kInvLn2));
   const float r = __fsub_rn(__fsub_rn(t, __fmul_rn(k, kHead)), __fmul_rn(k, kTail));
   float p = (float)(1.0 / 5040.0);
@@ -59,9 +59,10 @@ __device__ __forceinline__ float swiglu32(float g, float u) {
   p = __fadd_rn(__fmul_rn(p, r), 0.5f);
   p = __fadd_rn(__fmul_rn(p, r), 1.0f);
   p = __fadd_rn(__fmul_rn(p, r), 1.0f);
-  const float e = __builtin_ldexpf(p, (int)k);
-  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, e)), u);
+  return __builtin_ldexpf(p, (int)k);
 }
+__device__ __forceinline__ float silu32(float g) { return __fdiv_rn(g, __fadd_rn(1.0f, exp32(-g))); }
+__device__ __forceinline__ float swiglu32(float g, float u) { return __fmul_rn(silu32(g), u); }
 
 // LDS a stack kernel lends the prologue: the claim just made (two slots,
 // alternating) and the waves' partial minima and maxima.

@@ -33,6 +33,7 @@ TERN_HEAD_MAX_K = 43803
 TERN5_MAX_K = 65520
 TERN_KV_MAX_LEN = 1073741824
 TERN_SAMPLE_MAX_N = 524288
+TERN_ACT_NONE, TERN_ACT_SILU, TERN_ACT_GELU = 0, 1, 2
 
 # Every function include/tern.h declares.
 EXPORTS = (
@@ -42,6 +43,8 @@ EXPORTS = (
     "tern_quantize_weights", "tern_head_rowsum", "tern_head_gemv", "tern_row_bytes5", "tern_pack5", "tern_gemv5",
     "tern_rmsnorm_quantize", "tern_kv_append", "tern_attention_workspace_bytes", "tern_attention",
     "tern_sample_workspace_bytes", "tern_sample",
+    "tern_linear_epilogue", "tern_embed", "tern_qk_norm_rope", "tern_kv_pool_workspace_bytes", "tern_kv_fork",
+    "tern_kv_truncate", "tern_kv_reserve", "tern_kv_compact", "tern_kv_copy",
     "tern_read_probe",
     "tern_status_string", "tern_last_hip_error",
 )
@@ -93,6 +96,18 @@ class tern_kv_batch(ctypes.Structure):
     ]
 
 
+class tern_weights(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("s_row", ctypes.c_void_p), ("rowsum", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class tern_kv_pool(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int64), ("ld_table", ctypes.c_int64),
+        ("S", ctypes.c_int64), ("page_tokens", ctypes.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _handle = None
 
@@ -113,6 +128,7 @@ def _lib():
 def _declare(lib):
     i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
     cache, batch = ctypes.POINTER(tern_kv_cache), ctypes.POINTER(tern_kv_batch)
+    weights, pool = ctypes.POINTER(tern_weights), ctypes.POINTER(tern_kv_pool)
     sig = {
         "tern_row_bytes": (i64, [i64]),
         "tern_pack": (i32, [vp, i64, i64, i64, vp, vp, vp, vp]),
@@ -140,6 +156,16 @@ def _declare(lib):
         "tern_attention": (i32, [cache, batch, vp, i64, i64, f32, vp, i64, vp, i64, vp]),
         "tern_sample_workspace_bytes": (i64, [i64, i64]),
         "tern_sample": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "tern_linear_epilogue": (i32, [weights, weights, i64, i64, i64, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp]),
+        "tern_embed": (i32, [vp, vp, i64, i64, i64, vp, i64, f32, vp, i64, vp]),
+        "tern_qk_norm_rope": (i32, [batch, i64, vp, i64, f32, vp, i64, i64, vp, vp, i64, vp, i64, i64, vp, vp, i64, f32,
+                                    vp]),
+        "tern_kv_pool_workspace_bytes": (i64, [pool]),
+        "tern_kv_fork": (i32, [pool, vp, vp, vp, i64, vp]),
+        "tern_kv_truncate": (i32, [pool, vp, vp, vp]),
+        "tern_kv_reserve": (i32, [pool, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "tern_kv_compact": (i32, [pool, vp, vp, vp, i64, vp, vp, i64, vp]),
+        "tern_kv_copy": (i32, [cache, cache, i64, vp, vp, i64, vp]),
         "tern_row_bytes5": (i64, [i64]),
         "tern_pack5": (i32, [vp, i64, i64, i64, vp, vp, vp, vp]),
         "tern_gemv5": (i32, [vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
@@ -278,7 +304,7 @@ def make_kv_batch(table, ld_table, start, length, S, rows, max_new, max_len=0) -
     """The sequences of a call: device int32 tensors table (S x ld_table page
     ids), start (S + 1 row offsets) and length (S, the new rows included);
     plain data, so one batch serves the append and the attention."""
-    return tern_kv_batch(table.data_ptr(), int(ld_table), start.data_ptr(), length.data_ptr(), int(S), int(rows),
+    return tern_kv_batch(_ptr(table), int(ld_table), start.data_ptr(), length.data_ptr(), int(S), int(rows),
                          int(max_new), int(max_len))
 
 
@@ -309,6 +335,81 @@ def tern_sample(logits, M, N, ldl, temperature, u, token, workspace=None, top_k=
     _check(_lib().tern_sample(_ptr(logits), M, N, ldl, _ptr(temperature), _ptr(u), _ptr(top_k), _ptr(top_p),
                               _ptr(min_p), _ptr(token), _ptr(prob), _ptr(kept), _ptr(workspace), nbytes,
                               _stream(stream)), "tern_sample")
+
+
+def make_weights(packed, s_row, rowsum, bias=None) -> tern_weights:
+    """A linear's device tensors for tern_linear_epilogue (keep them alive)."""
+    return tern_weights(packed.data_ptr(), s_row.data_ptr(), rowsum.data_ptr(), _ptr(bias))
+
+
+def tern_linear_epilogue(w, N, K, M, q, ldq, s_act, z, y, ldy, up=None, act=TERN_ACT_NONE, res=None, ldr=0, stream=None):
+    """y = res + act(w's linear + bias) * (up's linear + bias); w and up from
+    make_weights, up and res None: left out."""
+    _check(_lib().tern_linear_epilogue(ctypes.byref(w), None if up is None else ctypes.byref(up), N, K, M, _ptr(q), ldq,
+                                       _ptr(s_act), _ptr(z), act, _ptr(res), ldr, _ptr(y), ldy, _stream(stream)),
+           "tern_linear_epilogue")
+
+
+def tern_embed(W, s_row, N, K, ldw, ids, M, x, ldx, scale=1.0, stream=None):
+    _check(_lib().tern_embed(_ptr(W), _ptr(s_row), N, K, ldw, _ptr(ids), M, scale, _ptr(x), ldx, _stream(stream)),
+           "tern_embed")
+
+
+def tern_qk_norm_rope(batch, head_dim, inv_freq, rot_dim, q=None, ldq=0, q_heads=0, q_gain=None, q_out=None, ldqo=0,
+                      k=None, ldk=0, heads=0, k_gain=None, k_out=None, ldko=0, eps=1e-6, magnitude=1.0, stream=None):
+    """Per-head norm (gain None: none) and rotary positions of q and k; q_out
+    and k_out may be q and k themselves, heads of 0 leave one out."""
+    _check(_lib().tern_qk_norm_rope(ctypes.byref(batch), head_dim, _ptr(inv_freq), rot_dim, magnitude, _ptr(q), ldq,
+                                    q_heads, _ptr(q_gain), _ptr(q_out), ldqo, _ptr(k), ldk, heads, _ptr(k_gain),
+                                    _ptr(k_out), ldko, eps, _stream(stream)), "tern_qk_norm_rope")
+
+
+def make_kv_pool(refs, table, ld_table, S, pages, page_tokens) -> tern_kv_pool:
+    """The pages under a cache: refs (pages) and table (S x ld_table), device
+    int32 tensors (keep them alive; refs of a fresh pool are zeros)."""
+    return tern_kv_pool(refs.data_ptr(), table.data_ptr(), int(pages), int(ld_table), int(S), int(page_tokens))
+
+
+def make_kv_layers(caches):
+    """The layers' caches (make_kv_cache) as tern_kv_copy takes them."""
+    return (tern_kv_cache * max(1, len(caches)))(*caches)
+
+
+def tern_kv_pool_workspace_bytes(pool) -> int:
+    return int(_lib().tern_kv_pool_workspace_bytes(ctypes.byref(pool)))
+
+
+def tern_kv_fork(pool, length, src, dst, n, stream=None):
+    _check(_lib().tern_kv_fork(ctypes.byref(pool), _ptr(length), _ptr(src), _ptr(dst), n, _stream(stream)),
+           "tern_kv_fork")
+
+
+def tern_kv_truncate(pool, length, keep, stream=None):
+    _check(_lib().tern_kv_truncate(ctypes.byref(pool), _ptr(length), _ptr(keep), _stream(stream)), "tern_kv_truncate")
+
+
+def tern_kv_reserve(pool, length, want, granted, src, dst, workspace, stream=None):
+    """src, dst: the pages to copy (tern_kv_copy's from and to), S each.
+    workspace: a device tensor of tern_kv_pool_workspace_bytes bytes."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib().tern_kv_reserve(ctypes.byref(pool), _ptr(length), _ptr(want), _ptr(granted), _ptr(src), _ptr(dst),
+                                  _ptr(workspace), nbytes, _stream(stream)), "tern_kv_reserve")
+
+
+def tern_kv_compact(pool, length, src, dst, moves, live, workspace, stream=None):
+    """src, dst: the pages to copy (tern_kv_copy's from and to), `moves` each."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib().tern_kv_compact(ctypes.byref(pool), _ptr(length), _ptr(src), _ptr(dst), moves, _ptr(live),
+                                  _ptr(workspace), nbytes, _stream(stream)), "tern_kv_compact")
+
+
+def tern_kv_copy(to_layers, from_layers, src, dst, n, stream=None):
+    """Page dst[i] of every layer of to_layers becomes page src[i] of
+    from_layers (make_kv_layers of as many caches; they may be the same)."""
+    if len(to_layers) != len(from_layers):
+        raise TernError(TERN_ERR_INVALID_ARG, "tern_kv_copy")
+    _check(_lib().tern_kv_copy(to_layers, from_layers, len(to_layers), _ptr(src), _ptr(dst), n, _stream(stream)),
+           "tern_kv_copy")
 
 
 def tern_row_bytes5(K: int) -> int:
