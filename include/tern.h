@@ -457,8 +457,7 @@ int tern_head_gemv(const int8_t* W, const float* s_row, const int32_t* rowsum, i
  *   w, up  host structures of device arrays: packed (N rows of
  *          tern_row_bytes(K) bytes, 16-byte aligned), s_row, rowsum (N each)
  *          and bias (N floats, or NULL);  up NULL: no gate;
- *   q, ldq, s_act, z, y, ldy  as for tern_gemm_smallM, any M; only the K
- *          columns of a q row are read;
+ *   q, ldq, s_act, z, y, ldy  as for tern_gemm_smallM, any M;
  *   res    device, M x N floats, row stride ldr >= N (when M > 1), or NULL; may
  *          be y itself (same address and stride: in place), and must not
  *          overlap it otherwise.

@@ -29,10 +29,11 @@ __device__ __forceinline__ i32x4 decode16(uint32_t x) {
 // silu(x) = x / (1 + e^-x), and gelu in its tanh form, x (1 + tanh(c (x + 0.044715
 // x^3))) / 2 with c = sqrt(2 / pi), as x / (1 + e^(-2 c (...))): nothing cancels
 // for negative x.
-__device__ __forceinline__ float activate(int act, float x) {
-  if (act == 0) return x;
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == 0) return x;
   float t = -x;
-  if (act == 2) {
+  if constexpr (ACT == 2) {
     const float cube = __fmul_rn(__fmul_rn(x, x), x);
     t = __fmul_rn(-1.5957691216057308f, __fadd_rn(x, __fmul_rn(0.044715f, cube)));
   }
@@ -52,23 +53,23 @@ __device__ __forceinline__ RowOps<MATS> row_ops(const EpilogueArgs& a, int64_t i
   for (int k = 0; k < MATS; ++k) {
     o.rowsum[k] = load_g(a.w[k].rowsum + i);
     o.s_row[k] = load_g(a.w[k].s_row + i);
-    o.bias[k] = a.w[k].bias ? load_g(a.w[k].bias + i) : 0.0f;
+    o.bias[k] = a.w[k].bias ? load_g(a.w[k].bias + i) : -0.0f;  // (adding -0 changes nothing)
   }
   return o;
 }
 
-// h of one output from the linears' sums
-template <int MATS>
-__device__ __forceinline__ float output(const EpilogueArgs& a, const int32_t (&sum)[MATS], const RowOps<MATS>& o,
-                                        int32_t z, float s_act) {
+// One output from the linears' sums and the residual (-0: none).
+template <int MATS, int ACT>
+__device__ __forceinline__ float output(const int32_t (&sum)[MATS], const RowOps<MATS>& o, int32_t z, float s_act,
+                                        float res) {
   float v[MATS];
 #pragma unroll
   for (int k = 0; k < MATS; ++k) {
-    v[k] = epilogue(o.s_row[k], (int32_t)((uint32_t)sum[k] - mul_zr(z, o.rowsum[k])), s_act);
-    if (a.w[k].bias) v[k] = __fadd_rn(v[k], o.bias[k]);
+    v[k] = __fadd_rn(epilogue(o.s_row[k], (int32_t)((uint32_t)sum[k] - mul_zr(z, o.rowsum[k])), s_act), o.bias[k]);
   }
-  const float h = activate(a.act, v[0]);
-  return MATS == 2 ? __fmul_rn(h, v[MATS - 1]) : h;
+  float h = activate<ACT>(v[0]);
+  if constexpr (MATS == 2) h = __fmul_rn(h, v[1]);
+  return __fadd_rn(res, h);
 }
 
 // 16 activations from column j on, zeros past K.
@@ -87,10 +88,10 @@ __device__ __forceinline__ i32x4 load_q16(const int8_t* q, int64_t j, int K) {
 // (r, g) loads the whole 16-byte chunk 4 i + g of row r, four operands of 64
 // weights for four instructions; the tokens' operands are the same columns of
 // token r, loaded as they lie (any order of K serves if both sides have it).
-constexpr int RB = 2;
+constexpr int RB = 2, kRowsT = 512;
 constexpr int kRedStride = 68;  // of 64 lanes' values of one register, off each other's banks
 
-template <int W, int TB, int MATS>
+template <int W, int TB, int MATS, int ACT>
 __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, int row_tiles) {
   __shared__ int32_t red[W][MATS * RB * 4 * kRedStride];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -161,8 +162,8 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
           sum[k] += red[i][((k * RB + row / 16) * 4 + row % 4) * kRedStride + 16 * (row % 16 / 4) + tok];
       }
       const int64_t i = row0 + row;
-      const float hid = output<MATS>(a, sum, row_ops<MATS>(a, i), load_g(a.z + m), load_g(a.s_act + m));
-      store_g(a.y + m * a.ldy + i, a.res ? __fadd_rn(load_g(a.res + m * a.ldr + i), hid) : hid);
+      const float res = a.res ? load_g(a.res + m * a.ldr + i) : -0.0f;
+      store_g(a.y + m * a.ldy + i, output<MATS, ACT>(sum, row_ops<MATS>(a, i), load_g(a.z + m), load_g(a.s_act + m), res));
     }
   }
 }
@@ -205,7 +206,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base,
 // every bank once
 __device__ __forceinline__ int piece_swz(int t) { return ((t >> 1) & 7) ^ ((t & 1) << 2); }
 
-template <int MATS, typename S>
+template <int MATS, int ACT, typename S>
 __global__ __launch_bounds__(64 * S::WAVES) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[S::LDS];
@@ -241,8 +242,8 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
     qrow[i] = t < toks ? (uint32_t)t * (uint32_t)a.ldq : kDropOffset;
     qcol[i] = 16 * ((lane & 7) ^ piece_swz(t)) + 128 * ks;
   }
-  auto issue = [&](int J) {
-    uint8_t* dst = lds + (J % S::RING) * S::SLOT + ks * S::SUB + 1024 * S::DMA * rg;
+  auto issue = [&](int J, int slot) {
+    uint8_t* dst = lds + slot * S::SLOT + ks * S::SUB + 1024 * S::DMA * rg;
 #pragma unroll
     for (int i = 0; i < S::DMA; ++i) {
       const uint32_t col = qcol[i] + 128u * S::KS * (uint32_t)J;
@@ -264,10 +265,9 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
   uint32_t tofs[4];  // this lane's piece for operand d of a stage
 #pragma unroll
   for (int d = 0; d < 4; ++d) tofs[d] = ks * S::SUB + r * 128 + 16 * ((4 * h + d) ^ piece_swz(r));
-  auto load_tok = [&](i32x4 (&x)[TB], int J, int d) {
-    const uint8_t* src = lds + (J % S::RING) * S::SLOT + tofs[d];
+  auto load_tok = [&](i32x4 (&x)[TB], int slot, int d) {
 #pragma unroll
-    for (int t = 0; t < TB; ++t) x[t] = *reinterpret_cast<const i32x4*>(src + 4096 * t);
+    for (int t = 0; t < TB; ++t) x[t] = *reinterpret_cast<const i32x4*>(lds + tofs[d] + (slot * S::SLOT + 4096 * t));
   };
   i32x16 acc[2][TB];
 #pragma unroll
@@ -284,40 +284,44 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
 #pragma unroll
       for (int t = 0; t < TB; ++t)
         acc[k][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wa[set][k], tok[set][t], acc[k][t], 0, 0, 0);
+    // issue order: the first MFMA, the next operand's LDS reads, then each MFMA
+    // followed by a share of the next operand's decode
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+    __builtin_amdgcn_sched_group_barrier(0x100, TB, 0);  // LDS reads
+    __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 4 : 7, 0);  // VALU
 #pragma unroll
-    for (int i = 0; i < 2 * TB; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // MFMA
-      if (i < TB) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 4 : 7, 0);  // VALU
+    for (int i = 1; i < 2 * TB; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 4 : 7, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
-  for (int J = 0; J < S::RING; ++J) issue(J);
+  for (int J = 0; J < S::RING; ++J) issue(J, J);
   load_w(cur, 0);
   wait_vm<0>();
   asm volatile("s_barrier" ::: "memory");
   load_tok(tok[0], 0, 0);
 #pragma unroll
   for (int k = 0; k < 2; ++k) wa[0][k] = decode16(cur[0][k][0]);
-  for (int c = 0; 2 * c < nst; ++c) {
-    load_w(nxt, c + 1);
+  // two stages (J, J + 1) in slots `slot` and slot + 1
+  auto two_stages = [&](int J, int slot) {
+    load_w(nxt, J / 2 + 1);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const int J = 2 * c + st;
 #pragma unroll
       for (int d = 0; d < 3; ++d) {
-        load_tok(tok[(d + 1) & 1], J, d + 1);
+        load_tok(tok[(d + 1) & 1], slot + st, d + 1);
 #pragma unroll
         for (int k = 0; k < 2; ++k) wa[(d + 1) & 1][k] = decode16(cur[st][k][d + 1]);
         multiply(d & 1);
       }
-      // this wave is done with slot J; stage J + 1 has landed, mine and then everybody's
+      // this wave is done with its slot; stage J + st + 1 has landed, mine and then everybody's
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       wait_vm<(S::RING - 2) * S::DMA + S::WL>();
       asm volatile("s_barrier" ::: "memory");
-      issue(J + S::RING);
-      load_tok(tok[0], J + 1, 0);
+      issue(J + st + S::RING, slot + st);
+      load_tok(tok[0], (slot + st + 1) % S::RING, 0);
 #pragma unroll
       for (int k = 0; k < 2; ++k) wa[0][k] = decode16(st == 0 ? cur[1][k][0] : nxt[0][k][0]);
       multiply(1);
@@ -326,133 +330,200 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
     for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int k = 0; k < 2; ++k) cur[st][k] = nxt[st][k];
+  };
+  static_assert(S::RING == 4, "slots of the loop below");
+  __builtin_amdgcn_s_setprio(2);
+  for (int J = 0; J < nst; J += 4) {
+    two_stages(J, 0);
+    two_stages(J + 2, 2);
   }
 
-  // lane (r, h), block k, register 4 q + v: row rows[k] + 8 q + 4 h + v, token 32 t + r.
-  // With KS > 1 the ks waves' sums meet in LDS, and each finishes the registers
-  // of some q.
-  wait_vm<0>();  // (the ring's last DMAs: they must not outlive the workgroup)
-  if constexpr (S::KS > 1) {
-    __syncthreads();
-    i32x4* mine = reinterpret_cast<i32x4*>(lds) + w * TB * 512 + lane;
+  // Lane (r, h), block k, register 4 q + v hold row rows[k] + 8 q + 4 h + v of token
+  // 32 t + r.  Stored from there, an instruction would write 32 pieces of 32
+  // bytes; so the sums go through LDS (one token block at a time, with KS > 1 all
+  // of them, where the ks waves' meet) to lanes that hold four rows each of the
+  // same token side by side: whole lines of y and of the residual.  The four rows
+  // 4 e .. of a block of 32 lie in register group q = e / 2 of half h = e % 2, and
+  // there at token r ^ e, off each other's banks.
+  constexpr int TC = S::KS > 1 ? TB : 1;       // token blocks in LDS at once
+  constexpr int KB = MATS == 2 ? 1 : 2;        // blocks of 32 rows of y
+  constexpr int PER = 8 / KB;                  // tokens of an instruction
+  constexpr int ITEMS = 32 / PER / (S::KS > 1 ? 2 : 1);  // instructions of a wave and token block
+  static_assert(S::KS == 1 || S::KS * ITEMS == TB * 32 / PER, "share of the ks waves");
+  i32x4* sums = reinterpret_cast<i32x4*>(lds);
+  auto put = [&](int t) {
+    i32x4* mine = sums + (w * TC + (S::KS > 1 ? t : 0)) * 512;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int t = 0; t < TB; ++t)
+      for (int q = 0; q < 4; ++q)
+        mine[(k * 4 + q) * 64 + 32 * h + (r ^ (2 * q + h))] =
+            i32x4{acc[k][t][4 * q], acc[k][t][4 * q + 1], acc[k][t][4 * q + 2], acc[k][t][4 * q + 3]};
+  };
+  const int e = lane & 7, kb = KB == 2 ? (lane >> 3) & 1 : 0;
+  const int i0 = rows[kb] + 4 * e;
+  const bool whole = i0 + 3 < a.N;
+  const bool yvec = whole && (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  const bool rvec = whole && (a.ldr & 3) == 0 && (reinterpret_cast<uintptr_t>(a.res) & 15) == 0;
+  RowOps<MATS> ops[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mine[((k * TB + t) * 4 + q) * 64] =
-              i32x4{acc[k][t][4 * q], acc[k][t][4 * q + 1], acc[k][t][4 * q + 2], acc[k][t][4 * q + 3]};
-    __syncthreads();
-  }
-  const bool yvec = (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-  const bool rvec = (a.ldr & 3) == 0 && (reinterpret_cast<uintptr_t>(a.res) & 15) == 0;
-  int32_t z[TB];
-  float s_act[TB];
+  for (int v = 0; v < 4; ++v) ops[v] = row_ops<MATS>(a, min(i0 + v, a.N - 1));
+  // token block t, instructions item0 .. of it
+  auto finish = [&](int t, int item0) {
+    int32_t z[ITEMS];
+    float s_act[ITEMS];
+    f32x4 res[ITEMS];
 #pragma unroll
-  for (int t = 0; t < TB; ++t) {
-    const int64_t m = min(tok0 + 32 * t + r, (int64_t)a.M - 1);
-    z[t] = load_g(a.z + m);
-    s_act[t] = load_g(a.s_act + m);
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (S::KS > 1 && q % S::KS != ks) continue;
-#pragma unroll
-    for (int k = 0; k < (MATS == 2 ? 1 : 2); ++k) {
-      const int i0 = rows[k] + 8 * q + 4 * h;
-      if (i0 >= a.N) continue;
-      RowOps<MATS> ops[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) ops[v] = row_ops<MATS>(a, min(i0 + v, a.N - 1));
-      const bool whole = i0 + 3 < a.N;
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const int64_t m = tok0 + 32 * t + r;
-        if (m >= a.M) continue;
-        i32x4 sum[MATS];
-#pragma unroll
-        for (int e = 0; e < MATS; ++e) {
-          const int blk = MATS == 2 ? e : k;
-          if constexpr (S::KS > 1) {
-            sum[e] = i32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < S::KS; ++i)
-              sum[e] += reinterpret_cast<const i32x4*>(lds)[(i * S::RG + rg) * TB * 512 +
-                                                            ((blk * TB + t) * 4 + q) * 64 + lane];
-          } else {
-            sum[e] = i32x4{acc[blk][t][4 * q], acc[blk][t][4 * q + 1], acc[blk][t][4 * q + 2], acc[blk][t][4 * q + 3]};
-          }
-        }
-        f32x4 res = {0.0f, 0.0f, 0.0f, 0.0f}, o;
-        if (a.res) {
-          const float* p = a.res + m * a.ldr + i0;
-          if (rvec && whole) {
-            res = load_g(reinterpret_cast<const f32x4*>(p));
-          } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (i0 + v < a.N) res[v] = load_g(p + v);
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          int32_t one[MATS];
-#pragma unroll
-          for (int e = 0; e < MATS; ++e) one[e] = sum[e][v];
-          o[v] = output<MATS>(a, one, ops[v], z[t], s_act[t]);
-          if (a.res) o[v] = __fadd_rn(res[v], o[v]);
-        }
-        float* y = a.y + m * a.ldy + i0;
-        if (yvec && whole) {
-          store_g(reinterpret_cast<f32x4*>(y), o);
+    for (int i = 0; i < ITEMS; ++i) {
+      const int64_t m = tok0 + 32 * t + PER * (item0 + i) + lane / (64 / PER);
+      const int64_t mc = min(m, (int64_t)a.M - 1);
+      z[i] = load_g(a.z + mc);
+      s_act[i] = load_g(a.s_act + mc);
+      res[i] = f32x4{-0.0f, -0.0f, -0.0f, -0.0f};
+      if (a.res) {
+        const float* p = a.res + mc * a.ldr;
+        if (rvec) {
+          res[i] = load_g(reinterpret_cast<const f32x4*>(p + i0));
         } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (i0 + v < a.N) store_g(y + v, o[v]);
+          for (int v = 0; v < 4; ++v) res[i][v] = load_g(p + min(i0 + v, a.N - 1));
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int token = PER * (item0 + i) + lane / (64 / PER);
+      const int64_t m = tok0 + 32 * t + token;
+      i32x4 sum[MATS];
+#pragma unroll
+      for (int n = 0; n < MATS; ++n) {
+        sum[n] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < S::KS; ++p)
+          sum[n] += sums[((p * S::RG + rg) * TC + (S::KS > 1 ? t : 0)) * 512 + ((MATS == 2 ? n : kb) * 4 + e / 2) * 64 +
+                         32 * (e & 1) + (token ^ e)];
+      }
+      f32x4 o;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        int32_t one[MATS];
+#pragma unroll
+        for (int n = 0; n < MATS; ++n) one[n] = sum[n][v];
+        o[v] = output<MATS, ACT>(one, ops[v], z[i], s_act[i], res[i][v]);
+      }
+      if (m >= a.M) continue;
+      float* y = a.y + m * a.ldy + i0;
+      if (yvec) {
+        __builtin_nontemporal_store(o, (f32x4 __attribute__((address_space(1)))*)(y));
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (i0 + v < a.N) store_g(y + v, o[v]);
+      }
+    }
+  };
+  __builtin_amdgcn_s_setprio(0);
+  wait_vm<0>();  // the ring's last DMAs, mine and then everybody's
+  __syncthreads();
+  if constexpr (S::KS > 1) {
+#pragma unroll
+    for (int t = 0; t < TB; ++t) put(t);
+    __syncthreads();
+    finish(ks * TB / S::KS, ks % 2 * ITEMS);
+  } else {
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      put(t);
+      finish(t, 0);
     }
   }
 }
 
-template <int MATS, typename S>
+template <int MATS, int ACT, typename S>
 hipError_t launch_tile(const EpilogueArgs& a, hipStream_t s) {
   const int row_tiles = (a.N + S::ROWS - 1) / S::ROWS, tok_tiles = (int)(((int64_t)a.M + S::TOK - 1) / S::TOK);
-  hipLaunchKernelGGL((epilogue_tile_kernel<MATS, S>), dim3((unsigned)((int64_t)row_tiles * tok_tiles)),
+  hipLaunchKernelGGL((epilogue_tile_kernel<MATS, ACT, S>), dim3((unsigned)((int64_t)row_tiles * tok_tiles)),
                      dim3(64 * S::WAVES), 0, s, a, row_tiles, tok_tiles);
   return hipGetLastError();
 }
 
-template <int TB, int MATS>
+template <int TB, int MATS, int ACT>
 hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
-  constexpr int W = 8;
+  constexpr int W = kRowsT / 64;
   const int64_t row_tiles = (a.N + 16 * RB - 1) / (16 * RB), tok_tiles = ((int64_t)a.M + 16 * TB - 1) / (16 * TB);
-  hipLaunchKernelGGL((epilogue_rows_kernel<W, TB, MATS>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s,
+  hipLaunchKernelGGL((epilogue_rows_kernel<W, TB, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s,
                      a, (int)row_tiles);
   return hipGetLastError();
 }
 
+// The shapes of a call's workgroups, from few tokens to many: rows kernels of 16
+// and 32 tokens, tiles of 128 x 64 (rows of both matrices x tokens; K split four
+// ways), 256 x 64 and 256 x 128.
+enum Shape { ROWS_16, ROWS_32, TILE_SPLIT, TILE_64, TILE_128, SHAPES };
 template <int MATS>
-hipError_t launch_mats(const EpilogueArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_rows<1, MATS>(a, s);
-  if (a.M <= 32) return launch_rows<2, MATS>(a, s);
-  // (the tiles' offsets within a token block are 32-bit)
-  if (a.M <= 64 || 128 * a.ldq >= (1ll << 31)) return launch_rows<4, MATS>(a, s);
-  if ((int64_t)((a.N * MATS + 255) / 256) * ((a.M + 127) / 128) >= 256) return launch_tile<MATS, Tile<MATS, 4, 1, 4, 4>>(a, s);
-  return launch_tile<MATS, Tile<MATS, 2, 4, 2, 4>>(a, s);
+using TileSplit = Tile<MATS, 2, 4, 2, 4>;
+template <int MATS>
+using Tile64 = Tile<MATS, 4, 1, 2, 4>;
+template <int MATS>
+using Tile128 = Tile<MATS, 4, 1, 4, 4>;
+
+int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
+  static constexpr int kRows[SHAPES] = {16 * RB, 16 * RB, 128, 256, 256}, kTokens[SHAPES] = {16, 32, 64, 64, 128};
+  const int64_t mats = a.w[1].packed ? 2 : 1;
+  const int64_t rows = shape <= ROWS_32 ? kRows[shape] : kRows[shape] / mats;
+  return ((a.N + rows - 1) / rows) * (((int64_t)a.M + kTokens[shape] - 1) / kTokens[shape]);
+}
+
+// The shape with the least estimated time: a start, and for each workgroup that a
+// CU gets in turn a time proportional to K, as measured over M = 16 .. 1,024 (us
+// for 4,096 columns; without a gate, with one).  Both sides of some borders, gate
+// and up of 12,288 x 4,096: 32 tokens in rows of 16, of 32 and split tiles 15.7,
+// 16.2, 16.0; 64: 27.1, 22.1, 17.4 and 20.9 in tiles of 64; 128: 47, 38.5, 30.2,
+// 22.1; 1,024: tiles of 64 113, of 128 101.  4,096 x 12,288 with a residual: 64
+// tokens in rows of 32 17.6, split 30.0; 256: 56.9, 30.8, tiles of 64 44.5; 1,024:
+// split 68.7, of 64 55.2, of 128 75.8.
+int pick_shape(const EpilogueArgs& a, int cus) {
+  static constexpr double kStart[SHAPES] = {3, 3, 6, 6, 6};
+  static constexpr double kTime[2][SHAPES] = {{3.0, 5.4, 10, 14, 23}, {4.0, 6.0, 14.5, 19, 33}};
+  // (one block of tokens: more in flight do not read fewer weights)
+  if (a.M <= 16) return ROWS_16;
+  const int gated = a.w[1].packed != nullptr;
+  int best = ROWS_16;
+  double least = 0;
+  for (int s = ROWS_16; s < SHAPES; ++s) {
+    // (the tiles' offsets inside a token block are 32-bit)
+    if (s >= TILE_SPLIT && 128 * a.ldq >= (1ll << 31)) break;
+    const double turns = (double)((shape_workgroups(s, a) + cus - 1) / cus);
+    const double t = kStart[s] + turns * kTime[gated][s] * a.K / 4096;
+    if (s == ROWS_16 || t < least) best = s, least = t;
+  }
+  return best;
+}
+
+template <int MATS, int ACT>
+hipError_t launch_act(const EpilogueArgs& a, int cus, hipStream_t s) {
+  switch (pick_shape(a, cus)) {
+    case ROWS_16: return launch_rows<1, MATS, ACT>(a, s);
+    case ROWS_32: return launch_rows<2, MATS, ACT>(a, s);
+    case TILE_SPLIT: return launch_tile<MATS, ACT, TileSplit<MATS>>(a, s);
+    case TILE_64: return launch_tile<MATS, ACT, Tile64<MATS>>(a, s);
+    default: return launch_tile<MATS, ACT, Tile128<MATS>>(a, s);
+  }
+}
+
+template <int MATS>
+hipError_t launch_mats(const EpilogueArgs& a, int cus, hipStream_t s) {
+  if (a.act == 0) return launch_act<MATS, 0>(a, cus, s);
+  return a.act == 1 ? launch_act<MATS, 1>(a, cus, s) : launch_act<MATS, 2>(a, cus, s);
 }
 
 }  // namespace
 
-int64_t epilogue_work_items(const EpilogueArgs& a) {
-  const int64_t row_tiles = ((int64_t)a.N + 16 * RB - 1) / (16 * RB), tb = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
-  return mul_sat(mul_sat(row_tiles, ((int64_t)a.M + tb - 1) / tb), 512);
-}
+// (the smallest workgroups' launch)
+int64_t epilogue_work_items(const EpilogueArgs& a) { return mul_sat(shape_workgroups(ROWS_16, a), kRowsT); }
 
 hipError_t launch_epilogue(const EpilogueArgs& a, int cus, hipStream_t s) {
-  (void)cus;
-  return a.w[1].packed ? launch_mats<2>(a, s) : launch_mats<1>(a, s);
+  return a.w[1].packed ? launch_mats<2>(a, cus, s) : launch_mats<1>(a, cus, s);
 }
 
 }  // namespace tern

@@ -109,6 +109,36 @@ def test_model_shapes(M):
     run(M, 4096, 12288, res="in place", rows=pick[:60:3] // 3)
 
 
+@pytest.mark.parametrize("M,N,K,gate", [
+    (300, 4001, 1019, False), (601, 2500, 1030, False), (300, 2501, 2049, True), (1001, 1003, 2050, True),
+    (1000, 2497, 1019, False), (577, 4000, 321, False), (600, 2500, 1019, True), (290, 4000, 2048, True),
+    (2050, 6001, 700, False), (3000, 4100, 130, False), (2100, 6145, 65, False), (1500, 9001, 577, False),
+    (1000, 2501, 1019, True), (1001, 4003, 321, True), (600, 4000, 1019, True), (2000, 4003, 130, True)])
+def test_large_odd_sizes(M, N, K, gate):
+    """Every shape of workgroup at sizes that none divides (in fours: tiles with
+    K split, of 64 tokens, of 128): the edges of its tiles."""
+    pick = np.unique(np.r_[0:70, 120:136, 250:262, N // 2: N // 2 + 30, N - 140: N])
+    run(M, N, K, gate=gate, act="silu", res="apart" if K % 2 else None, bias=K % 2 == 0, extra=K % 4, rows=pick)
+
+
+def test_strides_past_32_bits():
+    """Rows of activations so far apart that a block of them passes 2^31 bytes,
+    and outputs behind 2^31 elements."""
+    M, N, K = 100, 64, 128
+    rng = np.random.default_rng(9)
+    side = Side(rng, N, K, False)
+    q = to_dev(rng.integers(-128, 128, (M, K)).astype(np.int8))
+    s, z = to_dev(rng.uniform(0.01, 0.03, M).astype(np.float32)), torch.zeros(M, dtype=torch.int32, device=DEV)
+    want = torch.empty((M, N), device=DEV)
+    tern.tern_linear_epilogue(side.dev, N, K, M, q, K, s, z, want, N)
+    ld = 24 << 20
+    far_q = torch.empty(M * ld, dtype=torch.int8, device=DEV)
+    far_y = torch.empty(M * ld, device=DEV)
+    far_q.view(M, ld)[:, :K] = q
+    tern.tern_linear_epilogue(side.dev, N, K, M, far_q, ld, s, z, far_y, ld)
+    assert torch.equal(far_y.view(M, ld)[:, :N], want)
+
+
 def test_equals_the_chain_of_calls():
     """The gated linear gives what the two linears and the stack launch's gate
     give: its codes, scale and zero point, bit for bit."""
