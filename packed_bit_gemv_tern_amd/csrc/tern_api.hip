@@ -496,8 +496,7 @@ int tern_linear_epilogue(const tern_weights* w, const tern_weights* up, int64_t 
   a.q = q, a.s_act = s_act, a.z = z, a.res = res, a.y = y;
   a.ldq = ldq, a.ldr = ldr, a.ldy = ldy;
   a.N = (int32_t)N, a.K = (int32_t)K, a.ld = (int32_t)row_bytes(K), a.nch = a.ld / 16, a.M = (int32_t)M, a.act = act;
-  // (the most workgroups the call can take, on any device)
-  if (epilogue_work_items(a) > kMaxDispatchItems) return TERN_ERR_RANGE;
+  if (!epilogue_takes(a)) return TERN_ERR_RANGE;
   const int cus = device_cus();
   if (cus <= 0) return hip_fail(hipErrorNoDevice);
   const hipError_t e = launch_epilogue(a, cus, stream);

@@ -16,7 +16,6 @@ namespace tern {
 namespace {
 
 constexpr uint32_t kCodeTable = 0x000100FFu;  // code byte 0, 1, 2 -> -1, 0, +1
-constexpr uint32_t kZeroCodes = 0x55555555u;
 
 __device__ __forceinline__ i32x4 decode16(uint32_t x) {
   i32x4 b;
@@ -72,6 +71,13 @@ __device__ __forceinline__ float output(const int32_t (&sum)[MATS], const RowOps
   return __fadd_rn(res, h);
 }
 
+// buffer_rsrc of values that are the same in every lane, in scalar registers.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+  return buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
+}
+
 // 16 activations from column j on, zeros past K.
 __device__ __forceinline__ i32x4 load_q16(const int8_t* q, int64_t j, int K) {
   if (j + 16 <= K) return __builtin_bit_cast(i32x4, load16(q + j));
@@ -82,28 +88,40 @@ __device__ __forceinline__ i32x4 load_q16(const int8_t* q, int64_t j, int K) {
   return v;
 }
 
+// ---- few tokens: rows --------------------------------------------------------
+
 // RB blocks of 16 rows (of each matrix) and TB blocks of 16 tokens to a
 // workgroup; its W waves take 256 columns at a time in turn, and their exact
 // int32 sums meet in LDS.  v_mfma_i32_16x16x64_i8 with the weights as A: lane
 // (r, g) loads the whole 16-byte chunk 4 i + g of row r, four operands of 64
 // weights for four instructions; the tokens' operands are the same columns of
 // token r, loaded as they lie (any order of K serves if both sides have it).
-constexpr int RB = 2, kRowsT = 512;
+// The weights of the next step are asked for behind this step's activations:
+// loads return in order, so before them they would be waited for with them.
+// Bound by the weights' bytes for one token, by the activations that every
+// workgroup reads from the L2 for sixteen (gate and up of 12,288 x 4,096, weights
+// from memory, 25 MB: 8.5, 10.3 and 12.0 us for 1, 8 and 16 tokens, of which 2.3
+// are the launch; 32 rows to a workgroup 9.4, 10.0, 11.7).  Measured and not
+// kept: 128 bytes of a row to a lane's four (8.8), weights four steps ahead
+// (10.3), chunks transposed across the lanes so that a token's operands are 64
+// contiguous bytes (8.2).
 constexpr int kRedStride = 68;  // of 64 lanes' values of one register, off each other's banks
 
-template <int W, int TB, int MATS, int ACT>
+template <int W, int RB, int TB, int MATS, int ACT>
 __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, int row_tiles) {
   __shared__ int32_t red[W][MATS * RB * 4 * kRedStride];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int row0 = (blockIdx.x % row_tiles) * 16 * RB;
   const int64_t tok0 = (int64_t)(blockIdx.x / row_tiles) * 16 * TB;
-  const uint8_t* wsrc[MATS][RB];
-  const int8_t* qsrc[TB];
+  // (rows and chunks past the matrix give zeros or other rows' weights: they meet
+  // zero activations, or are not stored)
+  __amdgpu_buffer_rsrc_t wres[MATS];
+  const int here = min(a.N - row0, 16 * RB);
 #pragma unroll
   for (int k = 0; k < MATS; ++k)
-#pragma unroll
-    for (int b = 0; b < RB; ++b) wsrc[k][b] = a.w[k].packed + (int64_t)min(row0 + 16 * b + r, a.N - 1) * a.ld;
+    wres[k] = uniform_rsrc(a.w[k].packed + (int64_t)row0 * a.ld, (uint32_t)here * (uint32_t)a.ld);
+  const int8_t* qsrc[TB];
 #pragma unroll
   for (int t = 0; t < TB; ++t) qsrc[t] = a.q + min(tok0 + 16 * t + r, (int64_t)a.M - 1) * a.ldq;
   i32x4 acc[MATS][RB][TB];
@@ -113,30 +131,50 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int t = 0; t < TB; ++t) acc[k][b][t] = i32x4{0, 0, 0, 0};
-  for (int c0 = 4 * w; c0 < a.nch; c0 += 4 * W) {
-    const int c = c0 + g;
-    u32x4 wd[MATS][RB];
-    i32x4 qa[TB][4];
+  auto load_w = [&](u32x4 (&x)[MATS][RB], int c0) {
 #pragma unroll
     for (int k = 0; k < MATS; ++k)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
-        wd[k][b] = c < a.nch ? load16(wsrc[k][b] + 16ll * c) : u32x4{kZeroCodes, kZeroCodes, kZeroCodes, kZeroCodes};
+        x[k][b] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       wres[k],
+                       (int)(c0 + g < a.nch ? (uint32_t)(16 * b + r) * (uint32_t)a.ld + 16u * (c0 + g) : kDropOffset),
+                       0, 0));
+  };
+  u32x4 cur[MATS][RB], nxt[MATS][RB];
+  load_w(cur, 4 * w);
+  for (int c0 = 4 * w; c0 < a.nch; c0 += 4 * W) {
+    i32x4 qa[TB][4];
+    const int64_t j = 64ll * (c0 + g);
+    if (64 * (c0 + 4) <= a.K) {
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
+      for (int t = 0; t < TB; ++t)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) qa[t][d] = load_q16(qsrc[t], 64ll * c + 16 * d, a.K);
+        for (int d = 0; d < 4; ++d) qa[t][d] = __builtin_bit_cast(i32x4, load16(qsrc[t] + j + 16 * d));
+    } else {
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) qa[t][d] = load_q16(qsrc[t], j + 16 * d, a.K);
+    }
+    load_w(nxt, c0 + 4 * W);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < MATS; ++k)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const i32x4 wb = decode16(wd[k][b][d]);
+          const i32x4 wb = decode16(cur[k][b][d]);
 #pragma unroll
           for (int t = 0; t < TB; ++t)
             acc[k][b][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb, qa[t][d], acc[k][b][t], 0, 0, 0);
         }
+#pragma unroll
+    for (int k = 0; k < MATS; ++k)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) cur[k][b] = nxt[k][b];
   }
   // lane (r, g), register v: row 16 b + 4 g + v, token 16 t + r
 #pragma unroll
@@ -192,13 +230,6 @@ struct Tile {
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
-}
-
-// buffer_rsrc of values that are the same in every lane, in scalar registers.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t p = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
-  return buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 
 // swizzle of a token's eight 16-byte pieces of a stage: piece p sits at p ^
@@ -447,19 +478,19 @@ hipError_t launch_tile(const EpilogueArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int TB, int MATS, int ACT>
+template <int W, int RB, int TB, int MATS, int ACT>
 hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
-  constexpr int W = kRowsT / 64;
   const int64_t row_tiles = (a.N + 16 * RB - 1) / (16 * RB), tok_tiles = ((int64_t)a.M + 16 * TB - 1) / (16 * TB);
-  hipLaunchKernelGGL((epilogue_rows_kernel<W, TB, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s,
+  hipLaunchKernelGGL((epilogue_rows_kernel<W, RB, TB, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s,
                      a, (int)row_tiles);
   return hipGetLastError();
 }
 
-// The shapes of a call's workgroups, from few tokens to many: rows kernels of 16
-// and 32 tokens, tiles of 128 x 64 (rows of both matrices x tokens; K split four
-// ways), 256 x 64 and 256 x 128.
-enum Shape { ROWS_16, ROWS_32, TILE_SPLIT, TILE_64, TILE_128, SHAPES };
+// The shapes of a call's workgroups, rows (of both matrices together in the tiles,
+// of each in the rows kernels) x tokens: ROWS_WIDE for few tokens and very many
+// rows, then from few tokens to many.
+enum Shape { ROWS_16, ROWS_32, TILE_SPLIT, TILE_64, TILE_128, ROWS_WIDE, SHAPES };
+constexpr int kShapeRows[SHAPES] = {16, 32, 128, 256, 256, 64}, kShapeTokens[SHAPES] = {16, 32, 64, 64, 128, 16};
 template <int MATS>
 using TileSplit = Tile<MATS, 2, 4, 2, 4>;
 template <int MATS>
@@ -468,46 +499,65 @@ template <int MATS>
 using Tile128 = Tile<MATS, 4, 1, 4, 4>;
 
 int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
-  static constexpr int kRows[SHAPES] = {16 * RB, 16 * RB, 128, 256, 256}, kTokens[SHAPES] = {16, 32, 64, 64, 128};
-  const int64_t mats = a.w[1].packed ? 2 : 1;
-  const int64_t rows = shape <= ROWS_32 ? kRows[shape] : kRows[shape] / mats;
-  return ((a.N + rows - 1) / rows) * (((int64_t)a.M + kTokens[shape] - 1) / kTokens[shape]);
+  const bool tile = shape >= TILE_SPLIT && shape <= TILE_128;
+  const int64_t rows = kShapeRows[shape] / (tile && a.w[1].packed ? 2 : 1), tokens = kShapeTokens[shape];
+  return ((a.N + rows - 1) / rows) * ((a.M + tokens - 1) / tokens);
 }
 
-// The shape with the least estimated time: a start, and for each workgroup that a
-// CU gets in turn a time proportional to K, as measured over M = 16 .. 1,024 (us
-// for 4,096 columns; without a gate, with one).  Both sides of some borders, gate
-// and up of 12,288 x 4,096: 32 tokens in rows of 16, of 32 and split tiles 15.7,
-// 16.2, 16.0; 64: 27.1, 22.1, 17.4 and 20.9 in tiles of 64; 128: 47, 38.5, 30.2,
-// 22.1; 1,024: tiles of 64 113, of 128 101.  4,096 x 12,288 with a residual: 64
-// tokens in rows of 32 17.6, split 30.0; 256: 56.9, 30.8, tiles of 64 44.5; 1,024:
-// split 68.7, of 64 55.2, of 128 75.8.
-int pick_shape(const EpilogueArgs& a, int cus) {
-  static constexpr double kStart[SHAPES] = {3, 3, 6, 6, 6};
-  static constexpr double kTime[2][SHAPES] = {{3.0, 5.4, 10, 14, 23}, {4.0, 6.0, 14.5, 19, 33}};
-  // (one block of tokens: more in flight do not read fewer weights)
-  if (a.M <= 16) return ROWS_16;
+// Whether a launch of the shape can count its threads (512 only where workgroups
+// are few) and, for tiles, reach a token block's rows by 32-bit offsets.
+bool shape_takes(int shape, const EpilogueArgs& a) {
+  if (shape >= TILE_SPLIT && shape <= TILE_128 && 128 * a.ldq >= (1ll << 31)) return false;
+  return shape_workgroups(shape, a) <= kMaxDispatchItems / 256;
+}
+
+// Up to 16 tokens take rows: 16 to a workgroup, for the most waves in flight, or
+// 64 from 16 such workgroups per CU on, where the activations that each reads
+// are what counts (151,936 x 4,096: 46 and 38 us for one token, 90 and 49 for 16;
+// gate and up of 12,288 x 12,288, six per CU: 21 and 27, 31 and 30).  More tokens
+// take the shape with the least estimated time: a start, and for each workgroup
+// that a CU gets in turn a time with a part proportional to K, as measured over
+// M = 16 .. 512 and K = 1,024 .. 12,288 (us, for 4,096 columns; without a gate,
+// with one).  Both sides of some borders, gate and up of 12,288 x 4,096: 32 tokens
+// in rows of 16, of 32 and split tiles 20.6, 16.9, 16.5; 64: 37, 22.4, 17.9 and
+// 21.3 in tiles of 64; 128: 70, 39, 30.5, 22.3; 512: tiles of 64 59.3, of 128 61.0;
+// 1,024: 113, 101.  4,096 x 12,288 with a residual: 64 tokens in rows of 32 17.7,
+// split 30.0; 256: 57.7, 30.8, tiles of 64 44.7; 512: 111, 35.9, 46.4, of 128 74.1.
+Shape pick_shape(const EpilogueArgs& a, int cus) {
+  static constexpr double kStart[] = {2, 3.5, 2, 2, 2}, kEach[] = {0.3, 0.5, 6.5, 5.5, 9};
+  static constexpr double kTime[2][5] = {{2.2, 4.4, 8, 12.4, 21}, {2.7, 5.4, 9, 13.5, 24.5}};
+  if (a.M <= 16) return shape_workgroups(ROWS_16, a) >= 16ll * cus ? ROWS_WIDE : ROWS_16;
   const int gated = a.w[1].packed != nullptr;
-  int best = ROWS_16;
+  int best = -1;
   double least = 0;
-  for (int s = ROWS_16; s < SHAPES; ++s) {
-    // (the tiles' offsets inside a token block are 32-bit)
-    if (s >= TILE_SPLIT && 128 * a.ldq >= (1ll << 31)) break;
+  for (int s = ROWS_16; s <= TILE_128; ++s) {
+    if (!shape_takes(s, a)) continue;
     const double turns = (double)((shape_workgroups(s, a) + cus - 1) / cus);
-    const double t = kStart[s] + turns * kTime[gated][s] * a.K / 4096;
-    if (s == ROWS_16 || t < least) best = s, least = t;
+    const double t = kStart[s] + turns * (kEach[s] + kTime[gated][s] * a.K / 4096);
+    if (best < 0 || t < least) best = s, least = t;
   }
-  return best;
+  return (Shape)best;
+}
+
+// Eight waves for a workgroup where there are few (4,096 x 12,288, one token: 6.2
+// us, with four 8.1), four where every CU has two (gate and up of 12,288 x 4,096:
+// 8.9 and 8.5).
+template <int RB, int TB, int MATS, int ACT>
+hipError_t launch_rows_by(const EpilogueArgs& a, int64_t workgroups, int cus, hipStream_t s) {
+  return workgroups < 2ll * cus ? launch_rows<8, RB, TB, MATS, ACT>(a, s) : launch_rows<4, RB, TB, MATS, ACT>(a, s);
 }
 
 template <int MATS, int ACT>
 hipError_t launch_act(const EpilogueArgs& a, int cus, hipStream_t s) {
-  switch (pick_shape(a, cus)) {
-    case ROWS_16: return launch_rows<1, MATS, ACT>(a, s);
-    case ROWS_32: return launch_rows<2, MATS, ACT>(a, s);
+  const Shape shape = pick_shape(a, cus);
+  const int64_t n = shape_workgroups(shape, a);
+  switch (shape) {
+    case ROWS_16: return launch_rows_by<1, 1, MATS, ACT>(a, n, cus, s);
+    case ROWS_32: return launch_rows_by<2, 2, MATS, ACT>(a, n, cus, s);
     case TILE_SPLIT: return launch_tile<MATS, ACT, TileSplit<MATS>>(a, s);
     case TILE_64: return launch_tile<MATS, ACT, Tile64<MATS>>(a, s);
-    default: return launch_tile<MATS, ACT, Tile128<MATS>>(a, s);
+    case TILE_128: return launch_tile<MATS, ACT, Tile128<MATS>>(a, s);
+    default: return launch_rows<4, 4, 1, MATS, ACT>(a, s);
   }
 }
 
@@ -519,8 +569,12 @@ hipError_t launch_mats(const EpilogueArgs& a, int cus, hipStream_t s) {
 
 }  // namespace
 
-// (the smallest workgroups' launch)
-int64_t epilogue_work_items(const EpilogueArgs& a) { return mul_sat(shape_workgroups(ROWS_16, a), kRowsT); }
+bool epilogue_takes(const EpilogueArgs& a) {
+  if (a.M <= 16) return shape_takes(ROWS_WIDE, a);
+  bool any = false;
+  for (int s = ROWS_16; s <= TILE_128; ++s) any = any || shape_takes(s, a);
+  return any;
+}
 
 hipError_t launch_epilogue(const EpilogueArgs& a, int cus, hipStream_t s) {
   return a.w[1].packed ? launch_mats<2>(a, cus, s) : launch_mats<1>(a, cus, s);

@@ -368,7 +368,7 @@ struct EpilogueArgs {
   int64_t ldq, ldr, ldy;
   int32_t N, K, ld, nch, M, act;
 };
-int64_t epilogue_work_items(const EpilogueArgs& a);
+bool epilogue_takes(const EpilogueArgs& a);  // whether some launch can count its work-items
 hipError_t launch_epilogue(const EpilogueArgs& a, int cus, hipStream_t s);
 
 constexpr int kPoolThreads = 256;

@@ -31,16 +31,15 @@ __device__ __forceinline__ int64_t pages_for(int32_t tokens, int log_p) {
 __device__ __forceinline__ bool is_page(const PoolArgs& p, int32_t id) { return id >= 0 && id < p.pages; }
 __device__ __forceinline__ int32_t* entry(const PoolArgs& p, int64_t s, int64_t j) { return p.table + s * p.ld_table + j; }
 
-// One entry less holds page id; never below 0, so a page given up twice is
-// free, not lost.
+// One entry less holds a page; a count that was 0 stays 0 (it is given back), so a
+// page given up twice is free, not lost.
 __device__ __forceinline__ void drop_ref(int32_t* ref) {
-  int32_t old = __hip_atomic_load(ref, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  while (old > 0 && !__hip_atomic_compare_exchange_weak(ref, &old, old - 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                                        __HIP_MEMORY_SCOPE_AGENT)) {
-  }
+  if (__hip_atomic_fetch_add(ref, -1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <= 0)
+    __hip_atomic_fetch_add(ref, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Exclusive prefix of v over the workgroup's threads, and its total.
+// Exclusive prefix of v over the workgroup's T threads, and its total.
+template <int T = kPoolT>
 __device__ __forceinline__ int64_t wg_prefix(int64_t v, int64_t& total, int64_t* red) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int64_t x = v;
@@ -55,7 +54,7 @@ __device__ __forceinline__ int64_t wg_prefix(int64_t v, int64_t& total, int64_t*
   int64_t before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < kPoolT / 64; ++i) {
+  for (int i = 0; i < T / 64; ++i) {
     if (i < w) before += red[i];
     total += red[i];
   }
@@ -224,13 +223,119 @@ __global__ __launch_bounds__(kPoolT) void reserve_kernel(PoolArgs p, const int32
       int64_t j = j0 + (k - first) - nd.copy;
       if (nd.copy && k == first) {
         const int32_t old = load_g(entry(p, s, j));
-        drop_ref(p.refs + old);
+        __hip_atomic_fetch_add(p.refs + old, -1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // (it was above 1)
         store_g(from + s, old);
         store_g(to + s, id);
       }
       store_g(entry(p, s, j), id);
       store_g(p.refs + id, 1);
     }
+  }
+}
+
+// A pool of up to kSmallPages pages and kSmallSeqs sequences in one launch of one
+// workgroup: the free pages as a bitmap in LDS, the sequences' needs and their
+// running sum beside it; then thread r takes the r-th page that is handed out, and
+// finds its sequence and its page by bisection.
+constexpr int kSmallT = 1024, kSmallPages = 32768, kSmallSeqs = 2048;
+
+// the last i < n with first[i] <= r (first[0] <= r)
+__device__ __forceinline__ int last_at(const int32_t* first, int n, int32_t r) {
+  int lo = 0;
+  for (int d = 1 << (31 - __builtin_clz(n)); d; d >>= 1)
+    if (lo + d < n && first[lo + d] <= r) lo += d;
+  return lo;
+}
+
+__global__ __launch_bounds__(kSmallT) void reserve_small_kernel(PoolArgs p, const int32_t* len, const int32_t* want,
+                                                                int32_t* granted, int32_t* from, int32_t* to) {
+  __shared__ int64_t red[kSmallT / 64];
+  __shared__ uint64_t free_bits[kSmallPages / 64];
+  __shared__ int32_t free_first[kSmallPages / 64], first[kSmallSeqs], needs[kSmallSeqs];
+  __shared__ int32_t writes[kSmallSeqs];
+  __shared__ __attribute__((aligned(16))) struct { int32_t id, s; } sharer[kSmallSeqs];
+  __shared__ int32_t handed, sharers;
+  const int t = threadIdx.x, lane = t & 63, S = (int)p.S, pages = (int)p.pages, words = (pages + 63) / 64;
+  // each sequence's need, as if all others kept the page it writes into (first:
+  // how many hold that)
+  for (int i = t; i < kSmallSeqs; i += kSmallT) sharer[i].id = -2;  // (no page)
+  if (t == 0) sharers = handed = 0;
+  __syncthreads();
+  for (int s = t; s < S; s += kSmallT) {
+    const int32_t n = max(load_g(len + s), 0), w = load_g(want + s), id = written_page(p, len, want, s);
+    const int64_t j1 = pages_for(w, p.log_p);
+    const int32_t held = id >= 0 ? load_g(p.refs + id) : 0;
+    writes[s] = id;
+    first[s] = held;
+    needs[s] = w <= n ? 0 : j1 > p.ld_table ? kNeedNever : (int32_t)(j1 - pages_for(n, p.log_p)) | (held > 1 ? kNeedCopy : 0);
+    if (held > 1) sharer[atomicAdd(&sharers, 1)] = {id, s};
+  }
+  constexpr int U = 8;  // loads in flight
+  for (int i0 = 0; i0 < pages; i0 += U * kSmallT) {
+    int32_t held[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) held[u] = load_g(p.refs + min(i0 + u * kSmallT + t, pages - 1));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = i0 + u * kSmallT + t;
+      const uint64_t bits = __ballot(id < pages && held[u] <= 0);
+      if (lane == 0 && id < pages) free_bits[id / 64] = bits;
+    }
+  }
+  __syncthreads();
+  int64_t all;
+  const int mine = t < words ? __builtin_popcountll(free_bits[t]) : 0;
+  const int64_t before = wg_prefix<kSmallT>(mine, all, red);
+  if (t < words) free_first[t] = (int32_t)before;
+  int64_t run = 0;
+  for (int s0 = 0; s0 < S; s0 += kSmallT) {
+    const int s = s0 + t;
+    int32_t v = s < S ? needs[s] : 0;
+    const bool shared = v > 0 && (v & kNeedCopy);
+    if (__any(shared)) {  // how many write into the page, and the last that does
+      const int32_t id = s < S ? writes[s] : -1;
+      int writers = 0, last = 0;
+      for (int k0 = 0; k0 < sharers; k0 += 8) {
+#pragma unroll
+        for (int k = k0; k < k0 + 8; k += 2) {
+          const i32x4 w = *reinterpret_cast<const i32x4*>(&sharer[k]);
+          writers += (w[0] == id) + (w[2] == id);
+          last = max(last, max(w[0] == id ? w[1] : 0, w[2] == id ? w[3] : 0));
+        }
+      }
+      if (shared && writers >= first[s] && last == s) v = (v & ~kNeedCopy) | kNeedSole;
+    }
+    const Need nd = unpack_need(v);
+    const int64_t n = nd.copy + nd.fresh;
+    int64_t total;
+    const int64_t at = run + wg_prefix<kSmallT>(n, total, red);
+    run += total;
+    __syncthreads();  // (first is rewritten from here on, a part for each round)
+    if (s < S) {
+      const bool ok = v != kNeedNever && (at + n <= all || (n == 0 && !nd.sole));
+      store_g(granted + s, (int32_t)ok);
+      if (!(ok && nd.copy)) store_g(from + s, -1), store_g(to + s, -1);
+      needs[s] = v;
+      first[s] = (int32_t)min(at, (int64_t)pages);
+      if (ok && n > 0) atomicMax(&handed, (int32_t)(at + n));
+    }
+  }
+  __syncthreads();
+  // (the sums of the rows that get something lie side by side from 0 on)
+  for (int r = t; r < handed; r += kSmallT) {
+    const int s = last_at(first, S, r), w = last_at(free_first, words, r);
+    uint64_t bits = free_bits[w];
+    for (int k = r - free_first[w]; k > 0; --k) bits &= bits - 1;
+    const int32_t id = 64 * w + __builtin_ctzll(bits);
+    const Need nd = unpack_need(needs[s]);
+    const int64_t j = pages_for(load_g(len + s), p.log_p) + (r - first[s]) - nd.copy;
+    if (nd.copy && r == first[s]) {
+      __hip_atomic_fetch_add(p.refs + writes[s], -1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      store_g(from + s, writes[s]);
+      store_g(to + s, id);
+    }
+    store_g(entry(p, s, j), id);
+    store_g(p.refs + id, 1);
   }
 }
 
@@ -372,6 +477,10 @@ hipError_t launch_kv_truncate(const PoolArgs& p, const int32_t* len, const int32
 
 hipError_t launch_kv_reserve(const PoolArgs& p, const int32_t* len, const int32_t* want, int32_t* granted,
                              int32_t* from, int32_t* to, void* workspace, hipStream_t s) {
+  if (p.pages <= kSmallPages && p.S <= kSmallSeqs) {
+    hipLaunchKernelGGL(reserve_small_kernel, dim3(1), dim3(kSmallT), 0, s, p, len, want, granted, from, to);
+    return hipGetLastError();
+  }
   const int64_t chunks = chunks_of(p.pages);
   int32_t* count = static_cast<int32_t*>(workspace);
   int32_t* need = count + chunks;

@@ -113,10 +113,11 @@ def test_model_shapes(M):
     (300, 4001, 1019, False), (601, 2500, 1030, False), (300, 2501, 2049, True), (1001, 1003, 2050, True),
     (1000, 2497, 1019, False), (577, 4000, 321, False), (600, 2500, 1019, True), (290, 4000, 2048, True),
     (2050, 6001, 700, False), (3000, 4100, 130, False), (2100, 6145, 65, False), (1500, 9001, 577, False),
+    (130, 2500, 1019, False), (130, 4001, 1019, True), (1, 70001, 300, True), (9, 65537, 129, False), (16, 66000, 1019, True),
     (1000, 2501, 1019, True), (1001, 4003, 321, True), (600, 4000, 1019, True), (2000, 4003, 130, True)])
 def test_large_odd_sizes(M, N, K, gate):
-    """Every shape of workgroup at sizes that none divides (in fours: tiles with
-    K split, of 64 tokens, of 128): the edges of its tiles."""
+    """Every shape of workgroup at sizes that none divides (tiles with K split, of
+    64 tokens, of 128, rows for more tokens, for very many rows): their edges."""
     pick = np.unique(np.r_[0:70, 120:136, 250:262, N // 2: N // 2 + 30, N - 140: N])
     run(M, N, K, gate=gate, act="silu", res="apart" if K % 2 else None, bias=K % 2 == 0, extra=K % 4, rows=pick)
 

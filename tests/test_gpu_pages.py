@@ -63,7 +63,8 @@ def dev(a):
 
 
 @pytest.mark.parametrize("pages,S,columns,P", [(30, 6, 8, 16), (200, 13, 9, 32), (9000, 70, 33, 64), (13000, 300, 17, 128),
-                                               (1, 1, 1, 16), (3, 2, 4, 16)])
+                                               (1, 1, 1, 16), (3, 2, 4, 16),
+                                               (32768, 40, 60, 16), (32769, 40, 60, 16), (40000, 300, 9, 32)])
 def test_random_runs(pages, S, columns, P):
     b = Both(pages, S, columns, P)
     rng, length = b.rng, [0] * S
@@ -132,6 +133,21 @@ def test_pool_that_runs_out():
     # more tokens than the table has columns: refused alone
     c = Both(50, 3, 2, 16)
     assert c.reserve([0, 0, 0], [33, 32, 1])[0] == [0, 1, 1]
+
+
+@pytest.mark.parametrize("S", [1025, 2048, 2049])
+def test_many_sequences(S):
+    """Batches on both sides of what one workgroup takes, few pages left."""
+    b = Both(2 * S, S, 3, 16)
+    want = [int(n) for n in b.rng.integers(0, 33, S)]
+    granted, _, _ = b.reserve([0] * S, want)
+    length = [w if g else 0 for w, g in zip(want, granted)]
+    full = int(np.argmax(length))
+    empty = [s for s in range(S) if length[s] == 0][:5]
+    b.fork(length, [full] * len(empty), empty)
+    for s in empty:
+        length[s] = length[full]
+    b.reserve(length, [n + 9 for n in length])
 
 
 def test_pages_without_holders_and_bad_entries():
