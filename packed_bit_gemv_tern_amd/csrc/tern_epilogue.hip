@@ -15,13 +15,18 @@ namespace tern {
 
 namespace {
 
-constexpr uint32_t kCodeTable = 0x000100FFu;  // code byte 0, 1, 2 -> -1, 0, +1
-
+// Sixteen weights of a packed dword as signed bytes, negated: code 0, 1, 2 -> +1,
+// 0, -1.  v_perm_b32 takes a selector byte 0 .. 3 from its second operand, 4 .. 7
+// from its first, and 8 as the sign of the second's byte 1, spread over the byte;
+// so the codes at bit 2 (selectors 0, 4, 8) need no shift where the largest code
+// stands for a byte of ones: nine operations, eleven for the weights themselves.
 __device__ __forceinline__ i32x4 decode16(uint32_t x) {
   i32x4 b;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    b[k] = (int32_t)__builtin_amdgcn_perm(kCodeTable, kCodeTable, (x >> (2 * k)) & 0x03030303u);
+  const uint32_t hi = x >> 4;
+  b[0] = (int32_t)__builtin_amdgcn_perm(0u, 0x00FF0001u, x & 0x03030303u);
+  b[1] = (int32_t)__builtin_amdgcn_perm(0u, 0x00008001u, x & 0x0C0C0C0Cu);
+  b[2] = (int32_t)__builtin_amdgcn_perm(0u, 0x00FF0001u, hi & 0x03030303u);
+  b[3] = (int32_t)__builtin_amdgcn_perm(0u, 0x00008001u, hi & 0x0C0C0C0Cu);
   return b;
 }
 
@@ -57,14 +62,15 @@ __device__ __forceinline__ RowOps<MATS> row_ops(const EpilogueArgs& a, int64_t i
   return o;
 }
 
-// One output from the linears' sums and the residual (-0: none).
+// One output from the linears' sums (of negated weights) and the residual (-0: none).
 template <int MATS, int ACT>
 __device__ __forceinline__ float output(const int32_t (&sum)[MATS], const RowOps<MATS>& o, int32_t z, float s_act,
                                         float res) {
   float v[MATS];
 #pragma unroll
   for (int k = 0; k < MATS; ++k) {
-    v[k] = __fadd_rn(epilogue(o.s_row[k], (int32_t)((uint32_t)sum[k] - mul_zr(z, o.rowsum[k])), s_act), o.bias[k]);
+    const int32_t acc = (int32_t)(0u - ((uint32_t)sum[k] + mul_zr(z, o.rowsum[k])));
+    v[k] = __fadd_rn(epilogue(o.s_row[k], acc, s_act), o.bias[k]);
   }
   float h = activate<ACT>(v[0]);
   if constexpr (MATS == 2) h = __fmul_rn(h, v[1]);
@@ -214,17 +220,37 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // A workgroup of RG x KS waves computes ROWS rows (of each matrix) x TOK tokens:
 // wave (rg, ks) 64 rows (with a gate 32 of each matrix, so that its epilogue stays
 // in the lane) x all the tokens over its share of K.  K is walked in stages of
-// 128 columns per ks: tokens by DMA into a ring of RING LDS slots, weights
-// straight to registers (no other wave of the same ks reads those rows).
-template <int MATS, int RG_, int KS_, int TB_, int RING_>
+// 128 columns per ks: tokens by DMA into a ring of four LDS slots, three stages
+// ahead, weights as far ahead straight to registers (no other wave of the same ks
+// reads those rows).  v_mfma_i32_32x32x32_i8 with the weights as A: lane (r, h) the
+// columns 64 h + 16 d .. of the stage's operand d = 0 .. 3; operands come from LDS
+// and are decoded one instruction group ahead.  One barrier per stage, before its
+// last operand: it says that the next stage has landed and that the slot of the
+// one before is free.
+//
+// What bounds it, gate and up of 12,288 x 4,096 for 2,048 tokens (0.41 Tops; a
+// library's int8 product of that size alone takes 209 us): 187 us, 2.2 POPS.  The
+// matrix instructions by themselves take 125 (3.3 POPS: the card does not hold its
+// clock under them), with the decode and the operands' LDS reads 134, with the
+// loads 150; silu's 49 vector instructions per output would take 26 by themselves
+// and overlap with the other workgroup's products in part, the 100 MB of y 15.
+// Two workgroups of four waves to a CU, whose products and epilogues fall out of
+// step.  Steps measured: operands from the L2 per 64 tokens (the rows kernel) 740;
+// tiles 220; fixed slots and silu without branches 209; sums through LDS to whole
+// lines of y 208, without a gate 127 -> 101; non-temporal stores 197 and 96; the
+// products' waves ahead of those in an epilogue (s_setprio) 194; decode in nine
+// instructions instead of eleven 187.  Not kept (no gain): operands two groups
+// ahead, weights by 64 bytes of a row and lane swaps (5 % for tiles with K split,
+// whole stages lost at small K), priorities by the workgroup's place on its CU.
+template <int MATS, int RG_, int KS_, int TB_>
 struct Tile {
-  static constexpr int RG = RG_, KS = KS_, TB = TB_, RING = RING_;
+  static constexpr int RG = RG_, KS = KS_, TB = TB_, RING = 4;
   static constexpr int WAVES = RG * KS, TOK = 32 * TB, ROWS = 64 * RG / MATS;
   static constexpr int DMA = TOK / 8 / RG;           // DMA instructions of a wave per stage (1 KB each)
-  static constexpr int WL = 4;                       // weight loads of a wave per two stages
+  static constexpr int WL = 2;                       // weight loads of a wave per stage
   static constexpr int SUB = TOK * 128, SLOT = KS * SUB;
   static constexpr int LDS = RING * SLOT > (KS > 1 ? WAVES * TB * 8192 : 0) ? RING * SLOT : WAVES * TB * 8192;
-  static_assert(DMA * 8 * RG == TOK && (RING - 2) * DMA + WL < 64 && RING >= 2, "stage split");
+  static_assert(DMA * 8 * RG == TOK && 2 * (DMA + WL) < 64, "stage split");
 };
 
 template <int N>
@@ -282,16 +308,14 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
                                                (int)(col < kbytes ? qrow[i] + col : kDropOffset), 0, 0, 0);
     }
   };
-  // weights of stages 2 c and 2 c + 1: lane (r, h) chunk 2 j + h of row r
-  auto load_w = [&](u32x4 (&x)[2][2], int c) {
+  // weights of stage J: lane (r, h) chunk 2 j + h of row r
+  auto load_w = [&](u32x4 (&x)[2], int J) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int chunk = 2 * ((2 * c + st) * S::KS + ks) + h;
-        x[st][k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 wres[k], (int)((uint32_t)r * (uint32_t)a.ld + 16u * chunk), 0, 0));
-      }
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t chunk = 2 * (J * S::KS + ks) + h;
+      x[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           wres[k], (int)((uint32_t)r * (uint32_t)a.ld + 16u * chunk), 0, 0));
+    }
   };
   uint32_t tofs[4];  // this lane's piece for operand d of a stage
 #pragma unroll
@@ -307,7 +331,7 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
     for (int t = 0; t < TB; ++t)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[k][t][v] = 0;
-  u32x4 cur[2][2], nxt[2][2];
+  u32x4 wt[4][2];  // weights of stages J .. J + 3, stage j in wt[j % 4]
   i32x4 tok[2][TB], wa[2][2];
   auto multiply = [&](int set) {
 #pragma unroll
@@ -319,54 +343,49 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
     // followed by a share of the next operand's decode
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
     __builtin_amdgcn_sched_group_barrier(0x100, TB, 0);  // LDS reads
-    __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 4 : 7, 0);  // VALU
+    __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 3 : 5, 0);  // VALU
 #pragma unroll
     for (int i = 1; i < 2 * TB; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 4 : 7, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, TB == 4 ? 3 : 5, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
-  for (int J = 0; J < S::RING; ++J) issue(J, J);
-  load_w(cur, 0);
-  wait_vm<0>();
+  for (int J = 0; J < 3; ++J) {
+    load_w(wt[J], J);
+    issue(J, J);
+  }
+  wait_vm<2 * (S::DMA + S::WL)>();  // stage 0
   asm volatile("s_barrier" ::: "memory");
   load_tok(tok[0], 0, 0);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) wa[0][k] = decode16(cur[0][k][0]);
-  // two stages (J, J + 1) in slots `slot` and slot + 1
-  auto two_stages = [&](int J, int slot) {
-    load_w(nxt, J / 2 + 1);
+  for (int k = 0; k < 2; ++k) wa[0][k] = decode16(wt[0][k][0]);
+  // Stage J in slot `slot`.  At its barrier the loads issued behind stage J + 1's
+  // DMA are, in order, the weights of J + 2, stage J + 2's DMA and the weights of J +
+  // 3 (the compiler keeps them in place: each is followed by a fence of its own).
+  auto stage = [&](int J, int slot) {
+    load_w(wt[(slot + 3) % 4], J + 3);
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-#pragma unroll
-      for (int d = 0; d < 3; ++d) {
-        load_tok(tok[(d + 1) & 1], slot + st, d + 1);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) wa[(d + 1) & 1][k] = decode16(cur[st][k][d + 1]);
-        multiply(d & 1);
+    for (int d = 0; d < 4; ++d) {
+      if (d == 3) {
+        // stage J + 1 has landed, mine and then everybody's; everybody is done with stage J - 1
+        wait_vm<S::DMA + 2 * S::WL>();
+        asm volatile("s_barrier" ::: "memory");
+        issue(J + 3, (slot + 3) % 4);
       }
-      // this wave is done with its slot; stage J + st + 1 has landed, mine and then everybody's
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      wait_vm<(S::RING - 2) * S::DMA + S::WL>();
-      asm volatile("s_barrier" ::: "memory");
-      issue(J + st + S::RING, slot + st);
-      load_tok(tok[0], (slot + st + 1) % S::RING, 0);
+      load_tok(tok[(d + 1) & 1], (slot + (d + 1) / 4) % 4, (d + 1) & 3);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) wa[0][k] = decode16(st == 0 ? cur[1][k][0] : nxt[0][k][0]);
-      multiply(1);
+      for (int k = 0; k < 2; ++k) wa[(d + 1) & 1][k] = decode16(wt[(slot + (d + 1) / 4) % 4][k][(d + 1) & 3]);
+      multiply(d & 1);
     }
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) cur[st][k] = nxt[st][k];
   };
-  static_assert(S::RING == 4, "slots of the loop below");
   __builtin_amdgcn_s_setprio(2);
   for (int J = 0; J < nst; J += 4) {
-    two_stages(J, 0);
-    two_stages(J + 2, 2);
+    stage(J, 0);
+    stage(J + 1, 1);
+    stage(J + 2, 2);
+    stage(J + 3, 3);
   }
 
   // Lane (r, h), block k, register 4 q + v hold row rows[k] + 8 q + 4 h + v of token
@@ -492,11 +511,11 @@ hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
 enum Shape { ROWS_16, ROWS_32, TILE_SPLIT, TILE_64, TILE_128, ROWS_WIDE, SHAPES };
 constexpr int kShapeRows[SHAPES] = {16, 32, 128, 256, 256, 64}, kShapeTokens[SHAPES] = {16, 32, 64, 64, 128, 16};
 template <int MATS>
-using TileSplit = Tile<MATS, 2, 4, 2, 4>;
+using TileSplit = Tile<MATS, 2, 4, 2>;
 template <int MATS>
-using Tile64 = Tile<MATS, 4, 1, 2, 4>;
+using Tile64 = Tile<MATS, 4, 1, 2>;
 template <int MATS>
-using Tile128 = Tile<MATS, 4, 1, 4, 4>;
+using Tile128 = Tile<MATS, 4, 1, 4>;
 
 int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
   const bool tile = shape >= TILE_SPLIT && shape <= TILE_128;
