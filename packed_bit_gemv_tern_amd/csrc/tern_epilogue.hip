@@ -354,7 +354,9 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
 #pragma unroll
   for (int J = 0; J < 3; ++J) {
     load_w(wt[J], J);
+    __builtin_amdgcn_sched_barrier(0);  // (the waits below count the loads in this order)
     issue(J, J);
+    __builtin_amdgcn_sched_barrier(0);
   }
   wait_vm<2 * (S::DMA + S::WL)>();  // stage 0
   asm volatile("s_barrier" ::: "memory");
@@ -363,7 +365,7 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
   for (int k = 0; k < 2; ++k) wa[0][k] = decode16(wt[0][k][0]);
   // Stage J in slot `slot`.  At its barrier the loads issued behind stage J + 1's
   // DMA are, in order, the weights of J + 2, stage J + 2's DMA and the weights of J +
-  // 3 (the compiler keeps them in place: each is followed by a fence of its own).
+  // 3: the fences in multiply, and the barrier's, keep them in their places.
   auto stage = [&](int J, int slot) {
     load_w(wt[(slot + 3) % 4], J + 3);
 #pragma unroll
