@@ -31,7 +31,9 @@ a launch of its own (three); the whole 8B stack at M = 16; q/k/v and gate/up
 sharing inputs; block-wise scales inside the stack; the activation
 quantiser; and the calls between the linears (norm with int8 output, int8
 cache append and attention, sampling), alone and in a step from the residual
-stream to the sampled token.  Most lines carry the oracle timed on a bounded sample of the
+stream to the sampled token, and what is left of a step from token to token
+(embedding lookup, norm and rotation of queries and keys, the feed-forward by
+linears with their epilogues, pages of the cache).  Most lines carry the oracle timed on a bounded sample of the
 same workload.
 """
 from __future__ import annotations
@@ -751,6 +753,7 @@ def suite(args):
 
     # --- the calls between the linears
     decode_operators(emit)
+    step_operators(emit)
 
 
 def decode_operators(emit):
@@ -814,6 +817,103 @@ def decode_operators(emit):
         us = _event_times(lambda i: tern.tern_sample(x[i % 3], M, V, V, T, u, token, ws, top_k=k, top_p=p), 50)
         emit({"suite": "sample", "workload": "sampling from M rows of 151,936 logits (top-k 50, top-p 0.95), M = %d" % M,
               "M": M, **_stats(us, 4 * M * V)})
+
+
+def step_operators(emit):
+    """The lookup, the rotation, the feed-forward by linears with their
+    epilogues and the pages of the cache, in the 8B's geometry (one JSON line
+    each; rotating copies)."""
+    import torch
+    from packed_bit_gemv_tern_amd import tern
+    dev, K, F, V, HQ, H, D, P, L = "cuda:0", 4096, 12288, 151936, 32, 8, 128, 64, 36
+    W = torch.randint(-127, 128, (V, K), dtype=torch.int8, device=dev)
+    s_row = torch.rand(V, device=dev)
+    for M in (1, 512, 8192):
+        ids = [torch.randint(0, V, (M,), dtype=torch.int32, device=dev) for _ in range(3)]
+        x = torch.empty(M, K, device=dev)
+        us = _event_times(lambda i: tern.tern_embed(W, s_row, V, K, K, ids[i % 3], M, x, K), 50)
+        emit({"suite": "embed", "workload": "rows of the int8 embedding table (151,936 x 4,096), M = %d" % M, "M": M,
+              **_stats(us, 5 * M * K + 8 * M)})
+    del W
+    freq = (1e6 ** (-torch.arange(0, D, 2, device=dev) / D)).float()
+    for S, new in ((1, 1), (48, 1), (3, 2048)):
+        rows, ld = S * new, (HQ + 2 * H) * D
+        qkv = [torch.randn(rows, ld, device=dev) for _ in range(3)]
+        gain = torch.rand(D, device=dev)
+        start = torch.arange(S + 1, dtype=torch.int32, device=dev) * new
+        length = torch.full((S,), 4096, dtype=torch.int32, device=dev)
+        batch = tern.make_kv_batch(None, 0, start, length, S, rows, new)
+
+        def rope(i):
+            q, k = qkv[i % 3], qkv[i % 3][:, HQ * D:]
+            tern.tern_qk_norm_rope(batch, D, freq, D, q=q, ldq=ld, q_heads=HQ, q_gain=gain, q_out=q, ldqo=ld, k=k,
+                                   ldk=ld, heads=H, k_gain=gain, k_out=k, ldko=ld)
+        emit({"suite": "qk_norm_rope", "workload": "norm and rotation of q and k in place: %d sequence(s), %d new tokens "
+              "each, 32 query and 8 KV heads of 128" % (S, new), **_stats(_event_times(rope, 50),
+                                                                           8 * rows * (HQ + H) * D)})
+    # the gated feed-forward: gate and up with silu(g) * u, quantised, down onto the residual stream
+    copies = 8
+
+    def linear(N, Kc):
+        packed = torch.randint(0, 256, (N, tern.tern_row_bytes(Kc)), dtype=torch.uint8, device=dev)
+        packed &= ~((packed & 0xAA) >> 1)  # (no code 3)
+        return tern.make_weights(packed, *(keep := (torch.rand(N, device=dev) * 0.01, torch.randint(
+            -99, 99, (N,), dtype=torch.int32, device=dev)))), (packed, keep)
+    lins = [[linear(F, K), linear(F, K), linear(K, F)] for _ in range(copies)]
+    for M in (1, 8, 64, 512, 2048):
+        q = torch.randint(-128, 128, (M, K), dtype=torch.int8, device=dev)
+        s, z = torch.rand(M, device=dev) * 0.02, torch.randint(-8, 9, (M,), dtype=torch.int32, device=dev)
+        h, q2 = torch.empty(M, F, device=dev), torch.empty((M, F), dtype=torch.int8, device=dev)
+        s2, z2 = torch.empty(M, device=dev), torch.empty(M, dtype=torch.int32, device=dev)
+        r = torch.randn(M, K, device=dev)
+
+        def gate_up(i):
+            g, u, _ = lins[i % copies]
+            tern.tern_linear_epilogue(g[0], F, K, M, q, K, s, z, h, F, up=u[0], act=tern.TERN_ACT_SILU)
+
+        def down(i):
+            tern.tern_linear_epilogue(lins[i % copies][2][0], K, F, M, q2, F, s2, z2, r, K, res=r, ldr=K)
+
+        def ffn(i):
+            gate_up(i)
+            tern.tern_quantize_act(h, M, F, F, q2, F, s2, z2)
+            down(i)
+        for name, fn, mats in (("gate and up with silu(g) * u in the epilogue", gate_up, 2),
+                               ("down with the residual in the epilogue", down, 1),
+                               ("gate and up, quantiser, down with the residual (three launches)", ffn, 3)):
+            us = _event_times(fn, 40)
+            nbytes = mats * F * K // 4 + (4 * M * F if mats != 1 else 0) + (8 * M * K if mats != 2 else 0)
+            st_ = _stats(us, nbytes)
+            st_["dense_TOPS"] = round(2e-6 * M * F * K * mats / st_["median_us"], 2)
+            emit({"suite": "linear_epilogue", "workload": "8B feed-forward, %s, M = %d" % (name, M), "M": M, **st_})
+    del lins
+    torch.cuda.empty_cache()
+    # 256 sequences of 4,000 tokens on average, 8 drafted tokens each; then pages moved in every layer
+    S, J = 256, 130
+    length = torch.randint(100, 8000, (S,), dtype=torch.int32, device=dev)
+    held = (length.long() + P - 1) // P
+    pages = int(held.sum()) + 1024
+    table = torch.full((S, J), -1, dtype=torch.int32, device=dev)
+    table[torch.arange(J, device=dev) < held[:, None]] = torch.randperm(pages, device=dev)[: int(held.sum())].to(torch.int32)
+    refs = torch.bincount(table[table >= 0].long(), minlength=pages).to(torch.int32)
+    pool = tern.make_kv_pool(refs, table, J, S, pages, P)
+    want = length + 8
+    out = torch.empty((3, S), dtype=torch.int32, device=dev)
+    ws = torch.empty(tern.tern_kv_pool_workspace_bytes(pool), dtype=torch.uint8, device=dev)
+
+    def pages_step(i):
+        tern.tern_kv_reserve(pool, length, want, out[0], out[1], out[2], ws)
+        tern.tern_kv_truncate(pool, want, length)
+    emit({"suite": "kv_pages", "workload": "pages for 8 drafted tokens of 256 sequences (pool of %d), and back" % pages,
+          **_stats(_event_times(pages_step, 50))})
+    n, pages = 32, 128
+    k, v = (torch.randint(-127, 128, (L, pages, H * P * D), dtype=torch.int8, device=dev) for _ in range(2))
+    sc = torch.rand(2, L, pages, H, device=dev)
+    layers = tern.make_kv_layers([tern.make_kv_cache(k[i], v[i], sc[0, i], sc[1, i], pages, H, D, P) for i in range(L)])
+    src, dst = torch.randperm(pages, device=dev)[: 2 * n].to(torch.int32).reshape(2, n)
+    us = _event_times(lambda i: tern.tern_kv_copy(layers, layers, src, dst, n), 50)
+    emit({"suite": "kv_pages", "workload": "%d pages of 64 tokens copied in 36 layers, 8 KV heads of 128" % n,
+          **_stats(us, 2 * n * L * H * (2 * P * D + 8))})
 
 
 def prefill_case(args, M: int):
