@@ -228,20 +228,23 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // last operand: it says that the next stage has landed and that the slot of the
 // one before is free.
 //
-// What bounds it, gate and up of 12,288 x 4,096 for 2,048 tokens (0.41 Tops; a
-// library's int8 product of that size alone takes 209 us): 187 us, 2.2 POPS.  The
-// matrix instructions by themselves take 125 (3.3 POPS: the card does not hold its
-// clock under them), with the decode and the operands' LDS reads 134, with the
-// loads 150; silu's 49 vector instructions per output would take 26 by themselves
-// and overlap with the other workgroup's products in part, the 100 MB of y 15.
-// Two workgroups of four waves to a CU, whose products and epilogues fall out of
-// step.  Steps measured: operands from the L2 per 64 tokens (the rows kernel) 740;
-// tiles 220; fixed slots and silu without branches 209; sums through LDS to whole
-// lines of y 208, without a gate 127 -> 101; non-temporal stores 197 and 96; the
-// products' waves ahead of those in an epilogue (s_setprio) 194; decode in nine
-// instructions instead of eleven 187.  Not kept (no gain): operands two groups
-// ahead, weights by 64 bytes of a row and lane swaps (5 % for tiles with K split,
-// whole stages lost at small K), priorities by the workgroup's place on its CU.
+// What bounds it, gate and up of 12,288 x 4,096 for 2,048 tokens (412 Gops; a
+// library's int8 product of that size alone takes 209 us): 187 to 192 us, 2.2 POPS
+// (down, 4,096 x 12,288, 77 us and 2.7: fewer outputs per operation).  The matrix
+// cores are busy in 66 % of each SIMD's cycles, and the card holds 1.5 GHz under
+// them: the matrix instructions by themselves take 125 us, with the decode and the
+// operands' LDS reads 134, with the loads 150; silu's 49 vector instructions per
+// output would take 26 by themselves and overlap with the other workgroup's products
+// in part, the 100 MB of y 15.  Two workgroups of four waves to a CU, whose products
+// and epilogues fall out of step.  Steps measured: operands from the L2 per 64 tokens
+// (the rows kernel) 740; tiles 220; fixed slots and silu without branches 209; sums
+// through LDS to whole lines of y 198 (without a gate 127 -> 99); the products' waves
+// ahead of those in an epilogue (s_setprio) 194; decode in nine instructions instead
+// of eleven, tiles in groups 187.  Not kept (no gain): operands two groups ahead,
+// weights by 64 bytes of a row and lane swaps (5 % for tiles with K split, whole
+// stages lost at small K), priorities by the workgroup's place on its CU; and
+// non-temporal stores of y (1 us less here, 9 more for the quantiser that reads y
+// next).
 template <int MATS, int RG_, int KS_, int TB_>
 struct Tile {
   static constexpr int RG = RG_, KS = KS_, TB = TB_, RING = 4;
@@ -475,7 +478,7 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
       if (m >= a.M) continue;
       float* y = a.y + m * a.ldy + i0;
       if (yvec) {
-        __builtin_nontemporal_store(o, (f32x4 __attribute__((address_space(1)))*)(y));
+        store_g(reinterpret_cast<f32x4*>(y), o);
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v)

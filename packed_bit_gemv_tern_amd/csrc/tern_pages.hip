@@ -13,7 +13,8 @@
 // and sequences before it, not from the order in which threads arrive: results
 // are the same in every run.  Ids outside [0, pages) are passed over wherever
 // one is read, so no content of the tables reaches past the buffers.
-// Roofline: launches (the tables are a few KB to a few MB) and, for copy, HBM.
+// Roofline: launches and trips to memory (the tables are a few KB to a few MB) and,
+// for copy, HBM: 684 pages of 128 KB, 180 MB, in 42 us, 4.3 TB/s (a large copy: 4.7).
 #include <algorithm>
 
 #include "tern_device.h"
@@ -236,8 +237,11 @@ __global__ __launch_bounds__(kPoolT) void reserve_kernel(PoolArgs p, const int32
 // A pool of up to kSmallPages pages and kSmallSeqs sequences in one launch of one
 // workgroup: the free pages as a bitmap in LDS, the sequences' needs and their
 // running sum beside it; then thread r takes the r-th page that is handed out, and
-// finds its sequence and its page by bisection.
-constexpr int kSmallT = 1024, kSmallPages = 32768, kSmallSeqs = 2048;
+// finds its sequence and its page by bisection.  One step of 8 tokens, this against
+// the two launches above: 9 sequences, 80 pages 4.3 and 6.4 us, 64 and 4,096 6.9 and
+// 9.6, 256 and 15,548 8.9 and 9.6 (64 of them sharing pages 8.8 and 9.7), 256 and
+// 32,768 10.0 and 9.7, 65,536 13.9 and 9.9: a chain of trips to memory either way.
+constexpr int kSmallT = 1024, kSmallPages = 16384, kSmallSeqs = 2048;
 
 // the last i < n with first[i] <= r (first[0] <= r)
 __device__ __forceinline__ int last_at(const int32_t* first, int n, int32_t r) {

@@ -41,8 +41,8 @@ __device__ __forceinline__ float wave_max_f(float v) {
 //   t = clamp(-g, -87, 100); e = e^t by Cody and Waite's reduction
 //   t = k ln2 + r (k = rint(t / ln 2), ln 2 split in a 15-bit head, whose
 //   product with k is exact, and an fp32 tail) and the Taylor series of e^r
-//   through r^7 by Horner's rule, scaled by 2^k (+inf past 88.7);
-//   silu = g / (1 + e), correctly rounded; h = silu * u.
+//   through r^7 by Horner's rule, scaled by 2^k (+inf past 88.7): exp32;
+//   silu = g / (1 + e), correctly rounded: silu32; h = silu * u: swiglu32.
 __device__ __forceinline__ float exp32(float t) {
   constexpr double kLn2 = 0.69314718055994530942;
   constexpr float kInvLn2 = (float)(1.0 / kLn2);

@@ -12,7 +12,9 @@
 // all in fp64 with one rounding to fp32: positions reach 2^30, where an angle
 // in fp32 would be off by whole turns, and what fp64 costs stays under the
 // memory time.  The angles are one per (token, i) and shared by all heads.
-// Roofline: HBM, 8 bytes an element.
+// Roofline: HBM, 8 bytes an element: 5,270 tokens of 40 heads of 128, 216 MB, in
+// 43 us, 5.0 TB/s (a copy: 4.7).  48 single tokens, 3.9 us: the launch, the token's
+// sequence, the angles and the heads' rows one after the other.
 #include <algorithm>
 
 #include "tern_device.h"
@@ -126,10 +128,13 @@ __global__ __launch_bounds__(kRopeT) void rope_kernel(RopeArgs a, int splits) {
   }
 }
 
-// Workgroups that share a token's heads: one for many tokens, more for few.
+// Workgroups that share a token's heads: one for many tokens, whose angles are then
+// computed once; as many as there are groups of heads (three of 16 here) for few,
+// which would leave CUs idle (1 token: 3.3 us, in one workgroup 4.8; 512: 6.9 and
+// 7.5; 1,024: 12.7 and 10.8; 2,048: 17.7 and 16.0).
 int rope_splits(const RopeArgs& a) {
   const int per = kRopeT * 8 / a.D;
-  return a.rows >= 512 ? 1 : (a.heads[0] + a.heads[1] + per - 1) / per;
+  return a.rows >= 768 ? 1 : (a.heads[0] + a.heads[1] + per - 1) / per;
 }
 
 }  // namespace

@@ -372,7 +372,7 @@ def make_kv_pool(refs, table, ld_table, S, pages, page_tokens) -> tern_kv_pool:
 
 def make_kv_layers(caches):
     """The layers' caches (make_kv_cache) as tern_kv_copy takes them."""
-    return (tern_kv_cache * max(1, len(caches)))(*caches)
+    return (tern_kv_cache * len(caches))(*caches)
 
 
 def tern_kv_pool_workspace_bytes(pool) -> int:

@@ -64,7 +64,7 @@ def dev(a):
 
 @pytest.mark.parametrize("pages,S,columns,P", [(30, 6, 8, 16), (200, 13, 9, 32), (9000, 70, 33, 64), (13000, 300, 17, 128),
                                                (1, 1, 1, 16), (3, 2, 4, 16),
-                                               (32768, 40, 60, 16), (32769, 40, 60, 16), (40000, 300, 9, 32)])
+                                               (16384, 40, 60, 16), (16385, 40, 60, 16), (40000, 300, 9, 32)])
 def test_random_runs(pages, S, columns, P):
     b = Both(pages, S, columns, P)
     rng, length = b.rng, [0] * S
