@@ -346,12 +346,15 @@ __global__ __launch_bounds__(kSmallT) void reserve_small_kernel(PoolArgs p, cons
 
 // ---- compact -----------------------------------------------------------------
 
+__device__ __forceinline__ void clear_moves(int32_t* from, int32_t* to, int64_t moves, int64_t i0, int64_t step) {
+  for (int64_t i = i0; i < moves; i += step) store_g(from + i, -1), store_g(to + i, -1);
+}
+
 // Counts the pages in use of a chunk; clears the lists of moves.
-__global__ __launch_bounds__(kPoolT) void compact_count_kernel(PoolArgs p, int32_t* count, int64_t chunks,
-                                                               int32_t* from, int32_t* to, int64_t moves) {
+__global__ __launch_bounds__(kPoolT) void compact_count_kernel(PoolArgs p, int32_t* count, int32_t* from, int32_t* to,
+                                                               int64_t moves) {
   __shared__ int64_t red[kPoolT / 64];
-  for (int64_t i = (int64_t)blockIdx.x * kPoolT + threadIdx.x; i < moves; i += (int64_t)gridDim.x * kPoolT)
-    store_g(from + i, -1), store_g(to + i, -1);
+  clear_moves(from, to, moves, (int64_t)blockIdx.x * kPoolT + threadIdx.x, (int64_t)gridDim.x * kPoolT);
   int64_t n = 0, total;
   for (int i = 0; i < kChunk / kPoolT; ++i) {
     const int64_t id = (int64_t)blockIdx.x * kChunk + i * kPoolT + threadIdx.x;
@@ -363,31 +366,46 @@ __global__ __launch_bounds__(kPoolT) void compact_count_kernel(PoolArgs p, int32
 
 // Page p with u pages in use before it: a hole (p < live) is the (p - u)-th
 // from below, a page in use at or behind `live` the (live - 1 - u)-th from
-// above; there are as many of one as of the other.
-__global__ __launch_bounds__(kPoolT) void compact_plan_kernel(PoolArgs p, const int32_t* count, int64_t chunks,
-                                                              int32_t* from, int32_t* to, int64_t moves, int32_t* rank,
-                                                              int32_t* live_out) {
-  __shared__ int64_t red[kPoolT / 64];
+// above; there are as many of one as of the other.  With T = kSmallT the workgroup
+// is alone (up to kAlonePages pages), counts for itself and clears the lists too:
+// compact of 9 sequences' 80 pages 6.5 us, with the launch that counts 8.9, of 64
+// and 4,096 7.6 and 14.1, of 256 and 8,192 9.2 and 14.7, and 12,288 11.1 and 14.7, and
+// 16,384 17.4 and 15.2.
+constexpr int kAlonePages = 12 * kSmallT;
+template <int T>
+__global__ __launch_bounds__(T) void compact_plan_kernel(PoolArgs p, const int32_t* count, int64_t chunks,
+                                                         int32_t* from, int32_t* to, int64_t moves, int32_t* rank,
+                                                         int32_t* live_out) {
+  constexpr bool kAlone = T == kSmallT;
+  constexpr int kEach = kAlone ? kAlonePages / T : kChunk / T;
+  __shared__ int64_t red[T / 64];
   const int t = threadIdx.x;
   int64_t before = 0, live = 0, total;
-  for (int64_t c = t; c < chunks; c += kPoolT) {
-    const int64_t n = load_g(count + c);
-    live += n;
-    if (c < blockIdx.x) before += n;
-  }
-  wg_prefix(before, total, red);
-  before = total;
-  wg_prefix(live, total, red);
-  live = total;
-  if (blockIdx.x == 0 && t == 0) store_g(live_out, (int32_t)live);
-  const int64_t id0 = (int64_t)blockIdx.x * kChunk + (int64_t)t * (kChunk / kPoolT);
+  const int64_t id0 = ((int64_t)blockIdx.x * T + t) * kEach;
+  int32_t held[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) held[i] = load_g(p.refs + min(id0 + i, p.pages - 1));
   uint32_t mask = 0;
 #pragma unroll
-  for (int i = 0; i < kChunk / kPoolT; ++i)
-    if (id0 + i < p.pages && load_g(p.refs + id0 + i) > 0) mask |= 1u << i;
-  int64_t u = before + wg_prefix(__builtin_popcount(mask), total, red);
+  for (int i = 0; i < kEach; ++i) mask |= (uint32_t)(id0 + i < p.pages && held[i] > 0) << i;
+  if constexpr (kAlone) {
+    clear_moves(from, to, moves, t, T);
+  } else {
+    for (int64_t c = t; c < chunks; c += T) {
+      const int64_t n = load_g(count + c);
+      live += n;
+      if (c < blockIdx.x) before += n;
+    }
+    wg_prefix<T>(before, total, red);
+    before = total;
+    wg_prefix<T>(live, total, red);
+    live = total;
+  }
+  int64_t u = before + wg_prefix<T>(__builtin_popcount(mask), total, red);  // (its barriers also order the clearing)
+  if constexpr (kAlone) live = total;
+  if (blockIdx.x == 0 && t == 0) store_g(live_out, (int32_t)live);
 #pragma unroll
-  for (int i = 0; i < kChunk / kPoolT; ++i) {
+  for (int i = 0; i < kEach; ++i) {
     const int64_t id = id0 + i;
     if (id >= p.pages) break;
     const bool used = mask >> i & 1;
@@ -503,12 +521,17 @@ hipError_t launch_kv_compact(const PoolArgs& p, const int32_t* len, int32_t* fro
   const int64_t chunks = chunks_of(p.pages);
   int32_t* count = static_cast<int32_t*>(workspace);
   int32_t* rank = count + chunks;
-  hipLaunchKernelGGL(compact_count_kernel, dim3((unsigned)chunks), dim3(kPoolT), 0, s, p, count, chunks, from, to,
-                     moves);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(compact_plan_kernel, dim3((unsigned)chunks), dim3(kPoolT), 0, s, p, count, chunks, from, to,
-                     moves, rank, live);
+  hipError_t e;
+  if (p.pages <= kAlonePages) {
+    hipLaunchKernelGGL(compact_plan_kernel<kSmallT>, dim3(1), dim3(kSmallT), 0, s, p, count, chunks, from, to, moves,
+                       rank, live);
+  } else {
+    hipLaunchKernelGGL(compact_count_kernel, dim3((unsigned)chunks), dim3(kPoolT), 0, s, p, count, from, to, moves);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(compact_plan_kernel<kPoolT>, dim3((unsigned)chunks), dim3(kPoolT), 0, s, p, count, chunks, from,
+                       to, moves, rank, live);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   // (no more than pages / 2 of the listed moves are in use)

@@ -180,6 +180,21 @@ def test_large_pool():
         c.compact([0, 0], moves)
 
 
+@pytest.mark.parametrize("pages", [1, 2, 17, 4096, 4097, 12287, 12288, 12289, 16385])
+@pytest.mark.parametrize("share", [0.0, 0.03, 0.5, 1.0])
+def test_compact_sizes(pages, share):
+    """Pools inside one workgroup and past it, nearly full to nearly empty, lists
+    shorter and longer than the moves (compact compares every array)."""
+    for moves in (0, 1, 5, pages // 2, pages + 3):
+        c = Both(pages, 2, 4, 16, seed=2)
+        c.host.refs = [int(r < share) * int(k) for r, k in zip(c.rng.random(pages), c.rng.integers(1, 4, pages))]
+        used = [i for i, r in enumerate(c.host.refs) if r]
+        if len(used) > 4:
+            c.host.table = [used[:2] + used[-2:], [used[-1], -1, used[len(used) // 2], used[0]]]
+        c.upload()
+        c.compact([64, 40], moves)
+
+
 @pytest.mark.parametrize("H,D,P,L", [(2, 64, 16, 3), (1, 128, 128, 2), (8, 128, 64, 2), (3, 64, 32, 41), (1, 64, 16, 81)])
 def test_copy(H, D, P, L):
     rng = np.random.default_rng([H, D, P, L])
