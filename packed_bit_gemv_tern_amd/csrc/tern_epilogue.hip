@@ -229,7 +229,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // one before is free.
 //
 // What bounds it, gate and up of 12,288 x 4,096 for 2,048 tokens (412 Gops; a
-// library's int8 product of that size alone takes 209 us): 187 to 192 us, 2.2 POPS
+// library's int8 product of that size alone takes 209 us): 184 to 192 us, 2.2 POPS
 // (down, 4,096 x 12,288, 77 us and 2.7: fewer outputs per operation).  The matrix
 // cores are busy in 66 % of each SIMD's cycles, and the card holds 1.5 GHz under
 // them: the matrix instructions by themselves take 125 us, with the decode and the
