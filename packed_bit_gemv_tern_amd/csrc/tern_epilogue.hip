@@ -94,42 +94,171 @@ __device__ __forceinline__ i32x4 load_q16(const int8_t* q, int64_t j, int K) {
   return v;
 }
 
-// ---- few tokens: rows --------------------------------------------------------
+// ---- few tokens: streams of K -------------------------------------------------
 
-// RB blocks of 16 rows (of each matrix) and TB blocks of 16 tokens to a
-// workgroup; its W waves take 256 columns at a time in turn, and their exact
-// int32 sums meet in LDS.  v_mfma_i32_16x16x64_i8 with the weights as A: lane
-// (r, g) loads the whole 16-byte chunk 4 i + g of row r, four operands of 64
-// weights for four instructions; the tokens' operands are the same columns of
-// token r, loaded as they lie (any order of K serves if both sides have it).
-// The weights of the next step are asked for behind this step's activations:
-// loads return in order, so before them they would be waited for with them.
-// Bound by the weights' bytes for one token, by the activations that every
-// workgroup reads from the L2 for sixteen (gate and up of 12,288 x 4,096, weights
-// from memory, 25 MB: 8.5, 10.3 and 12.0 us for 1, 8 and 16 tokens, of which 2.3
-// are the launch; 32 rows to a workgroup 9.4, 10.0, 11.7).  Measured and not
-// kept: 128 bytes of a row to a lane's four (8.8), weights four steps ahead
-// (10.3), chunks transposed across the lanes so that a token's operands are 64
-// contiguous bytes (8.2).
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
 constexpr int kRedStride = 68;  // of 64 lanes' values of one register, off each other's banks
 
+// The sums of W waves and the epilogue: lane (r, g), register v of a block of
+// both holds row 16 b + 4 g + v, token 16 t + r.
 template <int W, int RB, int TB, int MATS, int ACT>
+__device__ __forceinline__ void join_rows(const EpilogueArgs& a, int row0, int64_t tok0,
+                                          const i32x4 (&acc)[MATS][RB][TB], int32_t* red) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int BLOCKS = TB * MATS * RB * 4;
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+#pragma unroll
+    for (int k = 0; k < MATS; ++k)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          red[(w * BLOCKS + ((t * MATS + k) * RB + b) * 4 + v) * kRedStride + lane] = acc[k][b][t][v];
+  __syncthreads();
+  for (int o = threadIdx.x; o < 16 * RB * 16 * TB; o += 64 * W) {
+    const int row = o % (16 * RB), tok = o / (16 * RB);
+    const int64_t m = tok0 + tok;
+    if (m >= a.M || row0 + row >= a.N) continue;
+    int32_t sum[MATS];
+#pragma unroll
+    for (int k = 0; k < MATS; ++k) {
+      sum[k] = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        sum[k] += red[(i * BLOCKS + ((tok / 16 * MATS + k) * RB + row / 16) * 4 + row % 4) * kRedStride +
+                      16 * (row % 16 / 4) + tok % 16];
+    }
+    const int64_t i = row0 + row;
+    const float res = a.res ? load_g(a.res + m * a.ldr + i) : -0.0f;
+    store_g(a.y + m * a.ldy + i, output<MATS, ACT>(sum, row_ops<MATS>(a, i), load_g(a.z + m), load_g(a.s_act + m), res));
+  }
+}
+
+// Rows whose K is no multiple of 16 may end inside a piece of 16 bytes, for up to 16
+// tokens: 16 rows x 16 tokens to a workgroup of W waves, operands loaded as they lie
+// (the columns behind K by the byte).  The weights of the next step are asked for
+// behind this step's activations: loads return in order, so before them they would
+// be waited for with them.
+template <int W, int MATS, int ACT>
 __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, int row_tiles) {
-  __shared__ int32_t red[W][MATS * RB * 4 * kRedStride];
+  __shared__ int32_t red[W * MATS * 4 * kRedStride];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int row0 = (blockIdx.x % row_tiles) * 16;
+  const int64_t tok0 = (int64_t)(blockIdx.x / row_tiles) * 16;
+  // (rows and chunks past the matrix give zeros: they meet zero activations, or are
+  // not stored)
+  __amdgpu_buffer_rsrc_t wres[MATS];
+#pragma unroll
+  for (int k = 0; k < MATS; ++k)
+    wres[k] = uniform_rsrc(a.w[k].packed + (int64_t)row0 * a.ld, (uint32_t)min(a.N - row0, 16) * (uint32_t)a.ld);
+  const int8_t* q = a.q + min(tok0 + r, (int64_t)a.M - 1) * a.ldq;
+  i32x4 acc[MATS][1][1];
+#pragma unroll
+  for (int k = 0; k < MATS; ++k) acc[k][0][0] = i32x4{0, 0, 0, 0};
+  auto load_w = [&](u32x4 (&x)[MATS], int c0) {
+#pragma unroll
+    for (int k = 0; k < MATS; ++k)
+      x[k] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     wres[k], (int)(c0 + g < a.nch ? (uint32_t)r * (uint32_t)a.ld + 16u * (c0 + g) : kDropOffset), 0, 0));
+  };
+  u32x4 cur[MATS], nxt[MATS];
+  load_w(cur, 4 * w);
+  for (int c0 = 4 * w; c0 < a.nch; c0 += 4 * W) {
+    i32x4 qa[4];
+    const int64_t j = 64ll * (c0 + g);
+    if (64 * (c0 + 4) <= a.K) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) qa[d] = __builtin_bit_cast(i32x4, load16(q + j + 16 * d));
+    } else {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) qa[d] = load_q16(q, j + 16 * d, a.K);
+    }
+    load_w(nxt, c0 + 4 * W);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < MATS; ++k) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        acc[k][0][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode16(cur[k][d]), qa[d], acc[k][0][0], 0, 0, 0);
+      cur[k] = nxt[k];
+    }
+  }
+  join_rows<W, 1, 1, MATS, ACT>(a, row0, tok0, acc, red);
+}
+
+// A workgroup's W waves share K (RB blocks of 16 rows of each matrix, TB blocks of
+// 16 tokens, a step 256 columns), and until the join of their exact int32 sums
+// nothing else: each brings its tokens and weights by DMA to a slot of its own in
+// LDS, reads them to registers, asks for the next step's and multiplies, so nobody
+// waits for a barrier.  v_mfma_i32_16x16x64_i8 with the weights as A: lane (r, g) has
+// the whole 16-byte chunk g of row r, four operands of 64 weights for four
+// instructions, and for operand d piece d of block g of token r.  What counts is
+// what L1 passes: a load instruction whose neighbouring lanes read different rows
+// (the operands as they lie) gets 16 bytes a cycle, one whose four neighbours read
+// 64 bytes of one row 58 (measured: 393 KB to each CU in 9.8 and 3.1 us).  So DMA
+// instruction c brings 64 columns: lane 4 t + p piece p ^ swz(t) of token t, where
+// the operands' reads then touch every bank once; weights alike.
+//
+// Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 7.7,
+// 7.9 and 8.5 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.1,
+// 12.0); down, 4,096 x 12,288, 8 and 64 tokens 5.9 and 10.3 (7.9 and 17.5).  One slot
+// for a wave and many workgroups on a CU: with two slots 8.7, 8.9 and 9.5, with three
+// 9.7, 9.8 and 10.3.
+__device__ __forceinline__ int slot_swz(int row) { return (row >> 1) & 3; }
+
+template <int W, int RB, int TB, int MATS, int ACT>
+__global__ __launch_bounds__(64 * W) void epilogue_stream_kernel(EpilogueArgs a, int row_tiles) {
+  constexpr int P = 4 * TB + MATS * RB;  // DMA instructions (1 KB each) of a step
+  constexpr int RED = W * TB * MATS * RB * 4 * kRedStride * 4, SLOTS = W * P * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SLOTS > RED ? SLOTS : RED];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int row0 = (blockIdx.x % row_tiles) * 16 * RB;
   const int64_t tok0 = (int64_t)(blockIdx.x / row_tiles) * 16 * TB;
-  // (rows and chunks past the matrix give zeros or other rows' weights: they meet
-  // zero activations, or are not stored)
   __amdgpu_buffer_rsrc_t wres[MATS];
-  const int here = min(a.N - row0, 16 * RB);
+  const int here = min(a.N - row0, 16 * RB), toks = (int)min((int64_t)16 * TB, a.M - tok0);
 #pragma unroll
   for (int k = 0; k < MATS; ++k)
     wres[k] = uniform_rsrc(a.w[k].packed + (int64_t)row0 * a.ld, (uint32_t)here * (uint32_t)a.ld);
-  const int8_t* qsrc[TB];
+  const uint32_t kbytes = ((uint32_t)a.K + 15) & ~15u;  // (inside ldq, or K itself: stream_takes)
+  const __amdgpu_buffer_rsrc_t qres =
+      uniform_rsrc(a.q + tok0 * a.ldq, (uint32_t)(toks - 1) * (uint32_t)a.ldq + kbytes);
+  const int lr = lane >> 2, lp = (lane & 3) ^ slot_swz(lr);
+  uint32_t qrow[TB];
 #pragma unroll
-  for (int t = 0; t < TB; ++t) qsrc[t] = a.q + min(tok0 + 16 * t + r, (int64_t)a.M - 1) * a.ldq;
+  for (int t = 0; t < TB; ++t) qrow[t] = 16 * t + lr < toks ? (uint32_t)(16 * t + lr) * (uint32_t)a.ldq : kDropOffset;
+  uint8_t* mine = lds + w * P * 1024;
+  // 256 columns from chunk c0 on; past K: zeros
+  auto issue = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < MATS; ++k) {
+      const __amdgpu_buffer_rsrc_t from = wres[k];
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            from, (lds_ptr_t)(mine + (k * RB + b) * 1024), 16,
+            (int)(c0 + lp < a.nch ? (uint32_t)(16 * b + lr) * (uint32_t)a.ld + 16u * (c0 + lp) : kDropOffset), 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t col = 64u * (c0 + c) + 16u * lp;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(qres, (lds_ptr_t)(mine + (MATS * RB + 4 * t + c) * 1024), 16,
+                                                 (int)(col < kbytes ? qrow[t] + col : kDropOffset), 0, 0, 0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   i32x4 acc[MATS][RB][TB];
 #pragma unroll
   for (int k = 0; k < MATS; ++k)
@@ -137,85 +266,43 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int t = 0; t < TB; ++t) acc[k][b][t] = i32x4{0, 0, 0, 0};
-  auto load_w = [&](u32x4 (&x)[MATS][RB], int c0) {
+  if (4 * w < a.nch) issue(4 * w);
+  for (int c0 = 4 * w; c0 < a.nch; c0 += 4 * W) {
+    wait_vm<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 wt[MATS][RB];
+    i32x4 qa[TB][4];
 #pragma unroll
     for (int k = 0; k < MATS; ++k)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
-        x[k][b] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       wres[k],
-                       (int)(c0 + g < a.nch ? (uint32_t)(16 * b + r) * (uint32_t)a.ld + 16u * (c0 + g) : kDropOffset),
-                       0, 0));
-  };
-  u32x4 cur[MATS][RB], nxt[MATS][RB];
-  load_w(cur, 4 * w);
-  for (int c0 = 4 * w; c0 < a.nch; c0 += 4 * W) {
-    i32x4 qa[TB][4];
-    const int64_t j = 64ll * (c0 + g);
-    if (64 * (c0 + 4) <= a.K) {
+        wt[k][b] = *reinterpret_cast<const u32x4*>(mine + (k * RB + b) * 1024 + 64 * r + 16 * (g ^ slot_swz(r)));
 #pragma unroll
-      for (int t = 0; t < TB; ++t)
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) qa[t][d] = __builtin_bit_cast(i32x4, load16(qsrc[t] + j + 16 * d));
-    } else {
-#pragma unroll
-      for (int t = 0; t < TB; ++t)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) qa[t][d] = load_q16(qsrc[t], j + 16 * d, a.K);
-    }
-    load_w(nxt, c0 + 4 * W);
+      for (int d = 0; d < 4; ++d)
+        qa[t][d] = *reinterpret_cast<const i32x4*>(mine + (MATS * RB + 4 * t + g) * 1024 + 64 * r + 16 * (d ^ slot_swz(r)));
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
     __builtin_amdgcn_sched_barrier(0);
+    if (c0 + 4 * W < a.nch) issue(c0 + 4 * W);
 #pragma unroll
     for (int k = 0; k < MATS; ++k)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const i32x4 wb = decode16(cur[k][b][d]);
+          const i32x4 wb = decode16(wt[k][b][d]);
 #pragma unroll
           for (int t = 0; t < TB; ++t)
             acc[k][b][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb, qa[t][d], acc[k][b][t], 0, 0, 0);
         }
-#pragma unroll
-    for (int k = 0; k < MATS; ++k)
-#pragma unroll
-      for (int b = 0; b < RB; ++b) cur[k][b] = nxt[k][b];
   }
-  // lane (r, g), register v: row 16 b + 4 g + v, token 16 t + r
-#pragma unroll
-  for (int t = 0; t < TB; ++t) {
-    if (t) __syncthreads();
-#pragma unroll
-    for (int k = 0; k < MATS; ++k)
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) red[w][((k * RB + b) * 4 + v) * kRedStride + lane] = acc[k][b][t][v];
-    __syncthreads();
-    for (int o = threadIdx.x; o < 16 * RB * 16; o += 64 * W) {
-      const int row = o % (16 * RB), tok = o / (16 * RB);
-      const int64_t m = tok0 + 16 * t + tok;
-      if (m >= a.M || row0 + row >= a.N) continue;
-      int32_t sum[MATS];
-#pragma unroll
-      for (int k = 0; k < MATS; ++k) {
-        sum[k] = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-          sum[k] += red[i][((k * RB + row / 16) * 4 + row % 4) * kRedStride + 16 * (row % 16 / 4) + tok];
-      }
-      const int64_t i = row0 + row;
-      const float res = a.res ? load_g(a.res + m * a.ldr + i) : -0.0f;
-      store_g(a.y + m * a.ldy + i, output<MATS, ACT>(sum, row_ops<MATS>(a, i), load_g(a.z + m), load_g(a.s_act + m), res));
-    }
-  }
+  __syncthreads();  // (slots become sums)
+  join_rows<W, RB, TB, MATS, ACT>(a, row0, tok0, acc, reinterpret_cast<int32_t*>(lds));
 }
 
 // ---- many tokens: tiles -----------------------------------------------------
 
-typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // A workgroup of RG x KS waves computes ROWS rows (of each matrix) x TOK tokens:
 // wave (rg, ks) 64 rows (with a gate 32 of each matrix, so that its epilogue stays
@@ -236,8 +323,8 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // operands' LDS reads 134, with the loads 150; silu's 49 vector instructions per
 // output would take 26 by themselves and overlap with the other workgroup's products
 // in part, the 100 MB of y 15.  Two workgroups of four waves to a CU, whose products
-// and epilogues fall out of step.  Steps measured: operands from the L2 per 64 tokens
-// (the rows kernel) 740; tiles 220; fixed slots and silu without branches 209; sums
+// and epilogues fall out of step.  Steps measured: operands from the L2 per 32 tokens
+// (no tiles) 740; tiles 220; fixed slots and silu without branches 209; sums
 // through LDS to whole lines of y 198 (without a gate 127 -> 99); the products' waves
 // ahead of those in an epilogue (s_setprio) 194; decode in nine instructions instead
 // of eleven, tiles in groups 187.  Not kept (no gain): operands two groups ahead,
@@ -255,11 +342,6 @@ struct Tile {
   static constexpr int LDS = RING * SLOT > (KS > 1 ? WAVES * TB * 8192 : 0) ? RING * SLOT : WAVES * TB * 8192;
   static_assert(DMA * 8 * RG == TOK && 2 * (DMA + WL) < 64, "stage split");
 };
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
-}
 
 // swizzle of a token's eight 16-byte pieces of a stage: piece p sits at p ^
 // piece_swz(token), so that a 128-bit read of one piece of 8 or 16 tokens touches
@@ -512,18 +594,26 @@ hipError_t launch_tile(const EpilogueArgs& a, hipStream_t s) {
 }
 
 template <int W, int RB, int TB, int MATS, int ACT>
-hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
+hipError_t launch_stream(const EpilogueArgs& a, hipStream_t s) {
   const int64_t row_tiles = (a.N + 16 * RB - 1) / (16 * RB), tok_tiles = ((int64_t)a.M + 16 * TB - 1) / (16 * TB);
-  hipLaunchKernelGGL((epilogue_rows_kernel<W, RB, TB, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s,
-                     a, (int)row_tiles);
+  hipLaunchKernelGGL((epilogue_stream_kernel<W, RB, TB, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)),
+                     dim3(64 * W), 0, s, a, (int)row_tiles);
+  return hipGetLastError();
+}
+
+template <int W, int MATS, int ACT>
+hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
+  const int64_t row_tiles = (a.N + 15) / 16, tok_tiles = ((int64_t)a.M + 15) / 16;
+  hipLaunchKernelGGL((epilogue_rows_kernel<W, MATS, ACT>), dim3((unsigned)(row_tiles * tok_tiles)), dim3(64 * W), 0, s, a,
+                     (int)row_tiles);
   return hipGetLastError();
 }
 
 // The shapes of a call's workgroups, rows (of both matrices together in the tiles,
-// of each in the rows kernels) x tokens: ROWS_WIDE for few tokens and very many
-// rows, then from few tokens to many.
-enum Shape { ROWS_16, ROWS_32, TILE_SPLIT, TILE_64, TILE_128, ROWS_WIDE, SHAPES };
-constexpr int kShapeRows[SHAPES] = {16, 32, 128, 256, 256, 64}, kShapeTokens[SHAPES] = {16, 32, 64, 64, 128, 16};
+// of each otherwise) x tokens, those by estimated time from few tokens to many.
+enum Shape { STREAM_16, STREAM_16X32, STREAM_32, TILE_SPLIT, TILE_64, TILE_128, STREAM_WIDE, ROWS, SHAPES };
+constexpr int kShapeRows[SHAPES] = {16, 16, 32, 128, 256, 256, 64, 16};
+constexpr int kShapeTokens[SHAPES] = {16, 32, 32, 64, 64, 128, 16, 16};
 template <int MATS>
 using TileSplit = Tile<MATS, 2, 4, 2>;
 template <int MATS>
@@ -537,60 +627,71 @@ int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
   return ((a.N + rows - 1) / rows) * ((a.M + tokens - 1) / tokens);
 }
 
-// Whether a launch of the shape can count its threads (512 only where workgroups
-// are few) and, for tiles, reach a token block's rows by 32-bit offsets.
+// Whether a launch of the shape can count its threads (more than 256 only where
+// workgroups are few, or 512 in STREAM_16X32) and, but for ROWS, reach its tokens by
+// 32-bit offsets and read them by 16 bytes: up to 16 tokens' rows may end at K.
 bool shape_takes(int shape, const EpilogueArgs& a) {
-  if (shape >= TILE_SPLIT && shape <= TILE_128 && 128 * a.ldq >= (1ll << 31)) return false;
-  return shape_workgroups(shape, a) <= kMaxDispatchItems / 256;
+  if (shape != ROWS && ((a.M > 1 && a.ldq >= (1 << 24)) || (a.M <= 16 && a.K % 16 != 0))) return false;
+  return shape_workgroups(shape, a) <= kMaxDispatchItems / (shape == STREAM_16X32 ? 512 : 256);
 }
 
-// Up to 16 tokens take rows: 16 to a workgroup, for the most waves in flight, or
-// 64 from 16 such workgroups per CU on, where the activations that each reads
-// are what counts (151,936 x 4,096: 46 and 38 us for one token, 90 and 49 for 16;
-// gate and up of 12,288 x 12,288, six per CU: 21 and 27, 31 and 30).  More tokens
-// take the shape with the least estimated time: a start, and for each workgroup
-// that a CU gets in turn a time with a part proportional to K, as measured over
-// M = 16 .. 512 and K = 1,024 .. 12,288 (us, for 4,096 columns; without a gate,
-// with one).  Both sides of some borders, gate and up of 12,288 x 4,096: 32 tokens
-// in rows of 16, of 32 and split tiles 20.6, 16.9, 16.5; 64: 37, 22.4, 17.9 and
-// 21.3 in tiles of 64; 128: 70, 39, 30.5, 22.3; 512: tiles of 64 59.3, of 128 61.0;
-// 1,024: 113, 101.  4,096 x 12,288 with a residual: 64 tokens in rows of 32 17.7,
-// split 30.0; 256: 57.7, 30.8, tiles of 64 44.7; 512: 111, 35.9, 46.4, of 128 74.1.
+// Up to 16 tokens take 16 rows to a workgroup, for the most loads in flight, or 64
+// from six such workgroups per CU on, where the activations that each reads are what
+// counts (151,936 x 4,096: 47 and 36 us for one token, 68 and 44 for 16; 32,768 rows,
+// eight per CU: 10.9 and 9.3, 12.8 and 10.2; gate and up of 12,288 x 12,288, three: 18
+// and 24, 27.4 and 27.1).  More tokens take the shape with the least estimated time:
+// a start, and for each workgroup that a CU gets in turn a time with a part
+// proportional to K, as measured over M = 16 .. 512 and K = 1,024 .. 12,288 (us, for
+// 4,096 columns; without a gate, with one).  Some borders, in the order of the
+// shapes: gate and up of 12,288 x 4,096: 32 tokens 12.6, 12.9, 12.2, 16.5; 64: 21, 20.8,
+// 16.3, 16.2, 21.3; 128: 36, 36, 25.8, 30.5, 22.8; 512: tiles of 64 59.3, of 128 61.0;
+// 1,024: 113, 101.  4,096 x 12,288 with a residual: 32 tokens 10.0, 9.0, 10.1, 30; 64:
+// 16.5, 14.4, 10.3, 30; 128: 28, 23, 17, 32; 256: 50, 42, 28, 30.8, 44.7; 512: split 35.9,
+// 46.4, of 128 74.1.
 Shape pick_shape(const EpilogueArgs& a, int cus) {
-  static constexpr double kStart[] = {2, 3.5, 2, 2, 2}, kEach[] = {0.3, 0.5, 6.5, 5.5, 9};
-  static constexpr double kTime[2][5] = {{2.2, 4.4, 8, 12.4, 21}, {2.7, 5.4, 9, 13.5, 24.5}};
-  if (a.M <= 16) return shape_workgroups(ROWS_16, a) >= 16ll * cus ? ROWS_WIDE : ROWS_16;
+  static constexpr double kStart[] = {3.3, 3.6, 4, 2, 4, 2}, kEach[] = {0.2, 0.4, 0.6, 6.5, 5.5, 9};
+  static constexpr double kTime[2][6] = {{0.95, 1.75, 2.3, 8, 12.4, 21}, {1.2, 2.8, 3.1, 9, 13.5, 24.5}};
+  if (a.M <= 16) {
+    if (shape_workgroups(STREAM_16, a) >= 6ll * cus && shape_takes(STREAM_WIDE, a)) return STREAM_WIDE;
+    return shape_takes(STREAM_16, a) ? STREAM_16 : ROWS;
+  }
   const int gated = a.w[1].packed != nullptr;
-  int best = -1;
+  int best = ROWS;
   double least = 0;
-  for (int s = ROWS_16; s <= TILE_128; ++s) {
+  for (int s = STREAM_16; s <= TILE_128; ++s) {
     if (!shape_takes(s, a)) continue;
     const double turns = (double)((shape_workgroups(s, a) + cus - 1) / cus);
     const double t = kStart[s] + turns * (kEach[s] + kTime[gated][s] * a.K / 4096);
-    if (best < 0 || t < least) best = s, least = t;
+    if (best == ROWS || t < least) best = s, least = t;
   }
   return (Shape)best;
 }
 
-// Eight waves for a workgroup where there are few (4,096 x 12,288, one token: 6.2
-// us, with four 8.1), four where every CU has two (gate and up of 12,288 x 4,096:
-// 8.9 and 8.5).
-template <int RB, int TB, int MATS, int ACT>
-hipError_t launch_rows_by(const EpilogueArgs& a, int64_t workgroups, int cus, hipStream_t s) {
-  return workgroups < 2ll * cus ? launch_rows<8, RB, TB, MATS, ACT>(a, s) : launch_rows<4, RB, TB, MATS, ACT>(a, s);
-}
-
+// More waves for a workgroup where workgroups are few: 16 rows from three steps of
+// four waves on eight (4,096 x 4,096, one token: 3.7 us, four 3.9), from three of
+// eight on sixteen (4,096 x 12,288: four 8.7, eight 6.4, sixteen 5.7; gate and up of
+// 1,024 x 1,024: 3.5, 3.7, 4.4); 32 rows (4,096 x 12,288, 64 tokens: 12.0, eight 10.3;
+// 6,144 x 1,024: 4.8, 6.2; where a CU gets two, gate and up of 12,288 x 4,096, 12.2 and
+// 15.3); ROWS as measured there (4,096 x 12,288: 8.1, eight 6.2; with
+// two workgroups per CU 8.5, 8.9).
 template <int MATS, int ACT>
 hipError_t launch_act(const EpilogueArgs& a, int cus, hipStream_t s) {
   const Shape shape = pick_shape(a, cus);
   const int64_t n = shape_workgroups(shape, a);
+  const bool few = n < 2ll * cus, fewer = n <= cus;
+  const int steps = (a.nch + 3) / 4;
   switch (shape) {
-    case ROWS_16: return launch_rows_by<1, 1, MATS, ACT>(a, n, cus, s);
-    case ROWS_32: return launch_rows_by<2, 2, MATS, ACT>(a, n, cus, s);
+    case STREAM_16:
+      if (fewer && steps > 24) return launch_stream<16, 1, 1, MATS, ACT>(a, s);
+      return few && steps > 12 ? launch_stream<8, 1, 1, MATS, ACT>(a, s) : launch_stream<4, 1, 1, MATS, ACT>(a, s);
+    case STREAM_16X32: return launch_stream<8, 1, 2, MATS, ACT>(a, s);
+    case STREAM_32:
+      return fewer && steps > 12 ? launch_stream<8, 2, 2, MATS, ACT>(a, s) : launch_stream<4, 2, 2, MATS, ACT>(a, s);
     case TILE_SPLIT: return launch_tile<MATS, ACT, TileSplit<MATS>>(a, s);
     case TILE_64: return launch_tile<MATS, ACT, Tile64<MATS>>(a, s);
     case TILE_128: return launch_tile<MATS, ACT, Tile128<MATS>>(a, s);
-    default: return launch_rows<4, 4, 1, MATS, ACT>(a, s);
+    case STREAM_WIDE: return launch_stream<4, 4, 1, MATS, ACT>(a, s);
+    default: return few ? launch_rows<8, MATS, ACT>(a, s) : launch_rows<4, MATS, ACT>(a, s);
   }
 }
 
@@ -603,9 +704,8 @@ hipError_t launch_mats(const EpilogueArgs& a, int cus, hipStream_t s) {
 }  // namespace
 
 bool epilogue_takes(const EpilogueArgs& a) {
-  if (a.M <= 16) return shape_takes(ROWS_WIDE, a);
   bool any = false;
-  for (int s = ROWS_16; s <= TILE_128; ++s) any = any || shape_takes(s, a);
+  for (int s = STREAM_16; s < SHAPES; ++s) any = any || shape_takes(s, a);
   return any;
 }
 

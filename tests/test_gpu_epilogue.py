@@ -122,6 +122,22 @@ def test_large_odd_sizes(M, N, K, gate):
     run(M, N, K, gate=gate, act="silu", res="apart" if K % 2 else None, bias=K % 2 == 0, extra=K % 4, rows=pick)
 
 
+@pytest.mark.parametrize("M,N,K,gate", [
+    (1, 300, 16, True), (5, 300, 6416, True), (16, 1003, 12304, False), (9, 1003, 4112, True), (16, 330, 3344, False),
+    (16, 4001, 1040, True), (3, 9001, 112, False), (13, 9001, 1296, True), (2, 9001, 6160, False),
+    (1, 24593, 272, False), (7, 24593, 304, True), (16, 24593, 48, False),
+    (17, 1003, 4099, True), (33, 300, 6401, False), (40, 1003, 1009, True), (130, 2500, 1019, True),
+    (17, 4001, 4099, False), (32, 4001, 7001, False), (50, 2003, 4112, False),
+    (50, 4001, 4112, True), (64, 4001, 6403, False), (33, 2501, 6416, True),
+    (50, 9001, 4112, False), (300, 4001, 1019, False), (130, 4001, 2050, True), (300, 2501, 2049, True)])
+def test_streams(M, N, K, gate):
+    """The shapes whose waves share K (16 rows in four, eight and sixteen waves, 64
+    rows; 32 tokens, 32 rows x 32 tokens in four and eight waves): steps that some
+    waves have and others not, pieces and blocks that end inside, odd edges."""
+    pick = np.unique(np.r_[0:min(N, 70), N // 2: N // 2 + 30, N - 70: N])
+    run(M, N, K, gate=gate, act="silu", res="apart" if M % 2 else None, bias=M % 2 == 0, extra=M % 4, rows=pick)
+
+
 def test_strides_past_32_bits():
     """Rows of activations so far apart that a block of them passes 2^31 bytes,
     and outputs behind 2^31 elements."""
