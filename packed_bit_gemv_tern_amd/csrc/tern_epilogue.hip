@@ -207,14 +207,14 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
 // (the operands as they lie) gets 16 bytes a cycle, one whose four neighbours read
 // 64 bytes of one row 58 (measured: 393 KB to each CU in 9.8 and 3.1 us).  So DMA
 // instruction c brings 64 columns: lane 4 t + p piece p ^ swz(t) of token t, where
-// the operands' reads then touch every bank once; weights alike.
+// the operands' reads hardly meet on a bank; weights alike.
 //
 // Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 7.7,
 // 7.9 and 8.5 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.1,
 // 12.0); down, 4,096 x 12,288, 8 and 64 tokens 5.9 and 10.3 (7.9 and 17.5).  One slot
 // for a wave and many workgroups on a CU: with two slots 8.7, 8.9 and 9.5, with three
 // 9.7, 9.8 and 10.3.
-__device__ __forceinline__ int slot_swz(int row) { return (row >> 1) & 3; }
+__device__ __forceinline__ int slot_swz(int row) { return ((row >> 2) & 1) | ((row ^ (row >> 2)) & 2); }
 
 template <int W, int RB, int TB, int MATS, int ACT>
 __global__ __launch_bounds__(64 * W) void epilogue_stream_kernel(EpilogueArgs a, int row_tiles) {
@@ -611,18 +611,19 @@ hipError_t launch_rows(const EpilogueArgs& a, hipStream_t s) {
 
 // The shapes of a call's workgroups, rows (of both matrices together in the tiles,
 // of each otherwise) x tokens, those by estimated time from few tokens to many.
-enum Shape { STREAM_16, STREAM_16X32, STREAM_32, TILE_SPLIT, TILE_64, TILE_128, STREAM_WIDE, ROWS, SHAPES };
-constexpr int kShapeRows[SHAPES] = {16, 16, 32, 128, 256, 256, 64, 16};
-constexpr int kShapeTokens[SHAPES] = {16, 32, 32, 64, 64, 128, 16, 16};
+enum Shape { STREAM_16, STREAM_16X32, STREAM_32, SPLIT_64, SPLIT_128, TILE_64, TILE_128, STREAM_WIDE, ROWS, SHAPES };
+constexpr int kShapeRows[SHAPES] = {16, 16, 32, 64, 128, 256, 256, 64, 16};
+constexpr int kShapeTokens[SHAPES] = {16, 32, 32, 64, 64, 64, 128, 16, 16};
+using Split64 = Tile<1, 1, 4, 2>;
 template <int MATS>
-using TileSplit = Tile<MATS, 2, 4, 2>;
+using Split128 = Tile<MATS, 2, 4, 2>;
 template <int MATS>
 using Tile64 = Tile<MATS, 4, 1, 2>;
 template <int MATS>
 using Tile128 = Tile<MATS, 4, 1, 4>;
 
 int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
-  const bool tile = shape >= TILE_SPLIT && shape <= TILE_128;
+  const bool tile = shape >= SPLIT_64 && shape <= TILE_128;
   const int64_t rows = kShapeRows[shape] / (tile && a.w[1].packed ? 2 : 1), tokens = kShapeTokens[shape];
   return ((a.N + rows - 1) / rows) * ((a.M + tokens - 1) / tokens);
 }
@@ -632,6 +633,7 @@ int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
 // 32-bit offsets and read them by 16 bytes: up to 16 tokens' rows may end at K.
 bool shape_takes(int shape, const EpilogueArgs& a) {
   if (shape != ROWS && ((a.M > 1 && a.ldq >= (1 << 24)) || (a.M <= 16 && a.K % 16 != 0))) return false;
+  if (shape == SPLIT_64 && a.w[1].packed) return false;  // (with a gate never the fastest)
   return shape_workgroups(shape, a) <= kMaxDispatchItems / (shape == STREAM_16X32 ? 512 : 256);
 }
 
@@ -642,15 +644,17 @@ bool shape_takes(int shape, const EpilogueArgs& a) {
 // and 24, 27.4 and 27.1).  More tokens take the shape with the least estimated time:
 // a start, and for each workgroup that a CU gets in turn a time with a part
 // proportional to K, as measured over M = 16 .. 512 and K = 1,024 .. 12,288 (us, for
-// 4,096 columns; without a gate, with one).  Some borders, in the order of the
-// shapes: gate and up of 12,288 x 4,096: 32 tokens 12.6, 12.9, 12.2, 16.5; 64: 21, 20.8,
-// 16.3, 16.2, 21.3; 128: 36, 36, 25.8, 30.5, 22.8; 512: tiles of 64 59.3, of 128 61.0;
-// 1,024: 113, 101.  4,096 x 12,288 with a residual: 32 tokens 10.0, 9.0, 10.1, 30; 64:
-// 16.5, 14.4, 10.3, 30; 128: 28, 23, 17, 32; 256: 50, 42, 28, 30.8, 44.7; 512: split 35.9,
-// 46.4, of 128 74.1.
+// 4,096 columns; without a gate, with one).  Both sides of some borders, weights
+// from memory, gate and up of 12,288 x 4,096: 32 tokens in rows of 32 13.9, split by 128
+// 15.9; 64: 17.3, split by 64 23.5, by 128 17.7; 96: 22.8, tiles of 64 26.5; 128: 27.2, split
+// 34 and 31.9, tiles 27.3; 256: 47, tiles of 128 39.5; 512: tiles of 64 59.3, of 128 61.0;
+// 1,024: 113, 101.  4,096 x 12,288 with a residual: 32 tokens in rows of 16 x 32 8.3, of 32
+// 9.4; 128: 19.8, split by 64 25.6; 192: 26.8, 25.9; 256: 34.0, 26.8, by 128 33.8; 512: 50, 37.0,
+// tiles of 64 46.4, of 128 74.1.
 Shape pick_shape(const EpilogueArgs& a, int cus) {
-  static constexpr double kStart[] = {3.3, 3.6, 4, 2, 4, 2}, kEach[] = {0.2, 0.4, 0.6, 6.5, 5.5, 9};
-  static constexpr double kTime[2][6] = {{0.95, 1.75, 2.3, 8, 12.4, 21}, {1.2, 2.8, 3.1, 9, 13.5, 24.5}};
+  static constexpr double kStart[2][7] = {{3.3, 3.6, 3.3, 3, 2, 4, 2}, {3.3, 3.6, 5, 0, 2, 4, 2}};
+  static constexpr double kEach[2][7] = {{0.2, 0.4, 0.1, 4, 6.5, 5.5, 9}, {0.2, 0.4, 0.6, 0, 6.5, 5.5, 9}};
+  static constexpr double kTime[2][7] = {{0.95, 1.75, 2.45, 6.4, 8, 12.4, 21}, {1.2, 2.8, 2.75, 0, 9, 13.5, 24.5}};
   if (a.M <= 16) {
     if (shape_workgroups(STREAM_16, a) >= 6ll * cus && shape_takes(STREAM_WIDE, a)) return STREAM_WIDE;
     return shape_takes(STREAM_16, a) ? STREAM_16 : ROWS;
@@ -661,7 +665,7 @@ Shape pick_shape(const EpilogueArgs& a, int cus) {
   for (int s = STREAM_16; s <= TILE_128; ++s) {
     if (!shape_takes(s, a)) continue;
     const double turns = (double)((shape_workgroups(s, a) + cus - 1) / cus);
-    const double t = kStart[s] + turns * (kEach[s] + kTime[gated][s] * a.K / 4096);
+    const double t = kStart[gated][s] + turns * (kEach[gated][s] + kTime[gated][s] * a.K / 4096);
     if (best == ROWS || t < least) best = s, least = t;
   }
   return (Shape)best;
@@ -687,7 +691,10 @@ hipError_t launch_act(const EpilogueArgs& a, int cus, hipStream_t s) {
     case STREAM_16X32: return launch_stream<8, 1, 2, MATS, ACT>(a, s);
     case STREAM_32:
       return fewer && steps > 12 ? launch_stream<8, 2, 2, MATS, ACT>(a, s) : launch_stream<4, 2, 2, MATS, ACT>(a, s);
-    case TILE_SPLIT: return launch_tile<MATS, ACT, TileSplit<MATS>>(a, s);
+    case SPLIT_64:
+      if constexpr (MATS == 1) return launch_tile<MATS, ACT, Split64>(a, s);
+      return hipErrorInvalidValue;  // (not taken with a gate)
+    case SPLIT_128: return launch_tile<MATS, ACT, Split128<MATS>>(a, s);
     case TILE_64: return launch_tile<MATS, ACT, Tile64<MATS>>(a, s);
     case TILE_128: return launch_tile<MATS, ACT, Tile128<MATS>>(a, s);
     case STREAM_WIDE: return launch_stream<4, 4, 1, MATS, ACT>(a, s);

@@ -129,11 +129,14 @@ def test_large_odd_sizes(M, N, K, gate):
     (17, 1003, 4099, True), (33, 300, 6401, False), (40, 1003, 1009, True), (130, 2500, 1019, True),
     (17, 4001, 4099, False), (32, 4001, 7001, False), (50, 2003, 4112, False),
     (50, 4001, 4112, True), (64, 4001, 6403, False), (33, 2501, 6416, True),
-    (50, 9001, 4112, False), (300, 4001, 1019, False), (130, 4001, 2050, True), (300, 2501, 2049, True)])
+    (50, 9001, 4112, False), (300, 4001, 1019, False), (130, 4001, 2050, True), (300, 2501, 2049, True),
+    (250, 4001, 4099, False), (256, 4001, 12304, False), (200, 4001, 7001, True), (200, 2003, 2047, True),
+    (1100, 1003, 1019, False)])
 def test_streams(M, N, K, gate):
     """The shapes whose waves share K (16 rows in four, eight and sixteen waves, 64
-    rows; 32 tokens, 32 rows x 32 tokens in four and eight waves): steps that some
-    waves have and others not, pieces and blocks that end inside, odd edges."""
+    rows; 32 tokens, 32 rows x 32 tokens in four and eight waves; tiles of 64 rows):
+    steps that some waves have and others not, pieces and blocks that end inside,
+    odd edges."""
     pick = np.unique(np.r_[0:min(N, 70), N // 2: N // 2 + 30, N - 70: N])
     run(M, N, K, gate=gate, act="silu", res="apart" if M % 2 else None, bias=M % 2 == 0, extra=M % 4, rows=pick)
 
