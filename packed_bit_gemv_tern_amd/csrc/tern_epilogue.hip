@@ -209,11 +209,11 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
 // instruction c brings 64 columns: lane 4 t + p piece p ^ swz(t) of token t, where
 // the operands' reads hardly meet on a bank; weights alike.
 //
-// Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 7.7,
-// 7.9 and 8.5 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.1,
-// 12.0); down, 4,096 x 12,288, 8 and 64 tokens 5.9 and 10.3 (7.9 and 17.5).  One slot
-// for a wave and many workgroups on a CU: with two slots 8.7, 8.9 and 9.5, with three
-// 9.7, 9.8 and 10.3.
+// Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 8.1,
+// 9.0 and 10.3 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.3,
+// 12.3); down, 4,096 x 12,288, 8 and 64 tokens 5.0 and 11.0 (7.4 and 17.5).  One slot
+// for a wave and many workgroups on a CU: 7.8, 8.0 and 8.5 with the weights in the
+// last-level cache, with two slots 8.7, 8.9 and 9.6, with three 9.7, 9.8 and 10.3.
 __device__ __forceinline__ int slot_swz(int row) { return ((row >> 2) & 1) | ((row ^ (row >> 2)) & 2); }
 
 template <int W, int RB, int TB, int MATS, int ACT>
