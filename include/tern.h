@@ -712,6 +712,8 @@ int tern_kv_reserve(const tern_kv_pool* pool, const int32_t* len, const int32_t*
  *   from, to  device, `moves` int32 each (written): the pages' old and new ids, -1
  *             and -1 past the last: for tern_kv_copy;
  *   live      device, one int32 (written): the number of pages in use.
+ * They are written for a pool without rows (S = 0; table and len are not used
+ * then) too; with refs NULL as well there is no pool, and nothing is touched.
  */
 int tern_kv_compact(const tern_kv_pool* pool, const int32_t* len, int32_t* from, int32_t* to, int64_t moves,
                     int32_t* live, void* workspace, int64_t workspace_bytes, hipStream_t stream);

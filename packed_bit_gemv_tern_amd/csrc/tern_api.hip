@@ -599,9 +599,14 @@ int tern_kv_compact(const tern_kv_pool* pool, const int32_t* len, int32_t* from,
   if (st != TERN_OK) return st;
   if (moves < 0) return TERN_ERR_INVALID_ARG;
   if (moves > kI32Max) return TERN_ERR_RANGE;
-  if (p.S == 0) return TERN_OK;
-  if (p.pages < 1 || p.ld_table < 1) return TERN_ERR_INVALID_ARG;
-  if ((st = check_pool_buffers(p, {len, live})) != TERN_OK) return st;
+  if (p.S == 0) {  // no rows, but live and the lists are written all the same
+    if (!p.refs) return TERN_OK;
+    if (!live) return TERN_ERR_INVALID_ARG;
+    if (!aligned(p.refs, 4) || !aligned(live, 4)) return TERN_ERR_ALIGNMENT;
+  } else {
+    if (p.pages < 1 || p.ld_table < 1) return TERN_ERR_INVALID_ARG;
+    if ((st = check_pool_buffers(p, {len, live})) != TERN_OK) return st;
+  }
   if (moves > 0 && (!from || !to)) return TERN_ERR_INVALID_ARG;
   if (!aligned(from, 4) || !aligned(to, 4)) return TERN_ERR_ALIGNMENT;
   if (!pool_workspace_ok(p, workspace, workspace_bytes)) return TERN_ERR_WORKSPACE;

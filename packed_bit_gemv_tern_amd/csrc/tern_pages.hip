@@ -384,7 +384,7 @@ __global__ __launch_bounds__(T) void compact_plan_kernel(PoolArgs p, const int32
   const int64_t id0 = ((int64_t)blockIdx.x * T + t) * kEach;
   int32_t held[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) held[i] = load_g(p.refs + min(id0 + i, p.pages - 1));
+  for (int i = 0; i < kEach; ++i) held[i] = p.pages > 0 ? load_g(p.refs + min(id0 + i, p.pages - 1)) : 0;
   uint32_t mask = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) mask |= (uint32_t)(id0 + i < p.pages && held[i] > 0) << i;
@@ -535,8 +535,10 @@ hipError_t launch_kv_compact(const PoolArgs& p, const int32_t* len, int32_t* fro
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   // (no more than pages / 2 of the listed moves are in use)
-  hipLaunchKernelGGL(compact_apply_kernel, dim3((unsigned)(p.S + (std::min(moves, p.pages) + kPoolT - 1) / kPoolT)),
-                     dim3(kPoolT), 0, s, p, len, from, to, moves, rank, live);
+  const int64_t apply = p.S + (std::min(moves, p.pages) + kPoolT - 1) / kPoolT;
+  if (apply == 0) return hipSuccess;
+  hipLaunchKernelGGL(compact_apply_kernel, dim3((unsigned)apply), dim3(kPoolT), 0, s, p, len, from, to, moves, rank,
+                     live);
   return hipGetLastError();
 }
 
