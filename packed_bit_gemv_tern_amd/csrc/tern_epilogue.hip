@@ -628,13 +628,17 @@ int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
   return ((a.N + rows - 1) / rows) * ((a.M + tokens - 1) / tokens);
 }
 
-// Whether a launch of the shape can count its threads (more than 256 only where
-// workgroups are few, or 512 in STREAM_16X32) and, but for ROWS, reach its tokens by
-// 32-bit offsets and read them by 16 bytes: up to 16 tokens' rows may end at K.
+// Whether pick_shape may pick the shape (up to 16 tokens: 16 or 64 rows, or ROWS;
+// more: one by estimated time, or ROWS): whether a launch of it can count its threads
+// (512 in STREAM_16X32 and SPLIT_128, otherwise more than 256 only where workgroups
+// are few) and, but for ROWS, reach its tokens by 32-bit offsets and read them by 16
+// bytes: up to 16 tokens' rows may end at K.
 bool shape_takes(int shape, const EpilogueArgs& a) {
-  if (shape != ROWS && ((a.M > 1 && a.ldq >= (1 << 24)) || (a.M <= 16 && a.K % 16 != 0))) return false;
+  const bool listed = a.M <= 16 ? shape == STREAM_16 || shape == STREAM_WIDE : shape <= TILE_128;
+  if (shape != ROWS && (!listed || (a.M > 1 && a.ldq >= (1 << 24)) || (a.M <= 16 && a.K % 16 != 0))) return false;
   if (shape == SPLIT_64 && a.w[1].packed) return false;  // (with a gate never the fastest)
-  return shape_workgroups(shape, a) <= kMaxDispatchItems / (shape == STREAM_16X32 ? 512 : 256);
+  const int threads = shape == STREAM_16X32 || shape == SPLIT_128 ? 512 : 256;
+  return shape_workgroups(shape, a) <= kMaxDispatchItems / threads;
 }
 
 // Up to 16 tokens take 16 rows to a workgroup, for the most loads in flight, or 64
@@ -656,7 +660,8 @@ Shape pick_shape(const EpilogueArgs& a, int cus) {
   static constexpr double kEach[2][7] = {{0.2, 0.4, 0.1, 4, 6.5, 5.5, 9}, {0.2, 0.4, 0.6, 0, 6.5, 5.5, 9}};
   static constexpr double kTime[2][7] = {{0.95, 1.75, 2.45, 6.4, 8, 12.4, 21}, {1.2, 2.8, 2.75, 0, 9, 13.5, 24.5}};
   if (a.M <= 16) {
-    if (shape_workgroups(STREAM_16, a) >= 6ll * cus && shape_takes(STREAM_WIDE, a)) return STREAM_WIDE;
+    const bool wide = shape_workgroups(STREAM_16, a) >= 6ll * cus || !shape_takes(STREAM_16, a);
+    if (wide && shape_takes(STREAM_WIDE, a)) return STREAM_WIDE;
     return shape_takes(STREAM_16, a) ? STREAM_16 : ROWS;
   }
   const int gated = a.w[1].packed != nullptr;

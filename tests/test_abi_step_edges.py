@@ -1,8 +1,11 @@
 """Calls at the borders of the lookup's, rotation's, epilogue's and pages' checks:
 status codes before any launch (no GPU needed: nothing below gets past them)."""
 
+import pytest
+
 from packed_bit_gemv_tern_amd import tern
-from test_abi_step import A16, ALIGN, INVALID, ODD2, OK, WORKSPACE, compact, lib, pool  # noqa: F401
+from test_abi_step import (A16, ALIGN, INVALID, ODD2, OK, RANGE, WORKSPACE, compact, lib, linear, pool,  # noqa: F401
+                           weights)
 
 
 def test_compact_without_rows(lib):  # noqa: F811
@@ -17,3 +20,13 @@ def test_compact_without_rows(lib):  # noqa: F811
     for kw in ({"ws": None}, {"ws": A16 + 16}, {"n": 64}):
         assert compact(lib, pool(**none), **kw) == WORKSPACE, kw
     assert compact(lib, pool(refs=None, **none), live=None, ws=None) == OK
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+@pytest.mark.parametrize("gate", [False, True])
+def test_linear_epilogue_rows_that_no_launch_counts(lib, M, gate):  # noqa: F811
+    """Up to 16 tokens take 64 rows to a workgroup at most, more could take 256: from
+    2^30 rows on no launch of the former counts its threads."""
+    up = weights() if gate else None
+    for N in (2 ** 30, 2 ** 30 + 1, 2 ** 31 - 1000):
+        assert linear(lib, up=up, N=N, M=M, ldr=N, ldy=N) == RANGE, N
