@@ -456,7 +456,7 @@ int tern_head_gemv(const int8_t* W, const float* s_row, const int32_t* rowsum, i
  * The activations only see finite values if scales, biases and inputs are.
  *   w, up  host structures of device arrays: packed (N rows of
  *          tern_row_bytes(K) bytes, 16-byte aligned), s_row, rowsum (N each)
- *          and bias (N floats, or NULL);  up NULL: no gate;
+ *          and bias (N floats, or NULL), N at most 2^31 - 256;  up NULL: no gate;
  *   q, ldq, s_act, z, y, ldy  as for tern_gemm_smallM, any M;
  *   res    device, M x N floats, row stride ldr >= N (when M > 1), or NULL; may
  *          be y itself (same address and stride: in place), and must not

@@ -716,6 +716,7 @@ hipError_t launch_mats(const EpilogueArgs& a, int cus, hipStream_t s) {
 }  // namespace
 
 bool epilogue_takes(const EpilogueArgs& a) {
+  if (a.N > INT32_MAX - 255) return false;  // (rows are int32 as far as the last tile of 256 reaches)
   bool any = false;
   for (int s = STREAM_16; s < SHAPES; ++s) any = any || shape_takes(s, a);
   return any;

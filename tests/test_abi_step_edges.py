@@ -30,3 +30,10 @@ def test_linear_epilogue_rows_that_no_launch_counts(lib, M, gate):  # noqa: F811
     up = weights() if gate else None
     for N in (2 ** 30, 2 ** 30 + 1, 2 ** 31 - 1000):
         assert linear(lib, up=up, N=N, M=M, ldr=N, ldy=N) == RANGE, N
+
+
+@pytest.mark.parametrize("M", [17, 64, 128])
+def test_linear_epilogue_rows_of_the_last_tile(lib, M):  # noqa: F811
+    """Row numbers are 32 bits wide: the last tile's may not pass them."""
+    for N in (2 ** 31 - 255, 2 ** 31 - 1):
+        assert linear(lib, N=N, M=M, ldr=N, ldy=N) == RANGE, N
