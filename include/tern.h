@@ -644,10 +644,18 @@ int tern_qk_norm_rope(const tern_kv_batch* batch, int64_t head_dim, const float*
  * number of entries that hold page p (0: free); the calls below keep it, and a
  * fresh pool is refs of zeros.  A page may be held by several rows (a prompt that
  * several answers share); nothing writes into a page that others hold, if
- * tern_kv_reserve precedes every tern_kv_append.  Per step:
+ * tern_kv_reserve precedes every tern_kv_append and that takes nothing of a row
+ * that was refused.  Per step, now, kept and the rest device arrays:
  *     want = len + new tokens;  tern_kv_reserve(len, want);  tern_kv_copy of what
- *     it lists, in every layer;  append and attention with length want;  after
- *     verification tern_kv_truncate(want, kept).
+ *     it lists, in every layer;  now = granted ? want : 0;  rotation, append and
+ *     attention with length now;  after verification tern_kv_truncate(now, kept);
+ *     then len = granted ? min(now, kept) : len.
+ * A refused row keeps the pages it has, a part-filled one that others hold among
+ * them, and gets none: length want would write its new tokens there, the old len
+ * over its last ones, and tern_kv_truncate(want, ..) would give up what stands in
+ * entries that it never had.  Length 0 makes it an idle slot (its rows of q and k
+ * are left, nothing is appended, its attention is 0) that keeps its pages and can
+ * ask again, shorter or after others have ended.
  *   refs   device, pages int32;  table  device, S x ld_table int32;
  *   page_tokens 16, 32, 64 or 128 (otherwise TERN_ERR_UNSUPPORTED).
  * len (device, S int32) is the number of tokens that a row has pages for: what
@@ -697,7 +705,8 @@ int tern_kv_truncate(const tern_kv_pool* pool, const int32_t* len, const int32_t
  * needs a page or keeps a shared one, gets nothing.  A row that wants more tokens than the
  * table has pages for gets nothing, and needs none.
  *   want     device, S int32;
- *   granted  device, S int32 (written): 1, or 0 for a row that got nothing;
+ *   granted  device, S int32 (written): 1, or 0 for a row that got nothing, whose
+ *            new tokens have no place (see above: an idle slot in this step);
  *   from, to device, S int32 each (written): row s's part-filled page and its
  *            copy, -1 and -1 without one: for tern_kv_copy.
  */

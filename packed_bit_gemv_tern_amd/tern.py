@@ -390,7 +390,9 @@ def tern_kv_truncate(pool, length, keep, stream=None):
 
 def tern_kv_reserve(pool, length, want, granted, src, dst, workspace, stream=None):
     """src, dst: the pages to copy (tern_kv_copy's from and to), S each.
-    workspace: a device tensor of tern_kv_pool_workspace_bytes bytes."""
+    workspace: a device tensor of tern_kv_pool_workspace_bytes bytes.  A row with
+    granted 0 has no place for its new tokens: the step goes on with the length
+    want * granted (an idle slot), not want."""
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_lib().tern_kv_reserve(ctypes.byref(pool), _ptr(length), _ptr(want), _ptr(granted), _ptr(src), _ptr(dst),
                                   _ptr(workspace), nbytes, _stream(stream)), "tern_kv_reserve")
