@@ -104,6 +104,14 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
+// LDS accesses of a wave's lanes on both sides stay in this order: the LDS serves a
+// wave's instructions as they come, so only the compiler has to be told (no
+// instruction comes of it).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 constexpr int kRedStride = 68;  // of 64 lanes' values of one register, off each other's banks
 
 // The sums of W waves and the epilogue: lane (r, g), register v of a block of
@@ -579,7 +587,10 @@ void epilogue_tile_kernel(EpilogueArgs a, int row_tiles, int tok_tiles) {
   } else {
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
+      // (put writes what other lanes of the wave have read, and they read what it writes)
+      wave_order();
       put(t);
+      wave_order();
       finish(t, 0);
     }
   }
