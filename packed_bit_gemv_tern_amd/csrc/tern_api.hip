@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <map>
 #include <mutex>
@@ -506,7 +507,7 @@ int tern_linear_epilogue(const tern_weights* w, const tern_weights* up, int64_t 
 int tern_embed(const int8_t* W, const float* s_row, int64_t N, int64_t K, int64_t ldw, const int32_t* ids, int64_t M,
                float scale, float* x, int64_t ldx, hipStream_t stream) {
   if (N < 1 || K < 1 || M < 0 || ldw < K || (M > 1 && ldx < K)) return TERN_ERR_INVALID_ARG;
-  if (!(scale > -3.4e38f && scale < 3.4e38f)) return TERN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return TERN_ERR_INVALID_ARG;
   if (N > kI32Max || K > TERN_MAX_K || embed_work_items(M, K) > kMaxDispatchItems) return TERN_ERR_RANGE;
   if (M == 0) return TERN_OK;
   if (!W || !s_row || !ids || !x) return TERN_ERR_INVALID_ARG;
@@ -523,7 +524,7 @@ int tern_qk_norm_rope(const tern_kv_batch* b, int64_t head_dim, const float* inv
   if (!b || b->S < 0 || b->rows < 0 || b->max_new < 0 || q_heads < 0 || heads < 0) return TERN_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return TERN_ERR_UNSUPPORTED;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0) return TERN_ERR_UNSUPPORTED;
-  if (!(eps > 0.0f) || eps > 3.4e38f || !(magnitude > -3.4e38f && magnitude < 3.4e38f)) return TERN_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(magnitude)) return TERN_ERR_INVALID_ARG;
   if (b->S > kI32Max || b->rows > kI32Max || b->max_new > kI32Max || q_heads > 65536 || heads > 65536)
     return TERN_ERR_RANGE;
   RopeArgs a;

@@ -4,8 +4,10 @@ status codes before any launch (no GPU needed: nothing below gets past them)."""
 import pytest
 
 from packed_bit_gemv_tern_amd import tern
-from test_abi_step import (A16, ALIGN, INVALID, ODD2, OK, RANGE, WORKSPACE, compact, lib, linear, pool,  # noqa: F401
-                           weights)
+from test_abi_step import (A16, ALIGN, INF, INVALID, NAN, ODD2, OK, RANGE, WORKSPACE, batch, compact, embed,  # noqa: F401
+                           lib, linear, pool, rope, weights)
+
+FLT_MAX = (2 - 2 ** -23) * 2.0 ** 127
 
 
 def test_compact_without_rows(lib):  # noqa: F811
@@ -37,3 +39,15 @@ def test_linear_epilogue_rows_of_the_last_tile(lib, M):  # noqa: F811
     """Row numbers are 32 bits wide: the last tile's may not pass them."""
     for N in (2 ** 31 - 255, 2 ** 31 - 1):
         assert linear(lib, N=N, M=M, ldr=N, ldy=N) == RANGE, N
+
+
+def test_every_finite_scale(lib):  # noqa: F811
+    """Up to the largest float, and nothing past it (empty calls: nothing is launched)."""
+    none = dict(b=batch(max_new=0))
+    for x in (3.401e38, FLT_MAX, 2.0 ** -149):
+        assert embed(lib, M=0, scale=x) == OK and embed(lib, M=0, scale=-x) == OK
+        assert rope(lib, mag=x, **none) == OK and rope(lib, mag=-x, **none) == OK and rope(lib, eps=x, **none) == OK
+        assert rope(lib, eps=-x, **none) == INVALID
+    for x in (INF, -INF, NAN):
+        assert embed(lib, M=0, scale=x) == INVALID
+        assert rope(lib, mag=x, **none) == INVALID and rope(lib, eps=x, **none) == INVALID
