@@ -145,7 +145,9 @@ int tern_gemv(const uint8_t* packed, const float* s_row, const int32_t* rowsum, 
  * tern_gemm_smallM -- M tokens against the same packed weights (the batched
  * verify pass of drafted decoding and prefill-sized batches: wiki entry
  * "Neutrino-1", "What is actually new here"; models page "Neutrino-1 0.6B").
- *   q      device, M x K int8, row stride ldq >= K (multiple of 16 when M > 1);
+ *   q      device, M x K int8, row stride ldq >= K (multiple of 16 when M > 1;
+ *          then every row, the last too, is ldq bytes of memory: those behind K
+ *          may be read, and their values do not matter);
  *   s_act  device, M floats;  z  device, M int32;
  *   y      device, M x N floats, row stride ldy >= N (written);
  *   acc    device, M x N int32 with the same stride ldy (written) or NULL;

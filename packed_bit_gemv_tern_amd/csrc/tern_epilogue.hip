@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * W) void epilogue_stream_kernel(EpilogueArgs a,
 #pragma unroll
   for (int k = 0; k < MATS; ++k)
     wres[k] = uniform_rsrc(a.w[k].packed + (int64_t)row0 * a.ld, (uint32_t)here * (uint32_t)a.ld);
-  const uint32_t kbytes = ((uint32_t)a.K + 15) & ~15u;  // (inside ldq, or K itself: stream_takes)
+  const uint32_t kbytes = ((uint32_t)a.K + 15) & ~15u;  // (inside ldq, or K itself: shape_takes)
   const __amdgpu_buffer_rsrc_t qres =
       uniform_rsrc(a.q + tok0 * a.ldq, (uint32_t)(toks - 1) * (uint32_t)a.ldq + kbytes);
   const int lr = lane >> 2, lp = (lane & 3) ^ slot_swz(lr);
@@ -643,7 +643,8 @@ int64_t shape_workgroups(int shape, const EpilogueArgs& a) {
 // more: one by estimated time, or ROWS): whether a launch of it can count its threads
 // (512 in STREAM_16X32 and SPLIT_128, otherwise more than 256 only where workgroups
 // are few) and, but for ROWS, reach its tokens by 32-bit offsets and read them by 16
-// bytes: up to 16 tokens' rows may end at K.
+// bytes: one token's row ends at K (those of 2 to 16 could be read on to ldq, as those
+// of more are, but go the same way).
 bool shape_takes(int shape, const EpilogueArgs& a) {
   const bool listed = a.M <= 16 ? shape == STREAM_16 || shape == STREAM_WIDE : shape <= TILE_128;
   if (shape != ROWS && (!listed || (a.M > 1 && a.ldq >= (1 << 24)) || (a.M <= 16 && a.K % 16 != 0))) return false;
