@@ -382,9 +382,11 @@ __global__ __launch_bounds__(T) void compact_plan_kernel(PoolArgs p, const int32
   const int t = threadIdx.x;
   int64_t before = 0, live = 0, total;
   const int64_t id0 = ((int64_t)blockIdx.x * T + t) * kEach;
-  int32_t held[kEach];
+  int32_t held[kEach] = {};
+  if (p.pages > 0) {
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) held[i] = p.pages > 0 ? load_g(p.refs + min(id0 + i, p.pages - 1)) : 0;
+    for (int i = 0; i < kEach; ++i) held[i] = load_g(p.refs + min(id0 + i, p.pages - 1));
+  }
   uint32_t mask = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) mask |= (uint32_t)(id0 + i < p.pages && held[i] > 0) << i;
