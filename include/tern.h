@@ -456,6 +456,8 @@ int tern_head_gemv(const int8_t* W, const float* s_row, const int32_t* rowsum, i
  * linear gives what the two linears and that gate give, bit for bit;
  * TERN_ACT_GELU, the tanh form x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
  * The activations only see finite values if scales, biases and inputs are.
+ * A linear with nothing behind it is tern_gemm_smallM's y, bit for bit, and from two
+ * tokens on comes sooner from here; tern_gemv is for one, tern_gemm_smallM for acc.
  *   w, up  host structures of device arrays: packed (N rows of
  *          tern_row_bytes(K) bytes, 16-byte aligned), s_row, rowsum (N each)
  *          and bias (N floats, or NULL), N at most 2^31 - 256;  up NULL: no gate;

@@ -217,11 +217,13 @@ __global__ __launch_bounds__(64 * W) void epilogue_rows_kernel(EpilogueArgs a, i
 // instruction c brings 64 columns: lane 4 t + p piece p ^ swz(t) of token t, where
 // the operands' reads hardly meet on a bank; weights alike.
 //
-// Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 8.1,
-// 9.0 and 10.3 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.3,
-// 12.3); down, 4,096 x 12,288, 8 and 64 tokens 5.0 and 11.0 (7.4 and 17.5).  One slot
-// for a wave and many workgroups on a CU: 7.8, 8.0 and 8.5 with the weights in the
-// last-level cache, with two slots 8.7, 8.9 and 9.6, with three 9.7, 9.8 and 10.3.
+// Gate and up of 12,288 x 4,096, 25 MB of weights from memory, 1, 8 and 16 tokens: 8.5,
+// 8.7 and 10.1 us, of which 2.3 are the launch (operands loaded as they lie 8.1, 10.3,
+// 12.3); down, 4,096 x 12,288, 8 and 64 tokens 6.3 and 11.6, with the weights in the
+// last-level cache 5.0 and 11.0 (as they lie 7.4 and 17.5 there).  One slot for a wave
+// and many workgroups on a CU: 7.8, 8.0 and 8.5 with the weights in the last-level
+// cache, with two slots 8.7, 8.9 and 9.6, with three 9.7, 9.8 and 10.3 (not measured
+// with the weights from memory).
 __device__ __forceinline__ int slot_swz(int row) { return ((row >> 2) & 1) | ((row ^ (row >> 2)) & 2); }
 
 template <int W, int RB, int TB, int MATS, int ACT>
@@ -324,8 +326,8 @@ __global__ __launch_bounds__(64 * W) void epilogue_stream_kernel(EpilogueArgs a,
 // one before is free.
 //
 // What bounds it, gate and up of 12,288 x 4,096 for 2,048 tokens (412 Gops; a
-// library's int8 product of that size alone takes 209 us): 184 to 192 us, 2.2 POPS
-// (down, 4,096 x 12,288, 77 us and 2.7: fewer outputs per operation).  The matrix
+// library's int8 product of that size alone takes 209 us): 192 us, 184 to 194 on
+// different cards, 2.1 POPS (down, 4,096 x 12,288, 96 us and 2.2).  The matrix
 // cores are busy in 66 % of each SIMD's cycles, and the card holds 1.5 GHz under
 // them: the matrix instructions by themselves take 125 us, with the decode and the
 // operands' LDS reads 134, with the loads 150; silu's 49 vector instructions per
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(64 * W) void epilogue_stream_kernel(EpilogueArgs a,
 // (no tiles) 740; tiles 220; fixed slots and silu without branches 209; sums
 // through LDS to whole lines of y 198 (without a gate 127 -> 99); the products' waves
 // ahead of those in an epilogue (s_setprio) 194; decode in nine instructions instead
-// of eleven, tiles in groups 187.  Not kept (no gain): operands two groups ahead,
+// of eleven, tiles in groups 187 on that card.  Not kept (no gain): operands two groups ahead,
 // weights by 64 bytes of a row and lane swaps (5 % for tiles with K split, whole
 // stages lost at small K), priorities by the workgroup's place on its CU; and
 // non-temporal stores of y (1 us less here, 9 more for the quantiser that reads y
@@ -655,18 +657,19 @@ bool shape_takes(int shape, const EpilogueArgs& a) {
 
 // Up to 16 tokens take 16 rows to a workgroup, for the most loads in flight, or 64
 // from six such workgroups per CU on, where the activations that each reads are what
-// counts (151,936 x 4,096: 47 and 36 us for one token, 68 and 44 for 16; 32,768 rows,
-// eight per CU: 10.9 and 9.3, 12.8 and 10.2; gate and up of 12,288 x 12,288, three: 18
-// and 24, 27.4 and 27.1).  More tokens take the shape with the least estimated time:
+// counts (weights from memory, 151,936 x 4,096: 43 and 34.5 us for one token, 67 and 42
+// for 16; 32,768 rows, eight per CU: 12.6 and 10.6, 16.3 and 12.0; gate and up of 12,288
+// x 12,288, three: 19.3 and 24.7, 26.3 and 26.3).  More tokens take the shape with the least estimated time:
 // a start, and for each workgroup that a CU gets in turn a time with a part
 // proportional to K, as measured over M = 16 .. 512 and K = 1,024 .. 12,288 (us, for
 // 4,096 columns; without a gate, with one).  Both sides of some borders, weights
-// from memory, gate and up of 12,288 x 4,096: 32 tokens in rows of 32 13.9, split by 128
-// 15.9; 64: 17.3, split by 64 23.5, by 128 17.7; 96: 22.8, tiles of 64 26.5; 128: 27.2, split
-// 34 and 31.9, tiles 27.3; 256: 47, tiles of 128 39.5; 512: tiles of 64 59.3, of 128 61.0;
-// 1,024: 113, 101.  4,096 x 12,288 with a residual: 32 tokens in rows of 16 x 32 8.3, of 32
-// 9.4; 128: 19.8, split by 64 25.6; 192: 26.8, 25.9; 256: 34.0, 26.8, by 128 33.8; 512: 50, 37.0,
-// tiles of 64 46.4, of 128 74.1.
+// from memory (600 MB of them in turn), gate and up of 12,288 x 4,096: 32 tokens in rows
+// of 32 14.2, split by 128 16.3; 64: 17.0, 17.5; 96: 22.0, 30.4, tiles of 64 22.6; 128:
+// 26.5, 32.6, 23.3; 256: 45, 48, tiles of 128 37.2; 512: tiles of 64 61.9, of 128 61.7;
+// 1,024: 115, 102.  4,096 x 12,288 with a residual: 32 tokens in rows of 16 x 32 10.3, of
+// 32 12.3; 64: 11.9, split by 128 32.5; 128: 18.5, split by 64 25.0, by 128 31.8; 192: 25.2,
+// 25.4, 32.1; 256: 30.1, 25.6, 32.1; 384: 42, 47, 32.6; 512: split by 64 49, by 128 35.6,
+// tiles of 64 52, of 128 75.
 Shape pick_shape(const EpilogueArgs& a, int cus) {
   static constexpr double kStart[2][7] = {{3.3, 3.6, 3.3, 3, 2, 4, 2}, {3.3, 3.6, 5, 0, 2, 4, 2}};
   static constexpr double kEach[2][7] = {{0.2, 0.4, 0.1, 4, 6.5, 5.5, 9}, {0.2, 0.4, 0.6, 0, 6.5, 5.5, 9}};
@@ -688,13 +691,14 @@ Shape pick_shape(const EpilogueArgs& a, int cus) {
   return (Shape)best;
 }
 
-// More waves for a workgroup where workgroups are few: 16 rows from three steps of
-// four waves on eight (4,096 x 4,096, one token: 3.7 us, four 3.9), from three of
-// eight on sixteen (4,096 x 12,288: four 8.7, eight 6.4, sixteen 5.7; gate and up of
-// 1,024 x 1,024: 3.5, 3.7, 4.4); 32 rows (4,096 x 12,288, 64 tokens: 12.0, eight 10.3;
-// 6,144 x 1,024: 4.8, 6.2; where a CU gets two, gate and up of 12,288 x 4,096, 12.2 and
-// 15.3); ROWS as measured there (4,096 x 12,288: 8.1, eight 6.2; with
-// two workgroups per CU 8.5, 8.9).
+// More waves for a workgroup where workgroups are few, weights from memory: 16 rows
+// from three steps of four waves on eight (4,096 x 4,096, one token: 3.8 us, four 4.6),
+// from three of eight on sixteen (4,096 x 12,288: four 10.9, eight 7.3, sixteen 5.9, and
+// for 16 tokens 10.9, 7.6, 8.3; gate and up of 1,024 x 1,024: 3.3, 3.2, 3.4; where a CU
+// gets three, gate and up of 12,288 x 4,096, 8.5, 8.9, 12.3); 32 rows (4,096 x 12,288, 64
+// tokens: 13.4, eight 11.7; 6,144 x 1,024: 4.5, 4.6; where a CU gets three, gate and up of
+// 12,288 x 4,096, 17.5 and 21.5); ROWS as measured there (4,096 x 12,288 in the
+// last-level cache: 8.1, eight 6.2; with two workgroups per CU 8.5, 8.9).
 template <int MATS, int ACT>
 hipError_t launch_act(const EpilogueArgs& a, int cus, hipStream_t s) {
   const Shape shape = pick_shape(a, cus);
