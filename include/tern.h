@@ -676,7 +676,8 @@ typedef struct {
 } tern_kv_pool;
 
 /* Bytes of the workspace (device, 256-byte aligned) of tern_kv_reserve and
- * tern_kv_compact; it carries nothing from call to call.  0 on bad arguments. */
+ * tern_kv_compact; it carries nothing from call to call, and calls that may overlap
+ * (on different pools) need one each.  0 on bad arguments. */
 int64_t tern_kv_pool_workspace_bytes(const tern_kv_pool* pool);
 
 /*
