@@ -648,8 +648,8 @@ int tern_qk_norm_rope(const tern_kv_batch* batch, int64_t head_dim, const float*
  * number of entries that hold page p (0: free); the calls below keep it, and a
  * fresh pool is refs of zeros.  A page may be held by several rows (a prompt that
  * several answers share); nothing writes into a page that others hold, if
- * tern_kv_reserve precedes every tern_kv_append and that takes nothing of a row
- * that was refused.  Per step, now, kept and the rest device arrays:
+ * tern_kv_reserve precedes every tern_kv_append and rows that it refused take no
+ * part in that.  Per step (len, want, granted, now and kept are device arrays):
  *     want = len + new tokens;  tern_kv_reserve(len, want);  tern_kv_copy of what
  *     it lists, in every layer;  now = granted ? want : 0;  rotation, append and
  *     attention with length now;  after verification tern_kv_truncate(now, kept);
